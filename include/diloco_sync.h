@@ -413,6 +413,157 @@ int dl_selftest_wait_timeout(void* d_workspace, int32_t polls, void* stream);
 int dl_selftest_pipeline(void* d_workspace, const float* d_src, int32_t n_tiles,
                          int32_t stall_tile, int32_t polls, float* d_out, void* stream);
 
+/* ------------------------------------------------------------------------
+ * A learner's inner step. Between two outer steps every learner k runs many
+ * inner steps on its replica theta_k: the layers' norms forward and backward,
+ * the clip by the global gradient norm, and AdamW over all tensors
+ * (INTELLECT-1 notes, section 2.2: the inner optimiser is AdamW). These calls
+ * work on the same flat fragment buffers that dl_pseudograd_stats reads
+ * afterwards. The conventions at the top of this file hold; bf16 and e4m3
+ * buffers are 16-byte aligned like fp32 ones unless a call says otherwise.
+ * ------------------------------------------------------------------------ */
+
+/* Element types. */
+#define DL_F32 0
+#define DL_BF16 1
+#define DL_F16 2
+#define DL_E4M3 3 /* 8-bit floats: 4 exponent and 3 mantissa bits, no infinities */
+
+#define DL_ADAMW_BLOCK 128 /* elements that share a scale of the 8-bit states */
+
+/* Workspace bytes needed by dl_grad_norm. Zero the workspace once when it is
+ * allocated; a call leaves it as it found it. */
+size_t dl_grad_norm_workspace_bytes(void);
+
+/*
+ * Global gradient norm and clip coefficient over any number of buffers:
+ *   norm = sqrt(sum of g^2 over every element of every buffer)
+ *   coef = 1 when norm <= max_norm, max_norm / norm when it is larger, and
+ *          NaN when a gradient is Inf or NaN (dl_adamw_step then leaves
+ *          its state untouched)
+ * Squares are summed in groups in fp32 and the groups in fp64, in a fixed
+ * order (repeated calls give the same bits on one GPU model); groups whose
+ * squares leave the fp32 range are summed in fp64 throughout.
+ *   grads      host [n_grads] of device buffers of grad_type, aligned to
+ *              their element size; NULL where numel is 0
+ *   numel      host [n_grads], each >= 0
+ *   grad_type  DL_F32 or DL_BF16
+ *   max_norm   > 0; infinity for no clipping
+ *   d_out      device [2] fp32, out: norm, coef
+ *   d_workspace device scratch of dl_grad_norm_workspace_bytes() bytes
+ * With no buffers or no elements the norm is 0 and coef 1.
+ */
+int dl_grad_norm(const void* const* grads, const int64_t* numel, int32_t n_grads,
+                 int32_t grad_type, double max_norm, float* d_out, void* d_workspace,
+                 size_t workspace_bytes, void* stream);
+
+/* One fragment's buffers of an AdamW step. */
+typedef struct dl_adamw_job {
+    const dl_fragment* frag; /* tensor layout of the fragment */
+    float* theta;            /* device [n] fp32 parameters, in/out */
+    const void* grad;        /* device [n] of grad_type */
+    void* m;                 /* device [n] of state_type: first moment, in/out */
+    void* v;                 /* device [n] of state_type: second moment (8 bits: its root), in/out */
+    float* m_scale;          /* device [slots] fp32, in/out; 8-bit states only, else NULL */
+    float* v_scale;          /* device [slots] fp32, in/out; 8-bit states only, else NULL */
+    void* theta_bf16;        /* device [n] bf16, out: rounded copy of theta; may be NULL */
+    const float* d_decay;    /* device [T] fp32 factors on weight_decay; NULL for all 1 */
+} dl_adamw_job;
+
+typedef struct dl_adamw_config {
+    double lr;           /* >= 0 */
+    double beta1, beta2; /* in [0, 1) */
+    double eps;          /* >= FLT_MIN */
+    double weight_decay; /* >= 0 */
+    int64_t step;        /* this step's number, from 1: the bias corrections' exponent */
+    uint64_t seed;       /* of the 8-bit states' rounding */
+} dl_adamw_config;
+
+/* Scale slots of a fragment's 8-bit states: n / 128 + T (integer division);
+ * a negative DL_ERR_* code for a bad fragment. */
+int64_t dl_adamw_scale_slots(const dl_fragment* frag);
+
+/*
+ * One AdamW step over every tensor of every job, in place, in one launch per
+ * 32 jobs. With g = coef * grad (coef = d_clip[1], or 1) and t = step:
+ *   m' = beta1 m + (1 - beta1) g          v' = beta2 v + (1 - beta2) g^2
+ *   theta' = theta (1 - lr weight_decay decay_t)
+ *            - lr / (1 - beta1^t) * m' / (sqrt(v') / sqrt(1 - beta2^t) + eps)
+ * A NaN or infinite coef skips the step: nothing is written.
+ *
+ * State in 32 bits (state_type DL_F32): m and v are fp32.
+ *
+ * State in 8 bits (DL_E4M3): m and the root s = sqrt(v) are e4m3 codes, each
+ * value being code * scale. A tensor's elements form blocks of 128 from its
+ * start, the last one shorter, so no block holds elements of two tensors.
+ * Block b of tensor t has scale slot offsets[t] / 128 + t + b; slots without
+ * a block are never written. Zeroed buffers are the start of training.
+ *   scale = 2^(k-7) with 2^k <= largest |value| of the block < 2^(k+1),
+ *           k >= -53; NaN when that value is Inf or NaN
+ *   code  = |value| / scale rounded stochastically: in units of the code's
+ *           last place, plus r / 2^16, rounded down; a positive s keeps at
+ *           least the smallest code, so that a moment never meets a zero root
+ * r: with P the slot (counted over all jobs: job j's slots follow those of
+ * the jobs before it), i = element - block start and z = mix(mix(seed +
+ * step * G) + (P * 32 + i / 4) * G), mix and G being SplitMix64's output
+ * function and increment (Steele, Lea, Flood 2014), 64-bit wrapping: m takes
+ * the low word of z and s the high word; of that word i % 4 = 0 and 2 take
+ * the low and the high half, 1 and 3 the same halves in reverse bit order.
+ * m' and v' are formed in fp32, each operation rounded once, in the order
+ * written above ((1 - beta2) multiplies g * g).
+ *   grad_type  DL_F32 or DL_BF16, of every job
+ *   cfg        host, read during the call
+ *   d_clip     device [2] fp32 as written by dl_grad_norm, or NULL
+ */
+int dl_adamw_step(const dl_adamw_job* jobs, int32_t n_jobs, int32_t grad_type, int32_t state_type,
+                  const dl_adamw_config* cfg, const float* d_clip, void* stream);
+
+#define DL_NORM_RMS 1        /* no mean: xhat = x * rstd, rstd = 1 / sqrt(mean(x^2) + eps) */
+#define DL_NORM_ACCUMULATE 2 /* backward adds to dweight and dbias instead of writing them */
+
+/*
+ * Layer norm forward, row by row over `width` columns:
+ *   mean = sum(x) / width, rstd = 1 / sqrt(sum((x - mean)^2) / width + eps)
+ *   y = (x - mean) * rstd * weight + bias
+ * in fp32, y rounded once to x_type. DL_NORM_RMS leaves the mean out.
+ *   x, y         device [rows][width] of x_type (DL_F32, DL_BF16 or DL_F16);
+ *                row r starts at r * stride elements, stride >= width
+ *   weight, bias device [width] of param_type (DL_F32 or DL_BF16); bias may be NULL
+ *   mean, rstd   device [rows] fp32, out; mean is ignored with DL_NORM_RMS
+ * Pointers need the alignment of their elements only (weights may lie
+ * anywhere in a fragment's flat buffer); 16-byte aligned rows are faster.
+ * y may be x itself (same stride). rows = 0 is a no-op; width >= 1.
+ */
+int dl_layernorm_forward(const void* x, int64_t x_stride, int32_t x_type, int64_t rows,
+                         int32_t width, const void* weight, const void* bias, int32_t param_type,
+                         double eps, int32_t flags, void* y, int64_t y_stride, float* mean,
+                         float* rstd, void* stream);
+
+/* Workspace bytes needed by dl_layernorm_backward for these sizes. */
+size_t dl_layernorm_workspace_bytes(int64_t rows, int32_t width);
+
+/*
+ * Layer norm backward. With xhat = (x - mean) * rstd and w = weight * dy:
+ *   dx      = rstd * (w - sum(w) / width - xhat * sum(w * xhat) / width)
+ *   dweight = sum over rows of dy * xhat      dbias = sum over rows of dy
+ * in fp32 (DL_NORM_RMS: xhat = x * rstd, no sum(w) term), in a fixed order
+ * of summation; dx is rounded once to x_type, the parameters' gradients once
+ * to param_type (with DL_NORM_ACCUMULATE after adding what they held).
+ *   dy, x, dx    device [rows][width] of x_type with their own strides;
+ *                dx may be dy itself (same stride)
+ *   mean, rstd   device [rows] fp32, as the forward call wrote them (mean is
+ *                ignored with DL_NORM_RMS)
+ *   dweight      device [width] of param_type, in/out
+ *   dbias        the same, or NULL where there is no bias
+ *   d_workspace  device scratch of dl_layernorm_workspace_bytes(rows, width) bytes
+ * rows = 0 writes zero gradients (accumulating: leaves them).
+ */
+int dl_layernorm_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                          int32_t x_type, int64_t rows, int32_t width, const void* weight,
+                          int32_t param_type, const float* mean, const float* rstd, int32_t flags,
+                          void* dx, int64_t dx_stride, void* dweight, void* dbias,
+                          void* d_workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

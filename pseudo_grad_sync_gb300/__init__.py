@@ -15,9 +15,17 @@ C entry points (see include/diloco_sync.h) keep their names here:
     outer_sync           the three calls over every fragment of a model, with
                          consecutive fragments overlapped on two streams
 
+A learner's inner step (``inner``, imported here):
+
+    grad_norm            global gradient norm and clip coefficient
+    adamw_step           AdamW over every tensor of a list of fragments
+    layernorm_forward    layer norm of rows
+    layernorm_backward   its gradients
+
 ``OuterSync`` bundles the three device calls of one fragment with their
 workspaces; ``ModelSync`` holds the workspace of ``outer_sync`` for a fixed
-list of fragments.
+list of fragments. ``InnerAdamW`` bundles a learner's clip and AdamW step with their
+states; ``layer_norm`` is the norm as a torch.autograd operation.
 """
 from __future__ import annotations
 
@@ -107,6 +115,7 @@ def lib():
         L.dl_selftest_pipeline.argtypes = [vp, vp, i32, i32, i32, vp, vp]
         L.dl_read_device_status.restype = ctypes.c_int
         L.dl_read_device_status.argtypes = [vp, vp, vp]
+        inner.declare(L)
         _lib = L
     return _lib
 
@@ -561,3 +570,10 @@ class ModelSync:
             flags |= self.mode
         outer_sync(self.frags, theta_g, momentum, replicas, self.K, self.workspace, weights,
                    present, min_quorum, self.clip, self.lr, self.mu, flags, delta_bar, stream)
+
+
+from . import inner  # noqa: E402  (it takes this module's helpers)
+from .inner import (  # noqa: E402,F401
+    DL_ADAMW_BLOCK, DL_BF16, DL_E4M3, DL_F16, DL_F32, DL_NORM_ACCUMULATE, DL_NORM_RMS, AdamWJobs,
+    GradList, InnerAdamW, adamw_scale_slots, adamw_step, grad_norm, grad_norm_workspace_bytes,
+    layer_norm, layernorm_backward, layernorm_forward, layernorm_workspace_bytes)

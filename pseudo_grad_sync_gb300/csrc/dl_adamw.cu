@@ -1,0 +1,476 @@
+// A learner's inner optimiser step: the global gradient norm with its clip
+// coefficient, and AdamW over every tensor of a list of fragments with
+// states in 32 or in 8 bits.
+#include <float.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "dl_types.cuh"
+
+namespace dl {
+namespace {
+
+// ---------------------------------------------------------------------------
+// gradient norm
+
+constexpr int kNormBuffers = 64;  // per launch; longer lists take several
+constexpr int kNormBlocks = 2048;
+constexpr int kNormVecs = 8;      // 16-byte loads of a thread in flight
+constexpr int kNormChunk = kThreads * kNormVecs;  // 16-byte vectors per chunk
+
+struct NormWorkspace {  // after the header; zeroed once, left as found
+    double total;       // sum over the launches of one call so far
+    uint32_t done;      // blocks of this launch that have finished
+    double partial[kNormBlocks];
+};
+
+struct NormArgs {
+    const void* g[kNormBuffers];
+    int64_t numel[kNormBuffers];
+    int64_t chunk_end[kNormBuffers];  // running number of chunks
+    int n;
+    int last;  // the call's last launch
+    double max_norm;
+    float* out;
+    NormWorkspace* ws;
+};
+
+__device__ __forceinline__ void unpack(const uint4& q, float (&v)[4], float) {
+    v[0] = __uint_as_float(q.x), v[1] = __uint_as_float(q.y);
+    v[2] = __uint_as_float(q.z), v[3] = __uint_as_float(q.w);
+}
+__device__ __forceinline__ void unpack(const uint4& q, float (&v)[8], __nv_bfloat16) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+// Elements before the first 16-byte boundary of a buffer.
+template <typename T>
+__host__ __device__ inline int64_t head_of(const void* p, int64_t n) {
+    const int64_t h = static_cast<int64_t>((16 - (reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) /
+                      static_cast<int64_t>(sizeof(T));
+    return h < n ? h : n;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ NormArgs a) {
+    constexpr int W = 16 / sizeof(T);
+    __shared__ double red[kWarps];
+    __shared__ bool final_block;
+    double sum = 0.0;
+    int j = 0;
+    const int64_t chunks = a.chunk_end[a.n - 1];
+    for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+        while (c >= a.chunk_end[j]) ++j;
+        const int64_t first = c - (j ? a.chunk_end[j - 1] : 0);
+        const T* g = static_cast<const T*>(a.g[j]);
+        const int64_t n = a.numel[j], head = head_of<T>(g, n);
+        const int64_t vecs = (n - head) / W;
+        const uint4* body = reinterpret_cast<const uint4*>(g + head);
+        for (int u = 0; u < kNormVecs; ++u) {
+            const int64_t i = first * kNormChunk + u * kThreads + threadIdx.x;
+            if (i < vecs) {
+                float v[W];
+                unpack(__ldg(body + i), v, T());
+#pragma unroll
+                for (int w = 0; w < W; ++w) sum = fma((double)v[w], (double)v[w], sum);
+            }
+        }
+        if (first == 0) {
+            const int64_t rest = n - vecs * W;  // the head's and the tail's elements
+            if (threadIdx.x < rest) {
+                const int64_t i = threadIdx.x < head ? threadIdx.x : threadIdx.x + vecs * W;
+                const double v = to_f32(g[i]);
+                sum = fma(v, v, sum);
+            }
+        }
+    }
+    for (int sh = 16; sh; sh >>= 1) sum += __shfl_xor_sync(kFull, sum, sh);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0) red[warp] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double s = 0.0;
+        for (int w = 0; w < kWarps; ++w) s += red[w];
+        a.ws->partial[blockIdx.x] = s;
+        __threadfence();
+        final_block = atomicAdd(&a.ws->done, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!final_block) return;
+    __threadfence();
+    double s = 0.0;
+    for (int b = threadIdx.x; b < static_cast<int>(gridDim.x); b += kThreads)
+        s += __ldcg(&a.ws->partial[b]);
+    for (int sh = 16; sh; sh >>= 1) s += __shfl_xor_sync(kFull, s, sh);
+    if (lane == 0) red[warp] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double t = a.ws->total;
+        for (int w = 0; w < kWarps; ++w) t += red[w];
+        a.ws->done = 0;
+        a.ws->total = a.last ? 0.0 : t;
+        if (a.last) {
+            const double norm = sqrt(t);
+            a.out[0] = static_cast<float>(norm);
+            a.out[1] = !isfinite(norm) ? __int_as_float(0x7fc00000)
+                       : norm > a.max_norm ? static_cast<float>(a.max_norm / norm)
+                                           : 1.0f;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// AdamW
+
+constexpr int kAdamJobs = 32;  // per launch; longer lists take several
+constexpr int kBlock = DL_ADAMW_BLOCK;
+
+struct AdamJob {
+    float* theta;
+    const void* grad;
+    void* m;
+    void* v;
+    float* m_scale;
+    float* v_scale;
+    __nv_bfloat16* copy;
+    const float* decay;
+    const int64_t* off;
+    int64_t n;
+    int64_t slot0;     // slots of all jobs before this one
+    int64_t work_end;  // running number of blocks' tiles
+    int T;
+};
+
+struct AdamArgs {
+    AdamJob job[kAdamJobs];
+    int n;
+    float lr_wd, step_size, beta1, om_beta1, beta2, om_beta2, inv_root_bc2, eps;
+    uint64_t key;
+    const float* clip;
+};
+
+struct Hyper {
+    float coef, keep;
+};
+
+// theta' from the new moments; root = sqrt(v')
+__device__ __forceinline__ float step_theta(const AdamArgs& a, float theta, float m, float root,
+                                            float keep) {
+    const float denom = fmaf(root, a.inv_root_bc2, a.eps);
+    return fmaf(-a.step_size, m / denom, theta * keep);
+}
+
+__device__ __forceinline__ float clip_coef(const AdamArgs& a) { return a.clip ? __ldg(a.clip + 1) : 1.0f; }
+
+__device__ __forceinline__ float keep_of(const AdamArgs& a, const AdamJob& J, int t) {
+    return J.decay ? 1.0f - a.lr_wd * __ldg(J.decay + t) : 1.0f - a.lr_wd;
+}
+
+constexpr int kTile32 = 2048;
+
+template <typename G>
+__global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ AdamArgs a) {
+    const float coef = clip_coef(a);
+    if (!isfinite(coef)) return;
+    int j = 0;
+    while (static_cast<int64_t>(blockIdx.x) >= a.job[j].work_end) ++j;
+    const AdamJob& J = a.job[j];
+    const int64_t base = (blockIdx.x - (j ? a.job[j - 1].work_end : 0)) * int64_t(kTile32);
+    const G* g = static_cast<const G*>(J.grad);
+    float* m = static_cast<float*>(J.m);
+    float* v = static_cast<float*>(J.v);
+    for (int64_t i = base + threadIdx.x; i < base + kTile32 && i < J.n; i += kThreads) {
+        const float keep = keep_of(a, J, J.decay ? tensor_containing(J.off, J.T, i) : 0);
+        const float gi = to_f32(g[i]) * coef;
+        const float mi = fmaf(a.beta1, m[i], a.om_beta1 * gi);
+        const float vi = fmaf(a.beta2, v[i], a.om_beta2 * (gi * gi));
+        const float th = step_theta(a, J.theta[i], mi, sqrtf(vi), keep);
+        m[i] = mi;
+        v[i] = vi;
+        J.theta[i] = th;
+        if (J.copy) J.copy[i] = __float2bfloat16_rn(th);
+    }
+}
+
+__host__ __device__ inline uint64_t mix64(uint64_t z) {
+    z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+    z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+    return z ^ (z >> 31);
+}
+constexpr uint64_t kGolden = 0x9E3779B97F4A7C15ull;
+
+// Smallest exponent field of a block's largest value: k = -53
+constexpr uint32_t kMinExp = 127 - 53;
+
+// 2^(k-7) of a block whose largest magnitude has these bits
+__device__ __forceinline__ float block_scale(uint32_t top) {
+    const uint32_t e = max(top >> 23, kMinExp);
+    return e == 255 ? __int_as_float(0x7fc00000) : __uint_as_float((e - 7) << 23);
+}
+// its reciprocal (a power of two; any finite value for a NaN scale)
+__device__ __forceinline__ float block_inverse(uint32_t top) {
+    return __uint_as_float((261 - max(top >> 23, kMinExp)) << 23);
+}
+
+// four e4m3 codes, the first in the low byte, to fp32
+__device__ __forceinline__ void decode4(uint32_t c, float (&x)[4]) {
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(c));
+    const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    x[0] = p.x, x[1] = p.y, x[2] = q.x, x[3] = q.y;
+}
+
+// Four values to codes with stochastic rounding by the hardware conversion:
+// of the 32 random bits, values 0 and 2 use the low and the high half, 1 and
+// 3 the same halves in reverse bit order; the first operand is the top byte.
+__device__ __forceinline__ uint32_t encode4(const float (&x)[4], uint32_t bits) {
+    uint32_t c;
+    asm("cvt.rs.satfinite.e4m3x4.f32 %0, {%1, %2, %3, %4}, %5;"
+        : "=r"(c)
+        : "f"(x[3]), "f"(x[2]), "f"(x[1]), "f"(x[0]), "r"(bits));
+    return c;
+}
+
+constexpr int kSlotsPerTile = 64;
+
+// first tensor t with off[t+1] / 128 + t + 1 > slot
+__device__ __forceinline__ int tensor_of_slot(const int64_t* off, int T, int64_t slot) {
+    int lo = 0, hi = T - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(off + mid + 1) / kBlock + mid + 1 > slot)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    return lo;
+}
+
+template <typename G>
+__global__ void __launch_bounds__(kThreads) k_adamw8(const __grid_constant__ AdamArgs a) {
+    const float coef = clip_coef(a);
+    if (!isfinite(coef)) return;
+    int j = 0;
+    while (static_cast<int64_t>(blockIdx.x) >= a.job[j].work_end) ++j;
+    const AdamJob& J = a.job[j];
+    const int64_t tile = (blockIdx.x - (j ? a.job[j - 1].work_end : 0)) * int64_t(kSlotsPerTile);
+    const int64_t slots = J.n / kBlock + J.T;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const G* g = static_cast<const G*>(J.grad);
+    uint8_t* m8 = static_cast<uint8_t*>(J.m);
+    uint8_t* s8 = static_cast<uint8_t*>(J.v);
+    for (int64_t s = tile + warp; s < tile + kSlotsPerTile && s < slots; s += kWarps) {
+        const int t = tensor_of_slot(J.off, J.T, s);
+        const int64_t o0 = __ldg(J.off + t), o1 = __ldg(J.off + t + 1);
+        const int64_t begin = o0 + (s - (o0 / kBlock + t)) * kBlock;
+        if (begin >= o1) continue;  // a slot without a block
+        const float keep = keep_of(a, J, t);
+        const int64_t i0 = begin + 4 * lane;
+        const int cnt = i0 >= o1 ? 0 : o1 - i0 < 4 ? static_cast<int>(o1 - i0) : 4;
+        uint32_t cm = 0, cs = 0;
+        float th[4], gr[4], m[4], r[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            th[e] = gr[e] = 0.f;
+            if (e < cnt) {
+                th[e] = J.theta[i0 + e];
+                gr[e] = to_f32(g[i0 + e]);
+                cm |= uint32_t(m8[i0 + e]) << (8 * e);
+                cs |= uint32_t(s8[i0 + e]) << (8 * e);
+            }
+        }
+        decode4(cm, m);
+        decode4(cs, r);
+        const float msc = J.m_scale[s], ssc = J.v_scale[s];
+        uint32_t mtop = 0, stop = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float gi = __fmul_rn(gr[e], coef);
+            m[e] = __fadd_rn(__fmul_rn(__fmul_rn(m[e], msc), a.beta1), __fmul_rn(gi, a.om_beta1));
+            const float old = __fmul_rn(r[e], ssc);
+            const float v = __fadd_rn(__fmul_rn(__fmul_rn(old, old), a.beta2),
+                                      __fmul_rn(__fmul_rn(gi, gi), a.om_beta2));
+            r[e] = __fsqrt_rn(v);
+            th[e] = step_theta(a, th[e], m[e], r[e], keep);
+            mtop = max(mtop, __float_as_uint(fabsf(m[e])));
+            stop = max(stop, __float_as_uint(r[e]) & 0x7fffffffu);
+        }
+        mtop = __reduce_max_sync(kFull, mtop);
+        stop = __reduce_max_sync(kFull, stop);
+        const float minv = block_inverse(mtop), sinv = block_inverse(stop);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            m[e] *= minv;
+            const float x = r[e] * sinv;
+            r[e] = r[e] > 0.f ? fmaxf(x, 0x1p-9f) : x;
+        }
+        const uint64_t z = mix64(a.key + ((J.slot0 + s) * (kBlock / 4) + lane) * kGolden);
+        cm = encode4(m, static_cast<uint32_t>(z));
+        cs = encode4(r, static_cast<uint32_t>(z >> 32));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (e < cnt) {
+                J.theta[i0 + e] = th[e];
+                m8[i0 + e] = static_cast<uint8_t>(cm >> (8 * e));
+                s8[i0 + e] = static_cast<uint8_t>(cs >> (8 * e));
+                if (J.copy) J.copy[i0 + e] = __float2bfloat16_rn(th[e]);
+            }
+        }
+        if (lane == 0) {
+            J.m_scale[s] = block_scale(mtop);
+            J.v_scale[s] = block_scale(stop);
+        }
+    }
+}
+
+bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+}  // namespace
+}  // namespace dl
+
+using namespace dl;
+
+extern "C" size_t dl_grad_norm_workspace_bytes(void) {
+    return align256(kWsHeader + sizeof(NormWorkspace));
+}
+
+extern "C" int dl_grad_norm(const void* const* grads, const int64_t* numel, int32_t n_grads,
+                            int32_t grad_type, double max_norm, float* d_out, void* d_workspace,
+                            size_t workspace_bytes, void* stream) {
+    if (n_grads < 0 || (n_grads > 0 && (!grads || !numel)) || !d_out || !(max_norm > 0.0) ||
+        (grad_type != DL_F32 && grad_type != DL_BF16))
+        return DL_ERR_ARG;
+    for (int32_t i = 0; i < n_grads; ++i) {
+        if (numel[i] < 0 || (numel[i] > 0 && !grads[i])) return DL_ERR_ARG;
+        if (numel[i] > 0 && !aligned_to(grads[i], type_size(grad_type))) return DL_ERR_ALIGN;
+    }
+    if (!aligned_to(d_out, 4)) return DL_ERR_ALIGN;
+    if (!d_workspace || workspace_bytes < dl_grad_norm_workspace_bytes()) return DL_ERR_WORKSPACE;
+    if (!aligned_to(d_workspace, 256)) return DL_ERR_ALIGN;
+    const void* kernel = grad_type == DL_F32 ? reinterpret_cast<const void*>(k_grad_norm<float>)
+                                             : reinterpret_cast<const void*>(k_grad_norm<__nv_bfloat16>);
+    NormArgs a;
+    a.max_norm = max_norm;
+    a.out = d_out;
+    a.ws = reinterpret_cast<NormWorkspace*>(static_cast<char*>(d_workspace) + kWsHeader);
+    int32_t i = 0;
+    do {
+        a.n = 0;
+        int64_t chunks = 0;
+        for (; i < n_grads && a.n < kNormBuffers; ++i) {
+            if (numel[i] == 0) continue;
+            const int64_t head = grad_type == DL_F32 ? head_of<float>(grads[i], numel[i])
+                                                     : head_of<__nv_bfloat16>(grads[i], numel[i]);
+            const int64_t vecs = (numel[i] - head) * static_cast<int64_t>(type_size(grad_type)) / 16;
+            chunks += vecs ? (vecs + kNormChunk - 1) / kNormChunk : 1;
+            a.g[a.n] = grads[i];
+            a.numel[a.n] = numel[i];
+            a.chunk_end[a.n++] = chunks;
+        }
+        a.last = i == n_grads;
+        if (a.n == 0) {  // nothing left to read: one block writes the result
+            a.g[0] = nullptr;
+            a.numel[0] = 0;
+            a.chunk_end[0] = 0;
+            a.n = 1;
+        }
+        int grid = grid_for(kernel, kThreads, 0, chunks ? chunks : 1);
+        if (grid > kNormBlocks) grid = kNormBlocks;
+        void* args[] = {&a};
+        if (cudaLaunchKernel(kernel, dim3(grid), dim3(kThreads), args, 0,
+                             static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+            cudaGetLastError();  // reported here, not by a later call
+            return DL_ERR_CUDA;
+        }
+    } while (i < n_grads);
+    return DL_OK;
+}
+
+extern "C" int64_t dl_adamw_scale_slots(const dl_fragment* frag) {
+    HostFrag f;
+    const int st = check_fragment(frag, &f);
+    return st != DL_OK ? st : f.n / kBlock + f.T;
+}
+
+extern "C" int dl_adamw_step(const dl_adamw_job* jobs, int32_t n_jobs, int32_t grad_type,
+                             int32_t state_type, const dl_adamw_config* cfg, const float* d_clip,
+                             void* stream) {
+    if (n_jobs < 0 || (n_jobs > 0 && !jobs) || !cfg || (grad_type != DL_F32 && grad_type != DL_BF16) ||
+        (state_type != DL_F32 && state_type != DL_E4M3))
+        return DL_ERR_ARG;
+    if (!(cfg->lr >= 0.0 && cfg->lr <= FLT_MAX) || !(cfg->beta1 >= 0.0 && cfg->beta1 < 1.0) ||
+        !(cfg->beta2 >= 0.0 && cfg->beta2 < 1.0) || !(cfg->eps >= FLT_MIN && cfg->eps <= FLT_MAX) ||
+        !(cfg->weight_decay >= 0.0 && cfg->weight_decay <= FLT_MAX) || cfg->step < 1)
+        return DL_ERR_ARG;
+    if (!aligned_to(d_clip, 4)) return DL_ERR_ALIGN;
+    const bool by8 = state_type == DL_E4M3;
+    for (int32_t i = 0; i < n_jobs; ++i) {
+        const dl_adamw_job& q = jobs[i];
+        HostFrag f;
+        const int st = check_fragment(q.frag, &f);
+        if (st != DL_OK) return st;
+        if (f.n == 0) continue;
+        if (!q.theta || !q.grad || !q.m || !q.v || (by8 && (!q.m_scale || !q.v_scale)))
+            return DL_ERR_ARG;
+        for (const void* p : {static_cast<const void*>(q.theta), q.grad, static_cast<const void*>(q.m),
+                              static_cast<const void*>(q.v), static_cast<const void*>(q.theta_bf16)})
+            if (!aligned16(p)) return DL_ERR_ALIGN;
+        if (!aligned_to(q.m_scale, 4) || !aligned_to(q.v_scale, 4) || !aligned_to(q.d_decay, 4))
+            return DL_ERR_ALIGN;
+    }
+    AdamArgs a;
+    const double t = static_cast<double>(cfg->step);
+    const double bc1 = 1.0 - pow(cfg->beta1, t), bc2 = 1.0 - pow(cfg->beta2, t);
+    a.lr_wd = static_cast<float>(cfg->lr * cfg->weight_decay);
+    a.step_size = static_cast<float>(cfg->lr / bc1);
+    a.beta1 = static_cast<float>(cfg->beta1);
+    a.om_beta1 = static_cast<float>(1.0 - cfg->beta1);
+    a.beta2 = static_cast<float>(cfg->beta2);
+    a.om_beta2 = static_cast<float>(1.0 - cfg->beta2);
+    a.inv_root_bc2 = static_cast<float>(1.0 / sqrt(bc2));
+    a.eps = static_cast<float>(cfg->eps);
+    a.key = mix64(cfg->seed + static_cast<uint64_t>(cfg->step) * kGolden);
+    a.clip = d_clip;
+    int64_t slot0 = 0;
+    int32_t i = 0;
+    while (i < n_jobs) {
+        a.n = 0;
+        int64_t work = 0;
+        for (; i < n_jobs && a.n < kAdamJobs; ++i) {
+            const dl_adamw_job& q = jobs[i];
+            HostFrag f;
+            check_fragment(q.frag, &f);
+            const int64_t slots = f.n / kBlock + f.T;
+            if (f.n > 0) {
+                work += by8 ? (slots + kSlotsPerTile - 1) / kSlotsPerTile : (f.n + kTile32 - 1) / kTile32;
+                a.job[a.n++] = AdamJob{q.theta, q.grad, q.m, q.v, q.m_scale, q.v_scale,
+                                       static_cast<__nv_bfloat16*>(q.theta_bf16), q.d_decay,
+                                       f.d_offsets, f.n, slot0, work, f.T};
+            }
+            slot0 += slots;
+        }
+        if (a.n == 0) continue;
+        if (work > INT32_MAX) return DL_ERR_ARG;
+        const void* kernel =
+            by8 ? (grad_type == DL_F32 ? reinterpret_cast<const void*>(k_adamw8<float>)
+                                       : reinterpret_cast<const void*>(k_adamw8<__nv_bfloat16>))
+                : (grad_type == DL_F32 ? reinterpret_cast<const void*>(k_adamw<float>)
+                                       : reinterpret_cast<const void*>(k_adamw<__nv_bfloat16>));
+        void* args[] = {&a};
+        if (cudaLaunchKernel(kernel, dim3(static_cast<unsigned>(work)), dim3(kThreads), args, 0,
+                             static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+            cudaGetLastError();
+            return DL_ERR_CUDA;
+        }
+    }
+    return DL_OK;
+}

@@ -1,0 +1,379 @@
+"""A learner's inner step: layer norms, gradient clipping and AdamW.
+
+Argument marshalling of the inner-step entry points of libdiloco_sync.so under
+their C names (imported into the package):
+
+    grad_norm            global gradient norm and clip coefficient
+    adamw_step           AdamW over every tensor of a list of fragments, with
+                         states in 32 or in 8 bits
+    layernorm_forward    layer norm (or RMS norm) of rows
+    layernorm_backward   its input's and its parameters' gradients
+
+``GradList`` and ``AdamWJobs`` check and marshal a list of buffers once, for a
+program that steps the same buffers again and again. ``InnerAdamW`` bundles
+the clip and the step with their states; ``layer_norm`` is the norm as a
+torch.autograd operation.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import (Fragment, _check, _cuda, _Fragment, _need, _need_all, _ptr, _stream, _F32, _U8, lib,
+               new_workspace)
+
+DL_F32, DL_BF16, DL_F16, DL_E4M3 = 0, 1, 2, 3
+DL_NORM_RMS = 1
+DL_NORM_ACCUMULATE = 2
+DL_ADAMW_BLOCK = 128
+
+_TYPE = {torch.float32: DL_F32, torch.bfloat16: DL_BF16, torch.float16: DL_F16}
+_GRADS = (torch.float32, torch.bfloat16)
+_PARAMS = (torch.float32, torch.bfloat16)
+
+
+class _AdamWJob(ctypes.Structure):
+    _fields_ = [("frag", ctypes.POINTER(_Fragment))] + [
+        (name, ctypes.c_void_p)
+        for name in ("theta", "grad", "m", "v", "m_scale", "v_scale", "theta_bf16", "d_decay")]
+
+
+class _AdamWConfig(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_double)
+                for name in ("lr", "beta1", "beta2", "eps", "weight_decay")] + [
+        ("step", ctypes.c_int64), ("seed", ctypes.c_uint64)]
+
+
+def declare(L):
+    """Argument and result types of the inner-step entry points."""
+    vp, i32, i64, f64, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_double,
+                             ctypes.c_size_t)
+    L.dl_grad_norm_workspace_bytes.restype = sz
+    L.dl_grad_norm_workspace_bytes.argtypes = []
+    L.dl_grad_norm.restype = ctypes.c_int
+    L.dl_grad_norm.argtypes = [vp, vp, i32, i32, f64, vp, vp, sz, vp]
+    L.dl_adamw_scale_slots.restype = i64
+    L.dl_adamw_scale_slots.argtypes = [ctypes.POINTER(_Fragment)]
+    L.dl_adamw_step.restype = ctypes.c_int
+    L.dl_adamw_step.argtypes = [ctypes.POINTER(_AdamWJob), i32, i32, i32,
+                                ctypes.POINTER(_AdamWConfig), vp, vp]
+    L.dl_layernorm_forward.restype = ctypes.c_int
+    L.dl_layernorm_forward.argtypes = [vp, i64, i32, i64, i32, vp, vp, i32, f64, i32, vp, i64, vp,
+                                       vp, vp]
+    L.dl_layernorm_workspace_bytes.restype = sz
+    L.dl_layernorm_workspace_bytes.argtypes = [i64, i32]
+    L.dl_layernorm_backward.restype = ctypes.c_int
+    L.dl_layernorm_backward.argtypes = [vp, i64, vp, i64, i32, i64, i32, vp, i32, vp, vp, i32, vp,
+                                        i64, vp, vp, vp, sz, vp]
+
+
+# ----------------------------------------------------------------------------
+# gradient norm
+
+
+def grad_norm_workspace_bytes() -> int:
+    return int(lib().dl_grad_norm_workspace_bytes())
+
+
+class GradList:
+    """Gradient buffers (contiguous, one element type), checked once."""
+
+    def __init__(self, grads):
+        self.grads = list(grads)
+        dtype = self.grads[0].dtype if self.grads else torch.float32
+        if dtype not in _GRADS:
+            raise TypeError(f"grads[0]: dtype {dtype}, expected float32 or bfloat16")
+        _need_all(self.grads, (dtype,), 0, "grads")
+        _cuda(self.grads)
+        n = len(self.grads)
+        self.type = _TYPE[dtype]
+        self._ptrs = (ctypes.c_void_p * max(n, 1))(*[g.data_ptr() for g in self.grads])
+        self._numel = (ctypes.c_int64 * max(n, 1))(*[g.numel() for g in self.grads])
+
+
+def grad_norm(grads, max_norm=math.inf, out=None, workspace=None, stream=None):
+    """Norm over all gradient buffers and the clip coefficient (dl_grad_norm).
+
+    grads: a list of device tensors, or a ``GradList``. Returns ``out``, a
+    device float32 tensor (norm, coefficient), the ``clip`` of adamw_step.
+    workspace: of grad_norm_workspace_bytes(), zeroed when allocated
+    (new_workspace); calls on different streams need their own."""
+    G = grads if isinstance(grads, GradList) else GradList(grads)
+    if out is None:
+        if not G.grads:
+            raise ValueError("grad_norm: an empty list needs an out tensor")
+        out = torch.empty(2, dtype=torch.float32, device=G.grads[0].device)
+    if workspace is None:
+        workspace = new_workspace(grad_norm_workspace_bytes(), out.device)
+    _need(out, _F32, 2, "out")
+    _need(workspace, _U8, 0, "workspace")
+    _cuda(out, workspace)
+    _check("dl_grad_norm", lib().dl_grad_norm(
+        G._ptrs, G._numel, len(G.grads), G.type, max_norm, out.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), _stream(stream)))
+    return out
+
+
+# ----------------------------------------------------------------------------
+# AdamW
+
+
+def adamw_scale_slots(frag: Fragment) -> int:
+    """Scale slots of a fragment's 8-bit states (dl_adamw_scale_slots)."""
+    return int(lib().dl_adamw_scale_slots(frag.c))
+
+
+class AdamWJobs:
+    """The buffers of an AdamW step over a list of fragments, checked once.
+
+    Per-fragment lists: theta (float32), grad (float32 or bfloat16), m and v
+    (float32, or float8_e4m3fn with m_scale and v_scale, float32 of
+    adamw_scale_slots(frag) elements), and optionally theta_bf16 (bfloat16
+    copies that every step writes) and decay (device float32 [T] factors on
+    the weight decay). Entries of the optional lists may be None."""
+
+    def __init__(self, frags, theta, grad, m, v, m_scale=None, v_scale=None, theta_bf16=None,
+                 decay=None):
+        self.frags = list(frags)
+        P = len(self.frags)
+        lists = {"theta": theta, "grad": grad, "m": m, "v": v, "m_scale": m_scale,
+                 "v_scale": v_scale, "theta_bf16": theta_bf16, "decay": decay}
+        lists = {k: [None] * P if x is None else list(x) for k, x in lists.items()}
+        for name, x in lists.items():
+            if len(x) != P:
+                raise ValueError(f"{name}: {len(x)} buffers for {P} fragments")
+        gtype = next((g.dtype for g in lists["grad"] if g is not None), torch.float32)
+        stype = next((s.dtype for s in lists["m"] if s is not None), torch.float32)
+        if gtype not in _GRADS:
+            raise TypeError(f"grad[0]: dtype {gtype}, expected float32 or bfloat16")
+        if stype not in (torch.float32, torch.float8_e4m3fn):
+            raise TypeError(f"m[0]: dtype {stype}, expected float32 or float8_e4m3fn")
+        by8 = stype == torch.float8_e4m3fn
+        self.grad_type, self.state_type = _TYPE[gtype], DL_E4M3 if by8 else DL_F32
+        self._jobs = (_AdamWJob * max(P, 1))()
+        for j, F in enumerate(self.frags):
+            slots = adamw_scale_slots(F) if by8 else 0
+            for name, dtypes, n, needed in (
+                    ("theta", _F32, F.n, True), ("grad", (gtype,), F.n, True),
+                    ("m", (stype,), F.n, True), ("v", (stype,), F.n, True),
+                    ("m_scale", _F32, slots, by8), ("v_scale", _F32, slots, by8),
+                    ("theta_bf16", (torch.bfloat16,), F.n, False), ("decay", _F32, F.T, False)):
+                t = lists[name][j]
+                if t is None and needed and F.n > 0:
+                    raise ValueError(f"{name}[{j}]: missing")
+                _need(t, dtypes, n, f"{name}[{j}]")
+                setattr(self._jobs[j], "d_decay" if name == "decay" else name,
+                        None if t is None else t.data_ptr())
+            self._jobs[j].frag = ctypes.pointer(F._c)
+        _cuda(*lists.values())
+        self.buffers = lists
+        self._cfg = _AdamWConfig()
+
+
+def adamw_step(jobs: AdamWJobs, step, lr=4e-4, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1,
+               clip=None, seed=0, stream=None):
+    """One AdamW step over every job, in place (dl_adamw_step). step counts
+    from 1. clip: device float32 (norm, coefficient) as grad_norm returns it;
+    a coefficient that is not finite skips the step on the device. seed: of
+    the 8-bit states' rounding; it may stay the same over a run."""
+    if clip is not None:
+        _need(clip, _F32, 2, "clip")
+        _cuda(clip)
+    c = jobs._cfg
+    c.lr, c.beta1, c.beta2, c.eps, c.weight_decay = lr, betas[0], betas[1], eps, weight_decay
+    c.step, c.seed = int(step), int(seed) & (2**64 - 1)
+    _check("dl_adamw_step", lib().dl_adamw_step(
+        jobs._jobs, len(jobs.frags), jobs.grad_type, jobs.state_type, ctypes.byref(c), _ptr(clip),
+        _stream(stream)))
+
+
+class InnerAdamW:
+    """AdamW over a learner's fragments with its states, clipping first.
+
+    theta and grad: per-fragment lists of flat device buffers (a learner's
+    replica and the gradients that its backward passes write). bits: 32 or 8,
+    the width of the states. max_norm: clip by the global gradient norm; a
+    step whose gradients are not all finite is then skipped on the device
+    (``steps`` still counts it). decay: per-fragment lists or arrays of T
+    factors on the weight decay (0 for norms and biases). theta_bf16: buffers
+    that receive a rounded copy of the parameters every step."""
+
+    def __init__(self, frags, theta, grad, bits=32, lr=4e-4, betas=(0.9, 0.95), eps=1e-8,
+                 weight_decay=0.1, decay=None, theta_bf16=None, max_norm=None, seed=0):
+        if bits not in (32, 8):
+            raise ValueError(f"bits: {bits}, expected 32 or 8")
+        frags, theta = list(frags), list(theta)
+        dev = theta[0].device
+        self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
+        self.max_norm, self.seed, self.steps = max_norm, seed, 0
+        dtype = torch.float32 if bits == 32 else torch.float8_e4m3fn
+
+        def zeros(sizes, dt):  # e4m3's code 0 is the value 0
+            return [torch.zeros(max(n, 1), dtype=torch.uint8 if dt == torch.float8_e4m3fn else dt,
+                                device=dev).view(dt) for n in sizes]
+        self.m, self.v = (zeros([F.n for F in frags], dtype) for _ in range(2))
+        self.m_scale = self.v_scale = None
+        if bits == 8:
+            self.m_scale, self.v_scale = (zeros([adamw_scale_slots(F) for F in frags],
+                                                torch.float32) for _ in range(2))
+        if decay is not None:
+            decay = [None if d is None else torch.as_tensor(d, dtype=torch.float32, device=dev)
+                     for d in decay]
+        self.jobs = AdamWJobs(frags, theta, grad, self.m, self.v, self.m_scale, self.v_scale,
+                              theta_bf16, decay)
+        self.grads = GradList([g for g in grad if g.numel()])
+        self.clip = torch.ones(2, dtype=torch.float32, device=dev)
+        self.workspace = new_workspace(grad_norm_workspace_bytes(), dev)
+
+    def step(self, lr=None, stream=None):
+        """Clip (with max_norm) and step; returns the device tensor (norm,
+        coefficient) or, without max_norm, None."""
+        self.steps += 1
+        clip = None
+        if self.max_norm is not None:
+            clip = grad_norm(self.grads, self.max_norm, self.clip, self.workspace, stream)
+        adamw_step(self.jobs, self.steps, self.lr if lr is None else lr, self.betas, self.eps,
+                   self.weight_decay, clip, self.seed, stream)
+        return clip
+
+
+# ----------------------------------------------------------------------------
+# layer norm
+
+
+def layernorm_workspace_bytes(rows: int, width: int) -> int:
+    return int(lib().dl_layernorm_workspace_bytes(rows, width))
+
+
+def _rows(t, name, like=None):
+    """(tensor, row stride) of rows of a last dimension with stride 1; the
+    leading dimensions must fold into one."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype not in _TYPE or (like is not None and t.dtype != like.dtype):
+        want = like.dtype if like is not None else "float32, bfloat16 or float16"
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {want}")
+    if like is not None and t.shape != like.shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(like.shape)}")
+    if t.dim() == 0:
+        raise ValueError(f"{name}: needs at least one dimension")
+    width = t.shape[-1]
+    if t.is_contiguous():
+        return t, width
+    if t.dim() != 2:
+        try:
+            t = t.view(-1, width)
+        except RuntimeError:
+            raise ValueError(f"{name}: the leading dimensions do not fold into rows") from None
+    if t.stride(1) != 1 and width > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if t.shape[0] > 1 and t.stride(0) < width:
+        raise ValueError(f"{name}: rows overlap (stride {t.stride(0)}, width {width})")
+    return t, max(t.stride(0), width)
+
+
+def _params(weight, bias, width):
+    _need(weight, _PARAMS, width, "weight")
+    if weight is None or weight.numel() != width:
+        raise ValueError(f"weight: expected {width} elements")
+    if bias is not None:
+        _need(bias, (weight.dtype,), width, "bias")
+    return _TYPE[weight.dtype]
+
+
+def layernorm_forward(x, weight, bias=None, eps=1e-5, rms=False, y=None, mean=None, rstd=None,
+                      stream=None):
+    """Layer norm over the last dimension (dl_layernorm_forward). Returns
+    (y, mean, rstd), mean None with rms=True. x: float32, bfloat16 or float16
+    with a contiguous last dimension; weight, bias: float32 or bfloat16."""
+    xr, xs = _rows(x, "x")
+    width = x.shape[-1]
+    if width < 1:
+        raise ValueError("x: the last dimension is empty")
+    rows = x.numel() // width
+    ptype = _params(weight, bias, width)
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    yr, ys = _rows(y, "y", x)
+    if rstd is None:
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    if rms:
+        mean = None
+    elif mean is None:
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    _need(mean, _F32, rows, "mean")
+    _need(rstd, _F32, rows, "rstd")
+    _cuda(x, weight, bias, y, mean, rstd)
+    _check("dl_layernorm_forward", lib().dl_layernorm_forward(
+        xr.data_ptr(), xs, _TYPE[x.dtype], rows, width, weight.data_ptr(), _ptr(bias), ptype, eps,
+        DL_NORM_RMS if rms else 0, yr.data_ptr(), ys, _ptr(mean), rstd.data_ptr(),
+        _stream(stream)))
+    return y, mean, rstd
+
+
+def layernorm_backward(dy, x, weight, mean, rstd, dweight=None, dbias=None, rms=False,
+                       accumulate=False, dx=None, workspace=None, bias=True, stream=None):
+    """Gradients of layernorm_forward (dl_layernorm_backward). Returns (dx,
+    dweight, dbias). dweight and dbias may be slices of a fragment's flat
+    gradient buffer; with accumulate=True the sums are added to what they
+    hold. Without a dweight both are allocated (dbias only with bias=True);
+    a call that passes dweight alone computes no dbias."""
+    xr, xs = _rows(x, "x")
+    dyr, ds = _rows(dy, "dy", x)
+    width = x.shape[-1]
+    if width < 1:
+        raise ValueError("x: the last dimension is empty")
+    rows = x.numel() // width
+    ptype = _params(weight, None, width)
+    if dweight is None:
+        if accumulate:
+            raise ValueError("accumulate: needs the dweight to add to")
+        dweight = torch.empty(width, dtype=weight.dtype, device=x.device)
+        if dbias is None and bias:
+            dbias = torch.empty(width, dtype=weight.dtype, device=x.device)
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dxr, os = _rows(dx, "dx", x)
+    if workspace is None:
+        workspace = torch.empty(layernorm_workspace_bytes(rows, width), dtype=torch.uint8,
+                                device=x.device)
+    if rms:
+        mean = None
+    elif mean is None:
+        raise ValueError("mean: missing (rms=False)")
+    _need(mean, _F32, rows, "mean")
+    _need(rstd, _F32, rows, "rstd")
+    _need(dweight, (weight.dtype,), width, "dweight")
+    _need(dbias, (weight.dtype,), width, "dbias")
+    _need(workspace, _U8, 0, "workspace")
+    _cuda(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace)
+    flags = (DL_NORM_RMS if rms else 0) | (DL_NORM_ACCUMULATE if accumulate else 0)
+    _check("dl_layernorm_backward", lib().dl_layernorm_backward(
+        dyr.data_ptr(), ds, xr.data_ptr(), xs, _TYPE[x.dtype], rows, width, weight.data_ptr(),
+        ptype, _ptr(mean), rstd.data_ptr(), flags, dxr.data_ptr(), os, dweight.data_ptr(),
+        _ptr(dbias), workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    return dx, dweight, dbias
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, rms):
+        y, mean, rstd = layernorm_forward(x, weight, bias, eps, rms)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.rms, ctx.bias = rms, bias is not None
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, mean, rstd = ctx.saved_tensors
+        # a broadcast gradient (as of a sum) has rows that overlap
+        dx, dw, db = layernorm_backward(dy.contiguous(), x, weight, mean, rstd, rms=ctx.rms,
+                                        bias=ctx.bias)
+        return dx, dw, db, None, None
+
+
+def layer_norm(x, weight, bias=None, eps=1e-5, rms=False):
+    """layernorm_forward as a torch.autograd operation."""
+    return _LayerNorm.apply(x, weight, bias, eps, rms)
