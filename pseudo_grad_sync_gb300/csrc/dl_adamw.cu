@@ -48,6 +48,38 @@ __device__ __forceinline__ void unpack(const uint4& q, float (&v)[8], __nv_bfloa
     }
 }
 
+// A group's sum of squares in this range lost nothing to fp32's range: none
+// of its squares overflowed, and a subnormal square is off by 2^-150 at most.
+// Any other group (zeros, tiny or huge values, Inf, NaN) is summed again in
+// fp64.
+constexpr float kSquareLo = 0x1p-100f, kSquareHi = 0x1p126f;
+
+// read once, not kept in L1
+__device__ __forceinline__ uint4 load_once(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// One group's squares in fp64, read again: out of line, so that the groups in
+// range keep their registers.
+template <typename T>
+__device__ __noinline__ double squares64(const uint4* body, int64_t i, int64_t vecs) {
+    constexpr int W = 16 / sizeof(T);
+    double s = 0.0;
+    for (int u = 0; u < kNormVecs && i < vecs; ++u, i += kThreads) {
+        const uint4 q = __ldg(body + i);
+        if ((q.x | q.y | q.z | q.w) == 0) continue;
+        float v[W];
+        unpack(q, v, T());
+#pragma unroll
+        for (int w = 0; w < W; ++w) s = fma(static_cast<double>(v[w]), static_cast<double>(v[w]), s);
+    }
+    return s;
+}
+
 // Elements before the first 16-byte boundary of a buffer.
 template <typename T>
 __host__ __device__ inline int64_t head_of(const void* p, int64_t n) {
@@ -71,15 +103,24 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ 
         const int64_t n = a.numel[j], head = head_of<T>(g, n);
         const int64_t vecs = (n - head) / W;
         const uint4* body = reinterpret_cast<const uint4*>(g + head);
-        for (int u = 0; u < kNormVecs; ++u) {
-            const int64_t i = first * kNormChunk + u * kThreads + threadIdx.x;
-            if (i < vecs) {
-                float v[W];
-                unpack(__ldg(body + i), v, T());
+        uint4 q[kNormVecs];
+        const int64_t i0 = first * kNormChunk + threadIdx.x;
 #pragma unroll
-                for (int w = 0; w < W; ++w) sum = fma((double)v[w], (double)v[w], sum);
-            }
+        for (int u = 0; u < kNormVecs; ++u)
+            q[u] = i0 + u * kThreads < vecs ? load_once(body + i0 + u * kThreads) : uint4{0, 0, 0, 0};
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < kNormVecs; ++u) {
+            float v[W];
+            unpack(q[u], v, T());
+#pragma unroll
+            for (int w = 0; w < W; ++w) part[w & 3] = fmaf(v[w], v[w], part[w & 3]);
         }
+        const float group = (part[0] + part[1]) + (part[2] + part[3]);
+        if (group >= kSquareLo && group <= kSquareHi)
+            sum += static_cast<double>(group);
+        else
+            sum += squares64<T>(body, i0, vecs);
         if (first == 0) {
             const int64_t rest = n - vecs * W;  // the head's and the tail's elements
             if (threadIdx.x < rest) {
@@ -154,15 +195,11 @@ struct AdamArgs {
     const float* clip;
 };
 
-struct Hyper {
-    float coef, keep;
-};
-
 // theta' from the new moments; root = sqrt(v')
 __device__ __forceinline__ float step_theta(const AdamArgs& a, float theta, float m, float root,
                                             float keep) {
     const float denom = fmaf(root, a.inv_root_bc2, a.eps);
-    return fmaf(-a.step_size, m / denom, theta * keep);
+    return fmaf(-a.step_size, __fdividef(m, denom), theta * keep);
 }
 
 __device__ __forceinline__ float clip_coef(const AdamArgs& a) { return a.clip ? __ldg(a.clip + 1) : 1.0f; }
@@ -171,7 +208,32 @@ __device__ __forceinline__ float keep_of(const AdamArgs& a, const AdamJob& J, in
     return J.decay ? 1.0f - a.lr_wd * __ldg(J.decay + t) : 1.0f - a.lr_wd;
 }
 
-constexpr int kTile32 = 2048;
+// Four elements of a type as one aligned load or store.
+__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
+    const float4 q = *reinterpret_cast<const float4*>(p);
+    v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&v)[4]) {
+    const uint2 q = *reinterpret_cast<const uint2*>(p);
+    v[0] = __uint_as_float(q.x << 16), v[1] = __uint_as_float(q.x & 0xffff0000u);
+    v[2] = __uint_as_float(q.y << 16), v[3] = __uint_as_float(q.y & 0xffff0000u);
+}
+__device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
+    __nv_bfloat162 q[2] = {__floats2bfloat162_rn(v[0], v[1]), __floats2bfloat162_rn(v[2], v[3])};
+    *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(q);
+}
+
+__device__ __forceinline__ float sqrt_approx(float v) {
+    float r;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+constexpr int kGroups32 = 2;                         // groups of four elements per thread
+constexpr int kTile32 = kThreads * 4 * kGroups32;
 
 template <typename G>
 __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ AdamArgs a) {
@@ -181,19 +243,74 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Adam
     while (static_cast<int64_t>(blockIdx.x) >= a.job[j].work_end) ++j;
     const AdamJob& J = a.job[j];
     const int64_t base = (blockIdx.x - (j ? a.job[j - 1].work_end : 0)) * int64_t(kTile32);
-    const G* g = static_cast<const G*>(J.grad);
-    float* m = static_cast<float*>(J.m);
-    float* v = static_cast<float*>(J.v);
-    for (int64_t i = base + threadIdx.x; i < base + kTile32 && i < J.n; i += kThreads) {
-        const float keep = keep_of(a, J, J.decay ? tensor_containing(J.off, J.T, i) : 0);
-        const float gi = to_f32(g[i]) * coef;
-        const float mi = fmaf(a.beta1, m[i], a.om_beta1 * gi);
-        const float vi = fmaf(a.beta2, v[i], a.om_beta2 * (gi * gi));
-        const float th = step_theta(a, J.theta[i], mi, sqrtf(vi), keep);
-        m[i] = mi;
-        v[i] = vi;
-        J.theta[i] = th;
-        if (J.copy) J.copy[i] = __float2bfloat16_rn(th);
+    const int n = static_cast<int>(min(J.n - base, int64_t(kTile32)));  // of this tile
+    const G* g = static_cast<const G*>(J.grad) + base;
+    float* m = static_cast<float*>(J.m) + base;
+    float* v = static_cast<float*>(J.v) + base;
+    float* theta = J.theta + base;
+    __nv_bfloat16* copy = J.copy ? J.copy + base : nullptr;
+    float tv[kGroups32][4], gv[kGroups32][4], mv[kGroups32][4], vv[kGroups32][4];
+#pragma unroll
+    for (int u = 0; u < kGroups32; ++u) {
+        const int i = (u * kThreads + static_cast<int>(threadIdx.x)) * 4;
+        if (i + 4 <= n) {
+            load4(theta + i, tv[u]);
+            load4(g + i, gv[u]);
+            load4(m + i, mv[u]);
+            load4(v + i, vv[u]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                tv[u][e] = gv[u][e] = mv[u][e] = vv[u][e] = 0.f;
+                if (i + e < n) {
+                    tv[u][e] = theta[i + e], gv[u][e] = to_f32(g[i + e]);
+                    mv[u][e] = m[i + e], vv[u][e] = v[i + e];
+                }
+            }
+        }
+    }
+    // the tile's tensor; a tile of several looks each group's up
+    int t = 0;
+    bool one = true;
+    if (J.decay) {
+        t = tensor_containing(J.off, J.T, base);
+        one = __ldg(J.off + t + 1) >= base + n;
+    }
+    const float keep = keep_of(a, J, t);
+#pragma unroll
+    for (int u = 0; u < kGroups32; ++u) {
+        const int i = (u * kThreads + static_cast<int>(threadIdx.x)) * 4;
+        if (i >= n) continue;
+        float kv[4] = {keep, keep, keep, keep};
+        if (!one) {
+            int te = tensor_from(J.off, t, J.T, base + i);
+            int64_t end = __ldg(J.off + te + 1);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                while (base + i + e >= end && te < J.T - 1) end = __ldg(J.off + ++te + 1);
+                kv[e] = keep_of(a, J, te);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float gi = gv[u][e] * coef;
+            mv[u][e] = fmaf(a.beta1, mv[u][e], a.om_beta1 * gi);
+            vv[u][e] = fmaf(a.beta2, vv[u][e], a.om_beta2 * (gi * gi));
+            tv[u][e] = step_theta(a, tv[u][e], mv[u][e], sqrt_approx(vv[u][e]), kv[e]);
+        }
+        if (i + 4 <= n) {
+            store4(theta + i, tv[u]);
+            store4(m + i, mv[u]);
+            store4(v + i, vv[u]);
+            if (copy) store4(copy + i, tv[u]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e < n) {
+                    theta[i + e] = tv[u][e], m[i + e] = mv[u][e], v[i + e] = vv[u][e];
+                    if (copy) copy[i + e] = __float2bfloat16_rn(tv[u][e]);
+                }
+        }
     }
 }
 
@@ -278,6 +395,13 @@ __global__ void __launch_bounds__(kThreads) k_adamw8(const __grid_constant__ Ada
         const int cnt = i0 >= o1 ? 0 : o1 - i0 < 4 ? static_cast<int>(o1 - i0) : 4;
         uint32_t cm = 0, cs = 0;
         float th[4], gr[4], m[4], r[4];
+        const bool quad = cnt == 4 && (begin & 3) == 0;
+        if (quad) {
+            load4(J.theta + i0, th);
+            load4(g + i0, gr);
+            cm = *reinterpret_cast<const uint32_t*>(m8 + i0);
+            cs = *reinterpret_cast<const uint32_t*>(s8 + i0);
+        } else
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             th[e] = gr[e] = 0.f;
@@ -316,6 +440,12 @@ __global__ void __launch_bounds__(kThreads) k_adamw8(const __grid_constant__ Ada
         const uint64_t z = mix64(a.key + ((J.slot0 + s) * (kBlock / 4) + lane) * kGolden);
         cm = encode4(m, static_cast<uint32_t>(z));
         cs = encode4(r, static_cast<uint32_t>(z >> 32));
+        if (quad) {
+            store4(J.theta + i0, th);
+            *reinterpret_cast<uint32_t*>(m8 + i0) = cm;
+            *reinterpret_cast<uint32_t*>(s8 + i0) = cs;
+            if (J.copy) store4(J.copy + i0, th);
+        } else
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             if (e < cnt) {
