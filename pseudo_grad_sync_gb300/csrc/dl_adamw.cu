@@ -183,14 +183,16 @@ struct AdamJob {
     const int64_t* off;
     int64_t n;
     int64_t slot0;     // slots of all jobs before this one
-    int64_t work_end;  // running number of blocks' tiles
+    int64_t work_end;  // running number of tiles (32-bit states) or slots (8-bit)
     int T;
 };
 
 struct AdamArgs {
     AdamJob job[kAdamJobs];
     int n;
+    int64_t run;  // 8-bit states: consecutive slots of a warp
     float lr_wd, step_size, beta1, om_beta1, beta2, om_beta2, inv_root_bc2, eps;
+    float one;  // 1
     uint64_t key;
     const float* clip;
 };
@@ -226,6 +228,11 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
     *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(q);
 }
 
+__device__ __forceinline__ float rcp_approx(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
 __device__ __forceinline__ float sqrt_approx(float v) {
     float r;
     asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -357,8 +364,6 @@ __device__ __forceinline__ uint32_t encode4(const float (&x)[4], uint32_t bits) 
     return c;
 }
 
-constexpr int kSlotsPerTile = 64;
-
 // first tensor t with off[t+1] / 128 + t + 1 > slot
 __device__ __forceinline__ int tensor_of_slot(const int64_t* off, int T, int64_t slot) {
     int lo = 0, hi = T - 1;
@@ -372,92 +377,386 @@ __device__ __forceinline__ int tensor_of_slot(const int64_t* off, int T, int64_t
     return lo;
 }
 
-template <typename G>
-__global__ void __launch_bounds__(kThreads) k_adamw8(const __grid_constant__ AdamArgs a) {
-    const float coef = clip_coef(a);
-    if (!isfinite(coef)) return;
-    int j = 0;
-    while (static_cast<int64_t>(blockIdx.x) >= a.job[j].work_end) ++j;
-    const AdamJob& J = a.job[j];
-    const int64_t tile = (blockIdx.x - (j ? a.job[j - 1].work_end : 0)) * int64_t(kSlotsPerTile);
-    const int64_t slots = J.n / kBlock + J.T;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const G* g = static_cast<const G*>(J.grad);
-    uint8_t* m8 = static_cast<uint8_t*>(J.m);
-    uint8_t* s8 = static_cast<uint8_t*>(J.v);
-    for (int64_t s = tile + warp; s < tile + kSlotsPerTile && s < slots; s += kWarps) {
-        const int t = tensor_of_slot(J.off, J.T, s);
-        const int64_t o0 = __ldg(J.off + t), o1 = __ldg(J.off + t + 1);
-        const int64_t begin = o0 + (s - (o0 / kBlock + t)) * kBlock;
-        if (begin >= o1) continue;  // a slot without a block
-        const float keep = keep_of(a, J, t);
-        const int64_t i0 = begin + 4 * lane;
-        const int cnt = i0 >= o1 ? 0 : o1 - i0 < 4 ? static_cast<int>(o1 - i0) : 4;
-        uint32_t cm = 0, cs = 0;
-        float th[4], gr[4], m[4], r[4];
-        const bool quad = cnt == 4 && (begin & 3) == 0;
-        if (quad) {
-            load4(J.theta + i0, th);
-            load4(g + i0, gr);
-            cm = *reinterpret_cast<const uint32_t*>(m8 + i0);
-            cs = *reinterpret_cast<const uint32_t*>(s8 + i0);
-        } else
+// The tensor of a warp's current slot, walking forward.
+struct SlotCursor {
+    int t;
+    int64_t o0, o1, first, next;  // elements [o0, o1), slots [first, next)
+    __device__ __forceinline__ void load(const int64_t* off) {
+        o0 = __ldg(off + t), o1 = __ldg(off + t + 1);
+        first = o0 / kBlock + t, next = o1 / kBlock + t + 1;
+    }
+    __device__ __forceinline__ void seek(const int64_t* off, int64_t slot) {
+        while (slot >= next) ++t, load(off);
+    }
+};
+
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float rsqrt_approx(float v) {
+    float r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// Two products or fused products at once, each rounded.
+__device__ __forceinline__ uint64_t bits2(float2 v) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+    return r;
+}
+__device__ __forceinline__ float2 floats2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(x)), "l"(bits2(y)));
+    return floats2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(x)), "l"(bits2(y)), "l"(bits2(z)));
+    return floats2(r);
+}
+
+// One lane's share of a block: four elements (those past a tensor's end are
+// zeros and are not stored).
+struct Quad {
+    float2 th[2], gr[2];
+    uint32_t cm, cs;
+    float msc, ssc;
+};
+
+// Moments above this have the rounded square root from root2 (tested against
+// the exact function for every float from here to FLT_MAX).
+constexpr uint32_t kRootLo = (127u - 100u) << 23, kRootEnd = 255u << 23;
+
+// sqrt(v): the estimate g = v y with y = rsqrt(v), corrected once by its
+// residual v - g^2, which the fused multiply-add gives (Markstein 1990).
+__device__ __forceinline__ float2 root2(float2 v) {
+    const float2 y = make_float2(rsqrt_approx(v.x), rsqrt_approx(v.y));
+    const float2 g = mul2(v, y);
+    const float2 less = fma2(g, g, mul2(v, both(-1.f)));
+    return fma2(less, mul2(y, both(-0.5f)), g);
+}
+
+// The step of one quad: theta and the codes in place; all 32 lanes of the
+// block's warp call it. Returns the bits of the block's largest moments.
+__device__ __forceinline__ void step_quad(const AdamArgs& a, float coef, float keep, uint64_t z,
+                                          Quad& q, uint32_t& mtop, uint32_t& stop) {
+    float c[4], d[4];
+    decode4(q.cm, c);
+    decode4(q.cs, d);
+    // The scales are powers of two: folded into the betas they give the same
+    // bits as value = code * scale first (the code's square is exact too).
+    const float2 b1 = both(a.beta1 * q.msc), b2 = both(a.beta2 * (q.ssc * q.ssc));
+    // The definition rounds the products before the sum. A packed product and
+    // a packed sum come out fused (CUDA 13.0, their .rn notwithstanding: exact
+    // cancellations then leave a residue), so the sums are x * one + y with a
+    // one that the compiler does not know.
+    const float2 one = both(a.one);
+    float2 m[2], v[2], r[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            th[e] = gr[e] = 0.f;
-            if (e < cnt) {
-                th[e] = J.theta[i0 + e];
-                gr[e] = to_f32(g[i0 + e]);
-                cm |= uint32_t(m8[i0 + e]) << (8 * e);
-                cs |= uint32_t(s8[i0 + e]) << (8 * e);
+    for (int h = 0; h < 2; ++h) {
+        const float2 cd = make_float2(c[2 * h], c[2 * h + 1]), dd = make_float2(d[2 * h], d[2 * h + 1]);
+        const float2 g = mul2(q.gr[h], both(coef));
+        m[h] = fma2(mul2(cd, b1), one, mul2(g, both(a.om_beta1)));
+        v[h] = fma2(mul2(mul2(dd, dd), b2), one, mul2(mul2(g, g), both(a.om_beta2)));
+        r[h] = root2(v[h]);
+    }
+    // zeros, tiny values, Inf and NaN wrap past the range
+    const uint32_t far = max(max(__float_as_uint(v[0].x) - kRootLo, __float_as_uint(v[0].y) - kRootLo),
+                             max(__float_as_uint(v[1].x) - kRootLo, __float_as_uint(v[1].y) - kRootLo));
+    const bool plain = far < kRootEnd - kRootLo;
+    if (!plain) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            r[h] = make_float2(__fsqrt_rn(v[h].x), __fsqrt_rn(v[h].y));
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float2 denom = fma2(r[h], both(a.inv_root_bc2), both(a.eps));
+        const float2 up = mul2(m[h], make_float2(rcp_approx(denom.x), rcp_approx(denom.y)));
+        q.th[h] = fma2(up, both(-a.step_size), mul2(q.th[h], both(keep)));
+    }
+    const float mt = max_nan(max_nan(fabsf(m[0].x), fabsf(m[0].y)), max_nan(fabsf(m[1].x), fabsf(m[1].y)));
+    const float st = max_nan(max_nan(r[0].x, r[0].y), max_nan(r[1].x, r[1].y));
+    mtop = __reduce_max_sync(kFull, __float_as_uint(mt));
+    stop = __reduce_max_sync(kFull, __float_as_uint(st) & 0x7fffffffu);
+    const float2 minv = both(block_inverse(mtop)), sinv = both(block_inverse(stop));
+    float mx[4], sx[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float2 x = mul2(m[h], minv), y = mul2(r[h], sinv);
+        mx[2 * h] = x.x, mx[2 * h + 1] = x.y;
+        sx[2 * h] = y.x, sx[2 * h + 1] = y.y;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)  // a positive root keeps at least the smallest code
+        sx[e] = plain || sx[e] > 0.f ? fmaxf(sx[e], 0x1p-9f) : sx[e];
+    q.cm = encode4(mx, static_cast<uint32_t>(z));
+    q.cs = encode4(sx, static_cast<uint32_t>(z >> 32));
+}
+
+// ---------------------------------------------------------------------------
+// A warp's run of whole blocks. Each warp has a ring of stages in shared
+// memory that asynchronous copies fill some blocks ahead; a stage holds the
+// aligned groups of four elements ("quads") that a block touches: 32, or 33
+// when the block starts A = 1, 2 or 3 elements into its first quad.
+constexpr int kStages = 4;
+
+template <typename G>
+struct __align__(16) Stage {
+    float4 th[33];
+    Pack<G, 4> gr[33];
+    uint32_t cm[33], cs[33];
+    float scale[2];
+};
+
+// Copies of up to BYTES (4, 8 or 16); the bytes past `valid` are not read.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, int valid = BYTES) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src),
+                     "r"(valid)
+                     : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_addr(dst)), "l"(src),
+                     "n"(BYTES), "r"(valid)
+                     : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// the four elements from A on of two consecutive quads
+template <int A>
+__device__ __forceinline__ void shifted(const float4* q, float2 (&v)[2]) {
+    const float4 x = q[0];
+    if constexpr (A == 0) {
+        v[0] = make_float2(x.x, x.y), v[1] = make_float2(x.z, x.w);
+    } else {
+        const float4 y = q[1];
+        const float w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        v[0] = make_float2(w[A], w[A + 1]), v[1] = make_float2(w[A + 2], w[A + 3]);
+    }
+}
+template <int A>
+__device__ __forceinline__ void shifted(const Pack<float, 4>* q, float2 (&v)[2]) {
+    shifted<A>(reinterpret_cast<const float4*>(q), v);
+}
+template <int A>
+__device__ __forceinline__ void shifted(const Pack<__nv_bfloat16, 4>* q, float2 (&v)[2]) {
+    const uint2 x = *reinterpret_cast<const uint2*>(q);
+    uint32_t lo = x.x, hi = x.y;
+    if constexpr (A != 0) {
+        const uint2 y = *reinterpret_cast<const uint2*>(q + 1);
+        const uint32_t w[4] = {x.x, x.y, y.x, y.y};
+        lo = __funnelshift_r(w[A / 2], w[A / 2 + 1], 16 * (A & 1));
+        hi = __funnelshift_r(w[A / 2 + 1], w[(A + 1) / 2 + 1], 16 * (A & 1));
+    }
+    v[0] = make_float2(__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u));
+    v[1] = make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
+}
+
+// `count` whole blocks from element `begin` (begin % 4 == A), slot `slot` on.
+// For A > 0 the first quad's leading A elements must be this warp's own or
+// not be written by anyone else.
+template <typename G, int A>
+__device__ __forceinline__ void run_blocks(const AdamArgs& a, const AdamJob& J, float coef, float keep,
+                                           int64_t begin, int64_t slot, int64_t count, int lane,
+                                           Stage<G>* ring) {
+    const int64_t q0 = begin - A + 4 * lane;  // this lane's quad of the first block
+    float* th = J.theta + q0;
+    const G* g = static_cast<const G*>(J.grad) + q0;
+    uint8_t* m8 = static_cast<uint8_t*>(J.m) + q0;
+    uint8_t* s8 = static_cast<uint8_t*>(J.v) + q0;
+    const float* sc = (lane == 0 ? J.m_scale : J.v_scale) + slot;
+    auto issue = [&](int64_t i) {
+        if (i < count) {
+            Stage<G>& st = ring[i % kStages];
+            const int64_t o = i * kBlock;
+            copy_async<16>(&st.th[lane], th + o);
+            copy_async<4 * sizeof(G)>(&st.gr[lane], g + o);
+            copy_async<4>(&st.cm[lane], m8 + o);
+            copy_async<4>(&st.cs[lane], s8 + o);
+            if (lane < 2) copy_async<4>(&st.scale[lane], sc + i);
+            if (A > 0 && lane == 0) {  // the block's last A elements
+                copy_async<16>(&st.th[32], th + o + kBlock, 4 * A);
+                copy_async<4 * sizeof(G)>(&st.gr[32], g + o + kBlock, sizeof(G) * A);
+                copy_async<4>(&st.cm[32], m8 + o + kBlock, A);
+                copy_async<4>(&st.cs[32], s8 + o + kBlock, A);
             }
         }
-        decode4(cm, m);
-        decode4(cs, r);
-        const float msc = J.m_scale[s], ssc = J.v_scale[s];
-        uint32_t mtop = 0, stop = 0;
+        copy_commit();
+    };
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float gi = __fmul_rn(gr[e], coef);
-            m[e] = __fadd_rn(__fmul_rn(__fmul_rn(m[e], msc), a.beta1), __fmul_rn(gi, a.om_beta1));
-            const float old = __fmul_rn(r[e], ssc);
-            const float v = __fadd_rn(__fmul_rn(__fmul_rn(old, old), a.beta2),
-                                      __fmul_rn(__fmul_rn(gi, gi), a.om_beta2));
-            r[e] = __fsqrt_rn(v);
-            th[e] = step_theta(a, th[e], m[e], r[e], keep);
-            mtop = max(mtop, __float_as_uint(fabsf(m[e])));
-            stop = max(stop, __float_as_uint(r[e]) & 0x7fffffffu);
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+    uint64_t counter = a.key + ((J.slot0 + slot) * (kBlock / 4) + lane) * kGolden;
+    // what the previous block's last lane left of a quad (lane 0 only)
+    float left[A + 1];
+    uint32_t left_m = 0, left_s = 0;
+    for (int64_t i = 0; i < count; ++i, counter += (kBlock / 4) * kGolden) {
+        copy_wait<kStages - 2>();
+        __syncwarp();  // the stage has every lane's copies, and the last one every lane's reads
+        issue(i + kStages - 1);
+        const Stage<G>& st = ring[i % kStages];
+        Quad q;
+        shifted<A>(&st.th[lane], q.th);
+        shifted<A>(&st.gr[lane], q.gr);
+        q.cm = A ? __funnelshift_r(st.cm[lane], st.cm[lane + 1], 8 * A) : st.cm[lane];
+        q.cs = A ? __funnelshift_r(st.cs[lane], st.cs[lane + 1], 8 * A) : st.cs[lane];
+        q.msc = st.scale[0], q.ssc = st.scale[1];
+        uint32_t mtop, stop;
+        step_quad(a, coef, keep, mix64(counter), q, mtop, stop);
+        float out[4] = {q.th[0].x, q.th[0].y, q.th[1].x, q.th[1].y};
+        const int64_t o = i * kBlock;
+        bool whole = true;
+        if constexpr (A > 0) {
+            // quads as they lie in memory: the lane before gives the first A elements
+            const int from = (lane + 31) & 31;
+            float own[4], got[A];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) own[k] = out[k];
+#pragma unroll
+            for (int k = 0; k < A; ++k) got[k] = __shfl_sync(kFull, own[4 - A + k], from);
+            const uint32_t pm = __shfl_sync(kFull, q.cm, from), ps = __shfl_sync(kFull, q.cs, from);
+            whole = lane > 0 || i > 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) out[k] = k < A ? (lane ? got[k] : left[k]) : own[k - A];
+            q.cm = __funnelshift_l(lane ? pm : left_m, q.cm, 8 * A);
+            q.cs = __funnelshift_l(lane ? ps : left_s, q.cs, 8 * A);
+#pragma unroll
+            for (int k = 0; k < A; ++k) left[k] = got[k];
+            left_m = pm, left_s = ps;
         }
-        mtop = __reduce_max_sync(kFull, mtop);
-        stop = __reduce_max_sync(kFull, stop);
-        const float minv = block_inverse(mtop), sinv = block_inverse(stop);
+        if (whole) {
+            store4(th + o, out);
+            *reinterpret_cast<uint32_t*>(m8 + o) = q.cm;
+            *reinterpret_cast<uint32_t*>(s8 + o) = q.cs;
+            if (J.copy) store4(J.copy + q0 + o, out);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            m[e] *= minv;
-            const float x = r[e] * sinv;
-            r[e] = r[e] > 0.f ? fmaxf(x, 0x1p-9f) : x;
-        }
-        const uint64_t z = mix64(a.key + ((J.slot0 + s) * (kBlock / 4) + lane) * kGolden);
-        cm = encode4(m, static_cast<uint32_t>(z));
-        cs = encode4(r, static_cast<uint32_t>(z >> 32));
-        if (quad) {
-            store4(J.theta + i0, th);
-            *reinterpret_cast<uint32_t*>(m8 + i0) = cm;
-            *reinterpret_cast<uint32_t*>(s8 + i0) = cs;
-            if (J.copy) store4(J.copy + i0, th);
-        } else
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (e < cnt) {
-                J.theta[i0 + e] = th[e];
-                m8[i0 + e] = static_cast<uint8_t>(cm >> (8 * e));
-                s8[i0 + e] = static_cast<uint8_t>(cs >> (8 * e));
-                if (J.copy) J.copy[i0 + e] = __float2bfloat16_rn(th[e]);
+            for (int k = A; k < 4; ++k) {
+                th[o + k] = out[k];
+                m8[o + k] = static_cast<uint8_t>(q.cm >> (8 * k));
+                s8[o + k] = static_cast<uint8_t>(q.cs >> (8 * k));
+                if (J.copy) J.copy[q0 + o + k] = __float2bfloat16_rn(out[k]);
             }
         }
         if (lane == 0) {
-            J.m_scale[s] = block_scale(mtop);
-            J.v_scale[s] = block_scale(stop);
+            J.m_scale[slot + i] = block_scale(mtop);
+            J.v_scale[slot + i] = block_scale(stop);
+        }
+    }
+    if (A > 0 && lane == 0) {
+        const int64_t o = count * kBlock;
+#pragma unroll
+        for (int k = 0; k < A; ++k) {
+            th[o + k] = left[k];
+            m8[o + k] = static_cast<uint8_t>(left_m >> (8 * (4 - A + k)));
+            s8[o + k] = static_cast<uint8_t>(left_s >> (8 * (4 - A + k)));
+            if (J.copy) J.copy[q0 + o + k] = __float2bfloat16_rn(left[k]);
+        }
+    }
+    copy_wait<0>();
+    __syncwarp();  // before the ring is filled again
+}
+
+// One block at any element, of any length up to 128.
+template <typename G>
+__device__ __forceinline__ void any_block(const AdamArgs& a, const AdamJob& J, float coef, float keep,
+                                          int64_t begin, int64_t end, int64_t slot, int lane) {
+    const int64_t i0 = begin + 4 * lane;
+    const int cnt = static_cast<int>(max(int64_t(0), min(int64_t(4), end - i0)));
+    float* th = J.theta + i0;
+    const G* g = static_cast<const G*>(J.grad) + i0;
+    uint8_t* m8 = static_cast<uint8_t*>(J.m) + i0;
+    uint8_t* s8 = static_cast<uint8_t*>(J.v) + i0;
+    Quad q;
+    q.msc = J.m_scale[slot], q.ssc = J.v_scale[slot];
+    float t4[4], g4[4];
+    q.cm = q.cs = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        t4[e] = g4[e] = 0.f;
+        if (e < cnt) {
+            t4[e] = th[e];
+            g4[e] = to_f32(g[e]);
+            q.cm |= uint32_t(m8[e]) << (8 * e);
+            q.cs |= uint32_t(s8[e]) << (8 * e);
+        }
+    }
+    q.th[0] = make_float2(t4[0], t4[1]), q.th[1] = make_float2(t4[2], t4[3]);
+    q.gr[0] = make_float2(g4[0], g4[1]), q.gr[1] = make_float2(g4[2], g4[3]);
+    uint32_t mtop, stop;
+    step_quad(a, coef, keep, mix64(a.key + ((J.slot0 + slot) * (kBlock / 4) + lane) * kGolden), q, mtop,
+              stop);
+    const float out[4] = {q.th[0].x, q.th[0].y, q.th[1].x, q.th[1].y};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (e < cnt) {
+            th[e] = out[e];
+            m8[e] = static_cast<uint8_t>(q.cm >> (8 * e));
+            s8[e] = static_cast<uint8_t>(q.cs >> (8 * e));
+            if (J.copy) J.copy[i0 + e] = __float2bfloat16_rn(out[e]);
+        }
+    if (lane == 0) {
+        J.m_scale[slot] = block_scale(mtop);
+        J.v_scale[slot] = block_scale(stop);
+    }
+}
+
+template <typename G>
+__global__ void __launch_bounds__(kThreads, 4) k_adamw8(const __grid_constant__ AdamArgs a) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    const float coef = clip_coef(a);
+    if (!isfinite(coef)) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Stage<G>* ring = reinterpret_cast<Stage<G>*>(smem) + warp * kStages;
+    int64_t at = (int64_t(blockIdx.x) * kWarps + warp) * a.run;  // slot over the launch's jobs
+    const int64_t last = min(at + a.run, a.job[a.n - 1].work_end);
+    for (int j = 0; at < last; ++j) {
+        const AdamJob& J = a.job[j];
+        if (at >= J.work_end) continue;
+        const int64_t base = j ? a.job[j - 1].work_end : 0;
+        int64_t s = at - base;
+        const int64_t end = min(last, J.work_end) - base;
+        at = end + base;
+        SlotCursor c;
+        c.t = tensor_of_slot(J.off, J.T, s);
+        c.load(J.off);
+        bool own = false;  // whether the block before s was this warp's, of the same tensor
+        while (s < end) {
+            if (s >= c.next) c.seek(J.off, s), own = false;
+            const int64_t begin = c.o0 + (s - c.first) * kBlock;
+            if (begin >= c.o1) {  // a slot without a block
+                ++s;
+                continue;
+            }
+            const float keep = keep_of(a, J, c.t);
+            const int64_t count = min(end - s, (c.o1 - begin) / kBlock);
+            const int shift = static_cast<int>(begin & 3);
+            if (count > 0 && (shift == 0 || own)) {
+                switch (shift) {
+                    case 0: run_blocks<G, 0>(a, J, coef, keep, begin, s, count, lane, ring); break;
+                    case 1: run_blocks<G, 1>(a, J, coef, keep, begin, s, count, lane, ring); break;
+                    case 2: run_blocks<G, 2>(a, J, coef, keep, begin, s, count, lane, ring); break;
+                    default: run_blocks<G, 3>(a, J, coef, keep, begin, s, count, lane, ring); break;
+                }
+                s += count;
+            } else {
+                any_block<G>(a, J, coef, keep, begin, c.o1, s, lane);
+                ++s;
+            }
+            own = true;
         }
     }
 }
@@ -568,6 +867,7 @@ extern "C" int dl_adamw_step(const dl_adamw_job* jobs, int32_t n_jobs, int32_t g
     a.om_beta2 = static_cast<float>(1.0 - cfg->beta2);
     a.inv_root_bc2 = static_cast<float>(1.0 / sqrt(bc2));
     a.eps = static_cast<float>(cfg->eps);
+    a.one = 1.0f;
     a.key = mix64(cfg->seed + static_cast<uint64_t>(cfg->step) * kGolden);
     a.clip = d_clip;
     int64_t slot0 = 0;
@@ -581,7 +881,7 @@ extern "C" int dl_adamw_step(const dl_adamw_job* jobs, int32_t n_jobs, int32_t g
             check_fragment(q.frag, &f);
             const int64_t slots = f.n / kBlock + f.T;
             if (f.n > 0) {
-                work += by8 ? (slots + kSlotsPerTile - 1) / kSlotsPerTile : (f.n + kTile32 - 1) / kTile32;
+                work += by8 ? slots : (f.n + kTile32 - 1) / kTile32;
                 a.job[a.n++] = AdamJob{q.theta, q.grad, q.m, q.v, q.m_scale, q.v_scale,
                                        static_cast<__nv_bfloat16*>(q.theta_bf16), q.d_decay,
                                        f.d_offsets, f.n, slot0, work, f.T};
@@ -589,14 +889,24 @@ extern "C" int dl_adamw_step(const dl_adamw_job* jobs, int32_t n_jobs, int32_t g
             slot0 += slots;
         }
         if (a.n == 0) continue;
-        if (work > INT32_MAX) return DL_ERR_ARG;
         const void* kernel =
             by8 ? (grad_type == DL_F32 ? reinterpret_cast<const void*>(k_adamw8<float>)
                                        : reinterpret_cast<const void*>(k_adamw8<__nv_bfloat16>))
                 : (grad_type == DL_F32 ? reinterpret_cast<const void*>(k_adamw<float>)
                                        : reinterpret_cast<const void*>(k_adamw<__nv_bfloat16>));
+        size_t smem = 0;
+        int64_t grid = work;
+        if (by8) {  // as many warps as the GPU holds, each with one run of slots
+            smem = kWarps * kStages * (grad_type == DL_F32 ? sizeof(Stage<float>) : sizeof(Stage<__nv_bfloat16>));
+            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(smem)) != cudaSuccess)
+                return DL_ERR_CUDA;
+            grid = grid_for(kernel, kThreads, smem, (work + kWarps - 1) / kWarps);
+            a.run = (work + grid * kWarps - 1) / (grid * kWarps);
+        }
+        if (grid > INT32_MAX) return DL_ERR_ARG;
         void* args[] = {&a};
-        if (cudaLaunchKernel(kernel, dim3(static_cast<unsigned>(work)), dim3(kThreads), args, 0,
+        if (cudaLaunchKernel(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), args, smem,
                              static_cast<cudaStream_t>(stream)) != cudaSuccess) {
             cudaGetLastError();
             return DL_ERR_CUDA;
