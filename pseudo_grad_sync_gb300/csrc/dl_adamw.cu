@@ -390,9 +390,9 @@ struct SlotCursor {
     }
 };
 
-__device__ __forceinline__ float max_nan(float x, float y) {
+__device__ __forceinline__ float max_nan(float x, float y, float z) {
     float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
     return r;
 }
 __device__ __forceinline__ float rsqrt_approx(float v) {
@@ -400,30 +400,6 @@ __device__ __forceinline__ float rsqrt_approx(float v) {
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-
-// Two products or fused products at once, each rounded.
-__device__ __forceinline__ uint64_t bits2(float2 v) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
-    return r;
-}
-__device__ __forceinline__ float2 floats2(uint64_t v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(x)), "l"(bits2(y)));
-    return floats2(r);
-}
-__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(x)), "l"(bits2(y)), "l"(bits2(z)));
-    return floats2(r);
-}
-
 // One lane's share of a block: four elements (those past a tensor's end are
 // zeros and are not stored).
 struct Quad {
@@ -434,7 +410,7 @@ struct Quad {
 
 // Moments above this have the rounded square root from root2 (tested against
 // the exact function for every float from here to FLT_MAX).
-constexpr uint32_t kRootLo = (127u - 100u) << 23, kRootEnd = 255u << 23;
+constexpr float kRootLo = 0x1p-100f;
 
 // sqrt(v): the estimate g = v y with y = rsqrt(v), corrected once by its
 // residual v - g^2, which the fused multiply-add gives (Markstein 1990).
@@ -469,10 +445,10 @@ __device__ __forceinline__ void step_quad(const AdamArgs& a, float coef, float k
         v[h] = fma2(mul2(mul2(dd, dd), b2), one, mul2(mul2(g, g), both(a.om_beta2)));
         r[h] = root2(v[h]);
     }
-    // zeros, tiny values, Inf and NaN wrap past the range
-    const uint32_t far = max(max(__float_as_uint(v[0].x) - kRootLo, __float_as_uint(v[0].y) - kRootLo),
-                             max(__float_as_uint(v[1].x) - kRootLo, __float_as_uint(v[1].y) - kRootLo));
-    const bool plain = far < kRootEnd - kRootLo;
+    // Zeros and tiny values take the exact function, as does Inf, whose
+    // corrected estimate is NaN (NaN stays NaN).
+    const bool plain = fminf(fminf(v[0].x, v[0].y), fminf(v[1].x, v[1].y)) >= kRootLo &&
+                       max_nan(max_nan(r[0].x, r[0].y, r[1].x), r[1].y, 0.f) < __int_as_float(0x7f800000);
     if (!plain) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -484,8 +460,9 @@ __device__ __forceinline__ void step_quad(const AdamArgs& a, float coef, float k
         const float2 up = mul2(m[h], make_float2(rcp_approx(denom.x), rcp_approx(denom.y)));
         q.th[h] = fma2(up, both(-a.step_size), mul2(q.th[h], both(keep)));
     }
-    const float mt = max_nan(max_nan(fabsf(m[0].x), fabsf(m[0].y)), max_nan(fabsf(m[1].x), fabsf(m[1].y)));
-    const float st = max_nan(max_nan(r[0].x, r[0].y), max_nan(r[1].x, r[1].y));
+    const float m3 = max_nan(fabsf(m[0].x), fabsf(m[0].y), fabsf(m[1].x));
+    const float s3 = max_nan(r[0].x, r[0].y, r[1].x);
+    const float mt = max_nan(m3, fabsf(m[1].y), 0.f), st = max_nan(s3, r[1].y, 0.f);
     mtop = __reduce_max_sync(kFull, __float_as_uint(mt));
     stop = __reduce_max_sync(kFull, __float_as_uint(st) & 0x7fffffffu);
     const float2 minv = both(block_inverse(mtop)), sinv = both(block_inverse(stop));
@@ -497,8 +474,11 @@ __device__ __forceinline__ void step_quad(const AdamArgs& a, float coef, float k
         sx[2 * h] = y.x, sx[2 * h + 1] = y.y;
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e)  // a positive root keeps at least the smallest code
-        sx[e] = plain || sx[e] > 0.f ? fmaxf(sx[e], 0x1p-9f) : sx[e];
+    for (int e = 0; e < 4; ++e) {  // a positive root keeps at least the smallest code
+        const float x = sx[e];
+        sx[e] = fmaxf(x, 0x1p-9f);
+        if (!plain && !(x > 0.f)) sx[e] = x;
+    }
     q.cm = encode4(mx, static_cast<uint32_t>(z));
     q.cs = encode4(sx, static_cast<uint32_t>(z >> 32));
 }
@@ -509,6 +489,7 @@ __device__ __forceinline__ void step_quad(const AdamArgs& a, float coef, float k
 // aligned groups of four elements ("quads") that a block touches: 32, or 33
 // when the block starts A = 1, 2 or 3 elements into its first quad.
 constexpr int kStages = 4;
+constexpr int64_t kMostRun = 32;  // slots of a warp
 
 template <typename G>
 struct __align__(16) Stage {
@@ -517,24 +498,6 @@ struct __align__(16) Stage {
     uint32_t cm[33], cs[33];
     float scale[2];
 };
-
-// Copies of up to BYTES (4, 8 or 16); the bytes past `valid` are not read.
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void* dst, const void* src, int valid = BYTES) {
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src),
-                     "r"(valid)
-                     : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_addr(dst)), "l"(src),
-                     "n"(BYTES), "r"(valid)
-                     : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 // the four elements from A on of two consecutive quads
 template <int A>
@@ -571,53 +534,59 @@ __device__ __forceinline__ void shifted(const Pack<__nv_bfloat16, 4>* q, float2 
 // not be written by anyone else.
 template <typename G, int A>
 __device__ __forceinline__ void run_blocks(const AdamArgs& a, const AdamJob& J, float coef, float keep,
-                                           int64_t begin, int64_t slot, int64_t count, int lane,
+                                           int64_t begin, int64_t slot, int count, int lane,
                                            Stage<G>* ring) {
     const int64_t q0 = begin - A + 4 * lane;  // this lane's quad of the first block
-    float* th = J.theta + q0;
-    const G* g = static_cast<const G*>(J.grad) + q0;
-    uint8_t* m8 = static_cast<uint8_t*>(J.m) + q0;
-    uint8_t* s8 = static_cast<uint8_t*>(J.v) + q0;
-    const float* sc = (lane == 0 ? J.m_scale : J.v_scale) + slot;
-    auto issue = [&](int64_t i) {
-        if (i < count) {
-            Stage<G>& st = ring[i % kStages];
-            const int64_t o = i * kBlock;
-            copy_async<16>(&st.th[lane], th + o);
-            copy_async<4 * sizeof(G)>(&st.gr[lane], g + o);
-            copy_async<4>(&st.cm[lane], m8 + o);
-            copy_async<4>(&st.cs[lane], s8 + o);
-            if (lane < 2) copy_async<4>(&st.scale[lane], sc + i);
-            if (A > 0 && lane == 0) {  // the block's last A elements
-                copy_async<16>(&st.th[32], th + o + kBlock, 4 * A);
-                copy_async<4 * sizeof(G)>(&st.gr[32], g + o + kBlock, sizeof(G) * A);
-                copy_async<4>(&st.cm[32], m8 + o + kBlock, A);
-                copy_async<4>(&st.cs[32], s8 + o + kBlock, A);
-            }
+    float* const th = J.theta + q0;
+    const G* const g = static_cast<const G*>(J.grad) + q0;
+    uint8_t* const m8 = static_cast<uint8_t*>(J.m) + q0;
+    uint8_t* const s8 = static_cast<uint8_t*>(J.v) + q0;
+    __nv_bfloat16* const copy = J.copy ? J.copy + q0 : nullptr;
+    float* const sc = (lane == 0 ? J.m_scale : J.v_scale) + slot;  // of lanes 0 and 1
+    auto issue = [&](int i, Stage<G>& st) {
+        const int o = i * kBlock;
+        copy_async<16>(&st.th[lane], th + o);
+        copy_async<4 * sizeof(G)>(&st.gr[lane], g + o);
+        copy_async<4>(&st.cm[lane], m8 + o);
+        copy_async<4>(&st.cs[lane], s8 + o);
+        if (lane < 2) copy_async<4>(&st.scale[lane], sc + i);
+        if (A > 0 && lane == 0) {  // the block's last A elements
+            copy_async<16>(&st.th[32], th + o + kBlock, 4 * A);
+            copy_async<4 * sizeof(G)>(&st.gr[32], g + o + kBlock, sizeof(G) * A);
+            copy_async<4>(&st.cm[32], m8 + o + kBlock, A);
+            copy_async<4>(&st.cs[32], s8 + o + kBlock, A);
         }
-        copy_commit();
     };
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(i);
+    for (int i = 0; i < kStages - 1; ++i) {
+        if (i < count) issue(i, ring[i]);
+        copy_commit();
+    }
     uint64_t counter = a.key + ((J.slot0 + slot) * (kBlock / 4) + lane) * kGolden;
     // what the previous block's last lane left of a quad (lane 0 only)
     float left[A + 1];
     uint32_t left_m = 0, left_s = 0;
-    for (int64_t i = 0; i < count; ++i, counter += (kBlock / 4) * kGolden) {
+    Stage<G>* st = ring;                     // the block's stage
+    Stage<G>* freed = ring + (kStages - 1);  // the one of the block before
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
         copy_wait<kStages - 2>();
-        __syncwarp();  // the stage has every lane's copies, and the last one every lane's reads
-        issue(i + kStages - 1);
-        const Stage<G>& st = ring[i % kStages];
+        __syncwarp();  // the stage has every lane's copies, and `freed` every lane's reads
+        if (i + kStages - 1 < count) issue(i + kStages - 1, *freed);
+        copy_commit();
         Quad q;
-        shifted<A>(&st.th[lane], q.th);
-        shifted<A>(&st.gr[lane], q.gr);
-        q.cm = A ? __funnelshift_r(st.cm[lane], st.cm[lane + 1], 8 * A) : st.cm[lane];
-        q.cs = A ? __funnelshift_r(st.cs[lane], st.cs[lane + 1], 8 * A) : st.cs[lane];
-        q.msc = st.scale[0], q.ssc = st.scale[1];
+        shifted<A>(&st->th[lane], q.th);
+        shifted<A>(&st->gr[lane], q.gr);
+        q.cm = A ? __funnelshift_r(st->cm[lane], st->cm[lane + 1], 8 * A) : st->cm[lane];
+        q.cs = A ? __funnelshift_r(st->cs[lane], st->cs[lane + 1], 8 * A) : st->cs[lane];
+        q.msc = st->scale[0], q.ssc = st->scale[1];
+        freed = st;
+        st = st == ring + (kStages - 1) ? ring : st + 1;
         uint32_t mtop, stop;
         step_quad(a, coef, keep, mix64(counter), q, mtop, stop);
+        counter += (kBlock / 4) * kGolden;
         float out[4] = {q.th[0].x, q.th[0].y, q.th[1].x, q.th[1].y};
-        const int64_t o = i * kBlock;
+        const int o = i * kBlock;
         bool whole = true;
         if constexpr (A > 0) {
             // quads as they lie in memory: the lane before gives the first A elements
@@ -641,29 +610,26 @@ __device__ __forceinline__ void run_blocks(const AdamArgs& a, const AdamJob& J, 
             store4(th + o, out);
             *reinterpret_cast<uint32_t*>(m8 + o) = q.cm;
             *reinterpret_cast<uint32_t*>(s8 + o) = q.cs;
-            if (J.copy) store4(J.copy + q0 + o, out);
+            if (copy) store4(copy + o, out);
         } else {
 #pragma unroll
             for (int k = A; k < 4; ++k) {
                 th[o + k] = out[k];
                 m8[o + k] = static_cast<uint8_t>(q.cm >> (8 * k));
                 s8[o + k] = static_cast<uint8_t>(q.cs >> (8 * k));
-                if (J.copy) J.copy[q0 + o + k] = __float2bfloat16_rn(out[k]);
+                if (copy) copy[o + k] = __float2bfloat16_rn(out[k]);
             }
         }
-        if (lane == 0) {
-            J.m_scale[slot + i] = block_scale(mtop);
-            J.v_scale[slot + i] = block_scale(stop);
-        }
+        if (lane < 2) sc[i] = block_scale(lane ? stop : mtop);
     }
     if (A > 0 && lane == 0) {
-        const int64_t o = count * kBlock;
+        const int o = count * kBlock;
 #pragma unroll
         for (int k = 0; k < A; ++k) {
             th[o + k] = left[k];
             m8[o + k] = static_cast<uint8_t>(left_m >> (8 * (4 - A + k)));
             s8[o + k] = static_cast<uint8_t>(left_s >> (8 * (4 - A + k)));
-            if (J.copy) J.copy[q0 + o + k] = __float2bfloat16_rn(left[k]);
+            if (copy) copy[o + k] = __float2bfloat16_rn(left[k]);
         }
     }
     copy_wait<0>();
@@ -742,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_adamw8(const __grid_constant__ 
                 continue;
             }
             const float keep = keep_of(a, J, c.t);
-            const int64_t count = min(end - s, (c.o1 - begin) / kBlock);
+            const int count = static_cast<int>(min(min(end - s, (c.o1 - begin) / kBlock), int64_t(1) << 20));
             const int shift = static_cast<int>(begin & 3);
             if (count > 0 && (shift == 0 || own)) {
                 switch (shift) {
@@ -760,8 +726,6 @@ __global__ void __launch_bounds__(kThreads, 4) k_adamw8(const __grid_constant__ 
         }
     }
 }
-
-bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 }  // namespace
 }  // namespace dl
@@ -898,11 +862,13 @@ extern "C" int dl_adamw_step(const dl_adamw_job* jobs, int32_t n_jobs, int32_t g
         int64_t grid = work;
         if (by8) {  // as many warps as the GPU holds, each with one run of slots
             smem = kWarps * kStages * (grad_type == DL_F32 ? sizeof(Stage<float>) : sizeof(Stage<__nv_bfloat16>));
-            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     static_cast<int>(smem)) != cudaSuccess)
-                return DL_ERR_CUDA;
+            if (!allow_shared(kernel, smem)) return DL_ERR_CUDA;
             grid = grid_for(kernel, kThreads, smem, (work + kWarps - 1) / kWarps);
             a.run = (work + grid * kWarps - 1) / (grid * kWarps);
+            if (a.run > kMostRun) {
+                a.run = kMostRun;
+                grid = (work + kWarps * a.run - 1) / (kWarps * a.run);
+            }
         }
         if (grid > INT32_MAX) return DL_ERR_ARG;
         void* args[] = {&a};

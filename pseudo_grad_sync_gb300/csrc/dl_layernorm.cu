@@ -1,168 +1,204 @@
-// Layer norm (centred or RMS) forward and backward.
+// Layer norm (centred or RMS) forward.
 #include <float.h>
 #include <math.h>
 #include <stdint.h>
 
-#include "dl_types.cuh"
+#include "dl_norm.cuh"
 
 namespace dl {
 namespace {
 
-__device__ __forceinline__ float load_param(const void* p, int32_t type, int64_t i) {
-    return type == DL_F32 ? static_cast<const float*>(p)[i]
-                          : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
-
-__device__ __forceinline__ float block_sum(float v, float* red) {
-    for (int sh = 16; sh; sh >>= 1) v += __shfl_xor_sync(kFull, v, sh);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float s = 0.f;
-    for (int w = 0; w < kWarps; ++w) s += red[w];
-    return s;
-}
-
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
-    k_norm_fwd(const T* x, int64_t xs, int64_t rows, int width, const void* weight,
-               const void* bias, int32_t ptype, float eps, bool rms, T* y, int64_t ys, float* mean,
-               float* rstd) {
-    __shared__ float red[kWarps];
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        const T* xr = x + r * xs;
+struct FwdArgs {
+    const T* x;
+    T* y;
+    const void* weight;
+    const void* bias;
+    float* mean;
+    float* rstd;
+    int64_t xs, ys, rows;
+    int width;
+    int32_t ptype;
+    float eps;
+    bool rms, vec_out;
+};
+
+// Rows in flight per thread; its ring holds one more, the one being read.
+// Threads of 32 fp32 elements take one: three would need 256 KB.
+template <typename T, int EPT>
+constexpr int kRowsAhead = EPT * sizeof(T) > 64 ? 1 : 3;
+
+template <typename T, int N, int TPR, int VPT, int BLOCK>
+__global__ void __launch_bounds__(BLOCK) k_norm_fwd(const __grid_constant__ FwdArgs<T> a) {
+    constexpr bool kAsync = N * sizeof(T) >= 4;
+    constexpr int kAhead = kRowsAhead<T, VPT * N>, kRing = kAhead + 1;
+    constexpr int kRowsAtOnce = BLOCK / TPR;
+    extern __shared__ __align__(16) unsigned char smem[];
+    using P = Pack<T, N>;
+    RowSum<TPR, BLOCK> sum{reinterpret_cast<float2*>(smem)};
+    P* ring = reinterpret_cast<P*>(smem + RowSum<TPR, BLOCK>::kBytes);
+    const int t = threadIdx.x % TPR;
+    const int64_t step = int64_t(gridDim.x) * kRowsAtOnce;
+    const int64_t r0 = int64_t(blockIdx.x) * kRowsAtOnce;  // of the block
+    const int64_t mine = r0 + threadIdx.x / TPR;
+    auto issue = [&](int64_t r, int stage) {
+        if (r < a.rows) {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int c = (k * TPR + t) * N;
+                if (c < a.width)
+                    copy_async<N * sizeof(T)>(ring + (stage * VPT + k) * BLOCK + threadIdx.x,
+                                              a.x + r * a.xs + c,
+                                              static_cast<int>(min(N, a.width - c) * sizeof(T)));
+            }
+        }
+        copy_commit();
+    };
+    if constexpr (kAsync) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) issue(mine + i * step, i);
+    }
+    float w[VPT * N], b[VPT * N];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int c = (k * TPR + t) * N + i;
+            w[k * N + i] = c < a.width ? load_param(a.weight, a.ptype, c) : 0.f;
+            b[k * N + i] = c < a.width && a.bias ? load_param(a.bias, a.ptype, c) : 0.f;
+        }
+    const float width = static_cast<float>(a.width);
+    int stage = 0;
+    for (int64_t first = r0; first < a.rows; first += step) {
+        const int64_t r = first + threadIdx.x / TPR;
+        float x[VPT * N];
+        if constexpr (kAsync) {
+            copy_wait<kAhead - 1>();
+            // the slot read in the round before this one
+            issue(r + kAhead * step, (stage + kAhead) % kRing);
+        }
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int c = (k * TPR + t) * N;
+            float v[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = 0.f;
+            if (r < a.rows && c < a.width) {
+                if constexpr (kAsync)
+                    unpack<T, N>(ring[(stage * VPT + k) * BLOCK + threadIdx.x], v);
+                else
+                    v[0] = to_f32(a.x[r * a.xs + c]);
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[k * N + i] = v[i];
+        }
+        stage = (stage + 1) % kRing;
         float mu = 0.f;
-        if (!rms) {
+        if (!a.rms) {
             float s = 0.f;
-            for (int c = threadIdx.x; c < width; c += kThreads) s += to_f32(xr[c]);
-            mu = block_sum(s, red) / width;
+#pragma unroll
+            for (int i = 0; i < VPT * N; ++i) s += x[i];
+            mu = sum(s) / width;
         }
         float q = 0.f;
-        for (int c = threadIdx.x; c < width; c += kThreads) {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const bool in = (k * TPR + t) * N + i < a.width;
+                const float d = in ? x[k * N + i] - mu : 0.f;
+                x[k * N + i] = d;
+                q = fmaf(d, d, q);
+            }
+        const float rs = rsqrtf(sum(q) / width + a.eps);
+        if (r < a.rows) {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int c = (k * TPR + t) * N;
+                float v[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] = fmaf(x[k * N + i] * rs, w[k * N + i], b[k * N + i]);
+                if (c < a.width) store_pack<T, N>(a.y + r * a.ys + c, v, a.width - c, a.vec_out);
+            }
+            if (t == 0) {
+                if (!a.rms) a.mean[r] = mu;
+                a.rstd[r] = rs;
+            }
+        }
+    }
+}
+
+// Rows too wide for a block's registers: the row is read three times (from
+// L2 after the first).
+template <typename T>
+__global__ void __launch_bounds__(1024) k_norm_fwd_wide(const __grid_constant__ FwdArgs<T> a) {
+    __shared__ float2 red[2 * 32];
+    RowSum<1024, 1024> sum{red};
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        const T* xr = a.x + r * a.xs;
+        float mu = 0.f;
+        if (!a.rms) {
+            float s = 0.f;
+            for (int c = threadIdx.x; c < a.width; c += 1024) s += to_f32(xr[c]);
+            mu = sum(s) / a.width;
+        }
+        float q = 0.f;
+        for (int c = threadIdx.x; c < a.width; c += 1024) {
             const float d = to_f32(xr[c]) - mu;
             q = fmaf(d, d, q);
         }
-        const float rs = 1.0f / sqrtf(block_sum(q, red) / width + eps);
-        for (int c = threadIdx.x; c < width; c += kThreads) {
-            const float h = (to_f32(xr[c]) - mu) * rs * load_param(weight, ptype, c);
-            y[r * ys + c] = from_f32<T>(bias ? h + load_param(bias, ptype, c) : h);
+        const float rs = rsqrtf(sum(q) / a.width + a.eps);
+        for (int c = threadIdx.x; c < a.width; c += 1024) {
+            const float h = (to_f32(xr[c]) - mu) * rs * load_param(a.weight, a.ptype, c);
+            a.y[r * a.ys + c] = from_f32<T>(a.bias ? h + load_param(a.bias, a.ptype, c) : h);
         }
         if (threadIdx.x == 0) {
-            if (!rms) mean[r] = mu;
-            rstd[r] = rs;
+            if (!a.rms) a.mean[r] = mu;
+            a.rstd[r] = rs;
         }
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-    k_norm_dx(const T* dy, int64_t ds, const T* x, int64_t xs, int64_t rows, int width,
-              const void* weight, int32_t ptype, const float* mean, const float* rstd, bool rms,
-              T* dx, int64_t os) {
-    __shared__ float red[kWarps];
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        const float mu = rms ? 0.f : mean[r], rs = rstd[r];
-        float s = 0.f, q = 0.f;
-        for (int c = threadIdx.x; c < width; c += kThreads) {
-            const float w = to_f32(dy[r * ds + c]) * load_param(weight, ptype, c);
-            s += w;
-            q = fmaf(w, (to_f32(x[r * xs + c]) - mu) * rs, q);
-        }
-        s = rms ? 0.f : block_sum(s, red) / width;
-        q = block_sum(q, red) / width;
-        for (int c = threadIdx.x; c < width; c += kThreads) {
-            const float w = to_f32(dy[r * ds + c]) * load_param(weight, ptype, c);
-            const float h = (to_f32(x[r * xs + c]) - mu) * rs;
-            dx[r * os + c] = from_f32<T>((w - s - h * q) * rs);
-        }
-    }
+template <typename T, int N, int TPR, int VPT, int BLOCK>
+int launch(const FwdArgs<T>& a, cudaStream_t s) {
+    const void* kernel = reinterpret_cast<const void*>(k_norm_fwd<T, N, TPR, VPT, BLOCK>);
+    const size_t smem = RowSum<TPR, BLOCK>::kBytes +
+                        (N * sizeof(T) >= 4 ? size_t(kRowsAhead<T, VPT * N> + 1) * VPT * BLOCK * N * sizeof(T) : 0);
+    if (!allow_shared(kernel, smem)) return DL_ERR_CUDA;
+    constexpr int at_once = BLOCK / TPR;
+    const int grid = grid_for(kernel, BLOCK, smem, (a.rows + at_once - 1) / at_once);
+    k_norm_fwd<T, N, TPR, VPT, BLOCK><<<grid, BLOCK, smem, s>>>(a);
+    return launch_status();
 }
 
-// Sums over rows: block (strip of 32 columns, part of the rows); warp w takes
-// every eighth row of the part; partial sums go to the workspace.
-constexpr int kParts = 32;
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-    k_norm_dw(const T* dy, int64_t ds, const T* x, int64_t xs, int64_t rows, int width,
-              const float* mean, const float* rstd, bool rms, float* part) {
-    __shared__ float sw[kWarps][32], sb[kWarps][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;
-    const int64_t r0 = rows * blockIdx.y / kParts, r1 = rows * (blockIdx.y + 1) / kParts;
-    float w = 0.f, b = 0.f;
-    if (c < width)
-        for (int64_t r = r0 + warp; r < r1; r += kWarps) {
-            const float g = to_f32(dy[r * ds + c]);
-            const float h = (to_f32(x[r * xs + c]) - (rms ? 0.f : mean[r])) * rstd[r];
-            w = fmaf(g, h, w);
-            b += g;
-        }
-    sw[warp][lane] = w;
-    sb[warp][lane] = b;
-    __syncthreads();
-    if (warp == 0 && c < width) {
-        for (int k = 1; k < kWarps; ++k) w += sw[k][lane], b += sb[k][lane];
-        part[(2 * blockIdx.y) * int64_t(width) + c] = w;
-        part[(2 * blockIdx.y + 1) * int64_t(width) + c] = b;
-    }
-}
-
-__global__ void __launch_bounds__(kThreads)
-    k_norm_join(const float* part, int width, int32_t ptype, bool accumulate, void* dw, void* db) {
-    const int c = blockIdx.x * kThreads + threadIdx.x;
-    if (c >= width) return;
-    for (int k = 0; k < (db ? 2 : 1); ++k) {
-        float s = 0.f;
-        for (int p = 0; p < kParts; ++p) s += part[(2 * p + k) * int64_t(width) + c];
-        void* out = k ? db : dw;
-        if (accumulate) s += load_param(out, ptype, c);
-        if (ptype == DL_F32)
-            static_cast<float*>(out)[c] = s;
-        else
-            static_cast<__nv_bfloat16*>(out)[c] = __float2bfloat16_rn(s);
-    }
-}
-
-bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-int grid_rows(int64_t rows) {
-    const int64_t most = int64_t(sm_count()) * 8;
-    return static_cast<int>(rows < most ? rows : most);
+// 16 elements per thread up to 8192 columns, 32 above.
+template <typename T, int N>
+int by_width(const FwdArgs<T>& a, cudaStream_t s) {
+    if (a.width <= 128) return launch<T, N, 8, 16 / N, 256>(a, s);
+    if (a.width <= 512) return launch<T, N, 32, 16 / N, 256>(a, s);
+    if (a.width <= 1024) return launch<T, N, 64, 16 / N, 256>(a, s);
+    if (a.width <= 2048) return launch<T, N, 128, 16 / N, 256>(a, s);
+    if (a.width <= 4096) return launch<T, N, 256, 16 / N, 256>(a, s);
+    if (a.width <= 8192) return launch<T, N, 512, 16 / N, 512>(a, s);
+    if (a.width <= 16384) return launch<T, N, 512, 32 / N, 512>(a, s);
+    const int64_t most = int64_t(sm_count()) * 2;
+    k_norm_fwd_wide<T><<<static_cast<int>(a.rows < most ? a.rows : most), 1024, 0, s>>>(a);
+    return launch_status();
 }
 
 template <typename T>
 int forward(const void* x, int64_t xs, int64_t rows, int width, const void* w, const void* b,
             int32_t pt, float eps, bool rms, void* y, int64_t ys, float* mean, float* rstd,
             cudaStream_t s) {
-    k_norm_fwd<T><<<grid_rows(rows), kThreads, 0, s>>>(static_cast<const T*>(x), xs, rows, width, w,
-                                                       b, pt, eps, rms, static_cast<T*>(y), ys, mean,
-                                                       rstd);
-    return launch_status();
+    FwdArgs<T> a{static_cast<const T*>(x), static_cast<T*>(y), w, b, mean, rstd, xs, ys, rows, width,
+                 pt, eps, rms, false};
+    a.vec_out = aligned16(y) && ys * sizeof(T) % 16 == 0;
+    if (aligned16(x) && xs * sizeof(T) % 16 == 0) return by_width<T, 16 / sizeof(T)>(a, s);
+    return by_width<T, 1>(a, s);
 }
-
-template <typename T>
-int backward(const void* dy, int64_t ds, const void* x, int64_t xs, int64_t rows, int width,
-             const void* w, int32_t pt, const float* mean, const float* rstd, bool rms,
-             bool accumulate, void* dx, int64_t os, void* dw, void* db, float* part,
-             cudaStream_t s) {
-    const T* dyt = static_cast<const T*>(dy);
-    const T* xt = static_cast<const T*>(x);
-    // the sums first: dx may overwrite dy
-    k_norm_dw<T><<<dim3((width + 31) / 32, kParts), kThreads, 0, s>>>(dyt, ds, xt, xs, rows, width,
-                                                                      mean, rstd, rms, part);
-    if (rows > 0)
-        k_norm_dx<T><<<grid_rows(rows), kThreads, 0, s>>>(dyt, ds, xt, xs, rows, width, w, pt, mean,
-                                                          rstd, rms, static_cast<T*>(dx), os);
-    k_norm_join<<<(width + kThreads - 1) / kThreads, kThreads, 0, s>>>(part, width, pt, accumulate,
-                                                                       dw, db);
-    return launch_status();
-}
-
-bool activation_type(int32_t t) { return t == DL_F32 || t == DL_BF16 || t == DL_F16; }
-bool param_type_ok(int32_t t) { return t == DL_F32 || t == DL_BF16; }
 
 }  // namespace
+
 }  // namespace dl
 
 using namespace dl;
@@ -171,7 +207,8 @@ extern "C" int dl_layernorm_forward(const void* x, int64_t x_stride, int32_t x_t
                                     int32_t width, const void* weight, const void* bias,
                                     int32_t param_type, double eps, int32_t flags, void* y,
                                     int64_t y_stride, float* mean, float* rstd, void* stream) {
-    if (!activation_type(x_type) || !param_type_ok(param_type) || rows < 0 || width < 1 ||
+    if ((x_type != DL_F32 && x_type != DL_BF16 && x_type != DL_F16) ||
+        (param_type != DL_F32 && param_type != DL_BF16) || rows < 0 || width < 1 ||
         x_stride < width || y_stride < width || !(eps >= 0.0 && eps <= FLT_MAX) ||
         (flags & ~DL_NORM_RMS))
         return DL_ERR_ARG;
@@ -194,47 +231,5 @@ extern "C" int dl_layernorm_forward(const void* x, int64_t x_stride, int32_t x_t
         default:
             return forward<__half>(x, x_stride, rows, width, weight, bias, param_type, e, rms, y,
                                    y_stride, mean, rstd, s);
-    }
-}
-
-extern "C" size_t dl_layernorm_workspace_bytes(int64_t rows, int32_t width) {
-    if (rows < 0 || width < 1) return 0;
-    return align256(kWsHeader + size_t(2) * kParts * static_cast<size_t>(width) * sizeof(float));
-}
-
-extern "C" int dl_layernorm_backward(const void* dy, int64_t dy_stride, const void* x,
-                                     int64_t x_stride, int32_t x_type, int64_t rows, int32_t width,
-                                     const void* weight, int32_t param_type, const float* mean,
-                                     const float* rstd, int32_t flags, void* dx, int64_t dx_stride,
-                                     void* dweight, void* dbias, void* d_workspace,
-                                     size_t workspace_bytes, void* stream) {
-    if (!activation_type(x_type) || !param_type_ok(param_type) || rows < 0 || width < 1 ||
-        dy_stride < width || x_stride < width || dx_stride < width ||
-        (flags & ~(DL_NORM_RMS | DL_NORM_ACCUMULATE)) || !dweight)
-        return DL_ERR_ARG;
-    const bool rms = flags & DL_NORM_RMS;
-    if (rows > 0 && (!dy || !x || !dx || !weight || !rstd || (!rms && !mean))) return DL_ERR_ARG;
-    const size_t xa = type_size(x_type), pa = type_size(param_type);
-    if (!aligned_to(dy, xa) || !aligned_to(x, xa) || !aligned_to(dx, xa) || !aligned_to(weight, pa) ||
-        !aligned_to(dweight, pa) || !aligned_to(dbias, pa) || (!rms && !aligned_to(mean, 4)) ||
-        !aligned_to(rstd, 4))
-        return DL_ERR_ALIGN;
-    if (!d_workspace || workspace_bytes < dl_layernorm_workspace_bytes(rows, width))
-        return DL_ERR_WORKSPACE;
-    if (!aligned_to(d_workspace, 256)) return DL_ERR_ALIGN;
-    const bool acc = flags & DL_NORM_ACCUMULATE;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    float* part = reinterpret_cast<float*>(static_cast<char*>(d_workspace) + kWsHeader);
-    switch (x_type) {
-        case DL_F32:
-            return backward<float>(dy, dy_stride, x, x_stride, rows, width, weight, param_type, mean,
-                                   rstd, rms, acc, dx, dx_stride, dweight, dbias, part, s);
-        case DL_BF16:
-            return backward<__nv_bfloat16>(dy, dy_stride, x, x_stride, rows, width, weight,
-                                           param_type, mean, rstd, rms, acc, dx, dx_stride, dweight,
-                                           dbias, part, s);
-        default:
-            return backward<__half>(dy, dy_stride, x, x_stride, rows, width, weight, param_type,
-                                    mean, rstd, rms, acc, dx, dx_stride, dweight, dbias, part, s);
     }
 }

@@ -32,4 +32,67 @@ struct __align__(sizeof(T) * N) Pack {
     T v[N];
 };
 
+// Asynchronous copies of BYTES (4, 8 or 16) from global to shared memory; the
+// bytes past `valid` are not read and become zeros.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, int valid = BYTES) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src),
+                     "r"(valid)
+                     : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_addr(dst)), "l"(src),
+                     "n"(BYTES), "r"(valid)
+                     : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// until at most N of this thread's groups are in flight
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Two products, sums or fused products at once, each rounded.
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ uint64_t bits2(float2 v) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+    return r;
+}
+__device__ __forceinline__ float2 floats2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(x)), "l"(bits2(y)));
+    return floats2(r);
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(x)), "l"(bits2(y)));
+    return floats2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(x)), "l"(bits2(y)), "l"(bits2(z)));
+    return floats2(r);
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory; false (and no error
+// left behind for a later call) when the device refuses.
+inline bool allow_shared(const void* kernel, size_t bytes) {
+    if (bytes <= 48 * 1024 || cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(bytes)) == cudaSuccess)
+        return true;
+    cudaGetLastError();
+    return false;
+}
+
+// p is a multiple of a (a power of two); null is
+inline bool aligned_to(const void* p, size_t a) {
+    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
 }  // namespace dl
