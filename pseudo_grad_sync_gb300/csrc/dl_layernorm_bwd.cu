@@ -20,47 +20,105 @@ struct BwdArgs {
     const float* mean;
     const float* rstd;
     float* part;  // [blocks][2][width]
+    uint32_t* status;
     int64_t ds, xs, os, rows;
+    int64_t run;  // rows of a block
     int width;
     int32_t ptype;
     bool rms, vec_out;
 };
 
-template <typename T, int N, int TPR, int VPT, int BLOCK, int AHEAD>
+constexpr int kStatRows = 512;  // rows whose mean and rstd a block holds at a time
+
+// How rows come in. Bulk copies of whole rows (rows of more than a warp, 16-byte
+// aligned) are issued by one thread into stages that the whole block reads;
+// otherwise every thread copies, or loads, what it works on itself.
+template <typename T, int N, int TPR, int EPT, int BLOCK>
+struct BwdGeometry {
+    static constexpr int kVecs = EPT / N, kGroups = BLOCK / TPR;
+    static constexpr bool kBulk = TPR > 32 && N > 1;
+    static constexpr bool kAsync = !kBulk && N * sizeof(T) >= 4;
+    static constexpr int kStages = kBulk || kAsync ? (sizeof(T) == 4 ? 3 : 4) : 0;
+    static constexpr size_t kStage = size_t(2) * BLOCK * EPT * sizeof(T);  // dy and x of a round
+    static constexpr size_t kRing = kStages * kStage;
+    static constexpr size_t kSums = kGroups > 1 ? size_t(BLOCK) * EPT * 2 * sizeof(float) : 0;
+    static constexpr size_t kFixed = 128 + kStatRows * sizeof(float2) + RowSum<TPR, BLOCK>::kBytes;
+    static constexpr size_t kBytes = kFixed + (kRing > kSums ? kRing : kSums);
+};
+
+// A block takes a run of consecutive rows, in rounds of one row per group of
+// TPR threads: the row's terms of its two sums and of the thread's columns'
+// sums, the exchange of the row sums (one barrier), then dx from the packs,
+// still in registers. The ring's other stages are in flight meanwhile.
+template <typename T, int N, int TPR, int EPT, int BLOCK>
 __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdArgs<T> a) {
-    constexpr bool kAsync = N * sizeof(T) >= 4;
-    constexpr int kRing = AHEAD + 1;
-    constexpr int kRowsAtOnce = BLOCK / TPR;
-    // Elements are handled in pairs: of one pack, or for single elements of
-    // two neighbouring packs of the thread.
-    constexpr int kPairs = VPT * N / 2;
-    extern __shared__ __align__(16) unsigned char smem[];
+    using Geo = BwdGeometry<T, N, TPR, EPT, BLOCK>;
+    constexpr int VPT = Geo::kVecs, kGroups = Geo::kGroups, kStages = Geo::kStages;
+    constexpr int kPairs = EPT / 2;
+    extern __shared__ __align__(128) unsigned char smem[];
     using P = Pack<T, N>;
-    RowSum<TPR, BLOCK> sum{reinterpret_cast<float2*>(smem)};
-    P* ring = reinterpret_cast<P*>(smem + RowSum<TPR, BLOCK>::kBytes);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem);
+    float2* stats = reinterpret_cast<float2*>(smem + 128);
+    RowSum<TPR, BLOCK> sum{stats + kStatRows};
+    unsigned char* ring = smem + Geo::kFixed;
     const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
-    const int64_t step = int64_t(gridDim.x) * kRowsAtOnce;
-    const int64_t r0 = int64_t(blockIdx.x) * kRowsAtOnce;
+    const int64_t begin = a.run * blockIdx.x, end = min(a.rows, begin + a.run);
     auto column = [&](int k) { return (k * TPR + t) * N; };
-    auto issue = [&](int64_t r, int stage) {
-        if (r < a.rows) {
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int c = column(k);
-                if (c < a.width) {
-                    const int valid = static_cast<int>(min(N, a.width - c) * sizeof(T));
-                    P* to = ring + (stage * 2 * VPT + k) * BLOCK + threadIdx.x;
-                    copy_async<N * sizeof(T)>(to, a.dy + r * a.ds + c, valid);
-                    copy_async<N * sizeof(T)>(to + VPT * BLOCK, a.x + r * a.xs + c, valid);
+    // this thread's pack k of array `which` in a stage
+    auto slot = [&](int stage, int which, int k) {
+        if constexpr (Geo::kBulk)
+            return reinterpret_cast<P*>(ring + stage * Geo::kStage) + ((group * 2 + which) * VPT + k) * TPR + t;
+        else
+            return reinterpret_cast<P*>(ring + stage * Geo::kStage) + (which * VPT + k) * BLOCK + threadIdx.x;
+    };
+    // bytes of a row that a bulk copy takes; the owner of a last, partial
+    // pack copies that one itself
+    const uint32_t row_bytes = static_cast<uint32_t>(a.width * sizeof(T)) & ~15u;
+    const bool tail = Geo::kBulk && a.width % N != 0 && [&] {
+        const int c = a.width / N * N;
+        return t == (c / N) % TPR;
+    }();
+    auto issue = [&](int64_t first, int stage) {  // the rows of the round from `first` on
+        if constexpr (Geo::kBulk) {
+            if (threadIdx.x == 0) {
+                const int64_t left = end - first;
+                const int n = left <= 0 ? 0 : left < kGroups ? static_cast<int>(left) : kGroups;
+                if (n > 0) {
+                    fence_proxy_async();
+                    mbar_arrive_expect_tx(full + stage, 2u * n * row_bytes);
+                    if (row_bytes)
+                        for (int j = 0; j < n; ++j) {
+                            unsigned char* to = ring + stage * Geo::kStage + j * 2 * (TPR * EPT * sizeof(T));
+                            bulk_copy_g2s(to, a.dy + (first + j) * a.ds, row_bytes, full + stage);
+                            bulk_copy_g2s(to + TPR * EPT * sizeof(T), a.x + (first + j) * a.xs, row_bytes, full + stage);
+                        }
                 }
             }
-        }
-        copy_commit();
-    };
-    if constexpr (kAsync) {
+        } else if constexpr (Geo::kAsync) {
+            const int64_t r = first + group;
+            if (r < end) {
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) issue(r0 + group + i * step, i);
+                for (int k = 0; k < VPT; ++k) {
+                    const int c = column(k);
+                    if (c < a.width) {
+                        const int valid = static_cast<int>(min(N, a.width - c) * sizeof(T));
+                        copy_async<N * sizeof(T)>(slot(stage, 0, k), a.dy + r * a.ds + c, valid);
+                        copy_async<N * sizeof(T)>(slot(stage, 1, k), a.x + r * a.xs + c, valid);
+                    }
+                }
+            }
+            copy_commit();
+        }
+    };
+    if constexpr (Geo::kBulk) {
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < kStages; ++i) mbar_init(full + i, 1);
+            fence_barrier_init();
+        }
+        __syncthreads();
     }
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(begin + i * kGroups, i);
     float2 w[kPairs], dw[kPairs], db[kPairs];
 #pragma unroll
     for (int p = 0; p < kPairs; ++p) {
@@ -73,86 +131,97 @@ __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdA
         w[p] = make_float2(f[0], f[1]);
         dw[p] = db[p] = make_float2(0.f, 0.f);
     }
-    const float width = static_cast<float>(a.width);
-    int64_t r = r0 + group;
-    float mu = 0.f, rs = 0.f;
-    if (r < a.rows) {
-        if (!a.rms) mu = __ldg(a.mean + r);
-        rs = __ldg(a.rstd + r);
-    }
-    int stage = 0;
-    for (int64_t first = r0; first < a.rows; first += step, r += step) {
-        const bool in = r < a.rows;
-        float mu_next = 0.f, rs_next = 0.f;
-        if (r + step < a.rows) {
-            if (!a.rms) mu_next = __ldg(a.mean + r + step);
-            rs_next = __ldg(a.rstd + r + step);
+    const bool whole = a.vec_out && column(VPT - 1) + N <= a.width;
+    const float inv = 1.0f / static_cast<float>(a.width);
+    bool ok = true;
+    int stage = 0, set = 0, at = kStatRows;
+    uint32_t parity = 0;
+    for (int64_t first = begin; first < end; first += kGroups, at += kGroups) {
+        const int64_t r = first + group;
+        const bool in = r < end;
+        if (at == kStatRows) {  // the next rows' statistics
+            __syncthreads();
+            for (int i = threadIdx.x; i < kStatRows && first + i < end; i += BLOCK)
+                stats[i] = make_float2(a.rms ? 0.f : __ldg(a.mean + first + i), __ldg(a.rstd + first + i));
+            __syncthreads();
+            at = 0;
         }
+        // the round's packs and statistics; zeros past the width and the rows
         P dyp[VPT], xp[VPT];
-        if constexpr (kAsync) {
-            copy_wait<AHEAD - 1>();
-            issue(r + AHEAD * step, (stage + AHEAD) % kRing);  // the slot read one round ago
+        const float2 st = stats[at + group];
+        const float mu = in ? st.x : 0.f, rs = in ? st.y : 0.f;
+        if constexpr (Geo::kBulk) {
+            if (ok && !mbar_wait_bounded(full + stage, parity)) {
+                ok = false;  // no wait and no copy after this; the status word says so
+                atomicOr(a.status, kDevErrCopyTimeout);
+            }
+        } else if constexpr (Geo::kAsync) {
+            copy_wait<kStages - 2>();
+            issue(first + (kStages - 1) * kGroups, stage == 0 ? kStages - 1 : stage - 1);  // read one round ago
         }
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const bool there = in && column(k) < a.width;
-            if constexpr (kAsync) {
-                const P* from = ring + (stage * 2 * VPT + k) * BLOCK + threadIdx.x;
-                if (there) dyp[k] = from[0], xp[k] = from[VPT * BLOCK];
+            const int c = column(k);
+            const bool there = in && c < a.width;
+            if constexpr (kStages > 0) {
+                if (there) dyp[k] = *slot(stage, 0, k), xp[k] = *slot(stage, 1, k);
+                if (Geo::kBulk && tail && there && c + N > a.width) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const bool el = c + i < a.width;
+                        dyp[k].v[i] = el ? a.dy[r * a.ds + c + i] : from_f32<T>(0.f);
+                        xp[k].v[i] = el ? a.x[r * a.xs + c + i] : from_f32<T>(0.f);
+                    }
+                }
             } else {
-                if (there) dyp[k].v[0] = a.dy[r * a.ds + column(k)], xp[k].v[0] = a.x[r * a.xs + column(k)];
+                if (there) dyp[k].v[0] = a.dy[r * a.ds + c], xp[k].v[0] = a.x[r * a.xs + c];
             }
             if (!there) {
 #pragma unroll
                 for (int i = 0; i < N; ++i) dyp[k].v[i] = xp[k].v[i] = from_f32<T>(0.f);
             }
         }
-        stage = stage + 1 == kRing ? 0 : stage + 1;
-        // xhat and dy of pair p (columns past the width: dy and the weight are zero)
-        auto pair = [&](const P* q, int p) {
-            if constexpr (N == 1) {
-                return make_float2(to_f32(q[2 * p].v[0]), to_f32(q[2 * p + 1].v[0]));
-            } else {
-                constexpr int H = N / 2;
-                return make_float2(to_f32(q[p / H].v[2 * (p % H)]), to_f32(q[p / H].v[2 * (p % H) + 1]));
-            }
-        };
         float2 s2 = make_float2(0.f, 0.f), q2 = s2;
 #pragma unroll
         for (int p = 0; p < kPairs; ++p) {
-            const float2 g = pair(dyp, p);
-            const float2 h = mul2(add2(pair(xp, p), both(-mu)), both(rs));
+            const float2 g = pair_of<T, N>(dyp, p);
+            const float2 h = mul2(add2(pair_of<T, N>(xp, p), both(-mu)), both(rs));
             const float2 wg = mul2(g, w[p]);
             s2 = add2(s2, wg);
             q2 = fma2(wg, h, q2);
             dw[p] = fma2(g, h, dw[p]);
             db[p] = add2(db[p], g);
         }
-        const float2 total = sum(make_float2(s2.x + s2.y, q2.x + q2.y));
-        const float2 s = both(a.rms ? 0.f : -(total.x / width)), q = both(-(total.y / width));
-        if (in) {
-            float out[VPT * N];
-#pragma unroll
-            for (int p = 0; p < kPairs; ++p) {
-                const float2 wg = mul2(pair(dyp, p), w[p]);
-                const float2 h = mul2(add2(pair(xp, p), both(-mu)), both(rs));
-                const float2 d = mul2(fma2(h, q, add2(wg, s)), both(rs));
-                out[2 * p] = d.x, out[2 * p + 1] = d.y;
-            }
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                float v[N];
-#pragma unroll
-                for (int i = 0; i < N; ++i) v[i] = out[k * N + i];
-                const int c = column(k);
-                if (c < a.width) store_pack<T, N>(a.dx + r * a.os + c, v, a.width - c, a.vec_out);
-            }
+        sum.give(make_float2(s2.x + s2.y, q2.x + q2.y), set);
+        if constexpr (RowSum<TPR, BLOCK>::kShared) __syncthreads();
+        // every thread has read this round's stage
+        if constexpr (Geo::kBulk) {
+            const int next = stage == 0 ? kStages - 1 : stage - 1;
+            if (ok) issue(first + (kStages - 1) * kGroups, next);
+            parity ^= stage == kStages - 1;
         }
-        mu = mu_next, rs = rs_next;
+        if constexpr (kStages > 0) stage = stage + 1 == kStages ? 0 : stage + 1;
+        const float2 total = sum.take(set);
+        set ^= 1;
+        if (in) {
+            // dx = rs (w dy - s - (x - mu) rs q) as two fused steps per element
+            const float s = a.rms ? 0.f : total.x * inv, rq = rs * (total.y * inv);
+            const float2 c1 = both(-rs * rq), c0 = both(rs * fmaf(mu, rq, -s)), r2 = both(rs);
+            float2 out[kPairs];
+#pragma unroll
+            for (int p = 0; p < kPairs; ++p)
+                out[p] = fma2(mul2(pair_of<T, N>(dyp, p), w[p]), r2, fma2(pair_of<T, N>(xp, p), c1, c0));
+            store_row<T, N, TPR, VPT>(a.dx + r * a.os, out, t, a.width, whole);
+        }
+    }
+    if constexpr (Geo::kBulk) {
+        if (!ok && threadIdx.x == 0)  // copies in flight land before the block ends
+            for (int i = 0; i < kStages; ++i)
+                mbar_wait_bounded(full + i, parity ^ (i < stage));
     }
     // the block's sums over its rows
     float* part = a.part + int64_t(blockIdx.x) * 2 * a.width;
-    if constexpr (kRowsAtOnce == 1) {
+    if constexpr (kGroups == 1) {
 #pragma unroll
         for (int p = 0; p < kPairs; ++p)
 #pragma unroll
@@ -164,10 +233,10 @@ __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdA
                 }
             }
     } else {
-        constexpr int kCols = TPR * VPT * N;
-        if constexpr (kAsync) copy_wait<0>();
+        constexpr int kCols = TPR * EPT;
+        if constexpr (Geo::kAsync) copy_wait<0>();
         __syncthreads();  // the ring's last reads and copies are done
-        float* acc = reinterpret_cast<float*>(smem);  // [rows at once][2][columns]
+        float* acc = reinterpret_cast<float*>(ring);  // [groups][2][columns]
 #pragma unroll
         for (int p = 0; p < kPairs; ++p)
 #pragma unroll
@@ -180,7 +249,7 @@ __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdA
         for (int e = threadIdx.x; e < 2 * a.width; e += BLOCK) {
             const int which = e >= a.width, c = e - which * a.width;
             float v = 0.f;
-            for (int g = 0; g < kRowsAtOnce; ++g) v += acc[(2 * g + which) * kCols + c];
+            for (int g = 0; g < kGroups; ++g) v += acc[(2 * g + which) * kCols + c];
             part[e] = v;
         }
     }
@@ -223,8 +292,7 @@ __global__ void __launch_bounds__(kThreads)
 // phase, and the sums by strips of 32 columns in a pass of their own.
 template <typename T>
 __global__ void __launch_bounds__(1024) k_norm_dx_wide(const __grid_constant__ BwdArgs<T> a) {
-    __shared__ float2 red[2 * 32];
-    RowSum<1024, 1024> sum{red};
+    __shared__ float2 red[32];
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const float mu = a.rms ? 0.f : a.mean[r], rs = a.rstd[r];
         float2 v = make_float2(0.f, 0.f);
@@ -233,7 +301,7 @@ __global__ void __launch_bounds__(1024) k_norm_dx_wide(const __grid_constant__ B
             v.x += w;
             v.y = fmaf(w, (to_f32(a.x[r * a.xs + c]) - mu) * rs, v.y);
         }
-        v = sum(v);
+        v = block_sum(v, red);
         const float s = a.rms ? 0.f : v.x / a.width, q = v.y / a.width;
         for (int c = threadIdx.x; c < a.width; c += 1024) {
             const float w = to_f32(a.dy[r * a.ds + c]) * load_param(a.weight, a.ptype, c);
@@ -269,19 +337,19 @@ __global__ void __launch_bounds__(kThreads) k_norm_dw_wide(const __grid_constant
 
 // launches the pass; returns the number of partial sums or a negative status
 template <typename T, int N, int TPR, int BLOCK>
-int launch(const BwdArgs<T>& a, cudaStream_t s) {
-    constexpr int VPT = 16 / N, AHEAD = sizeof(T) == 4 ? 1 : 3;
-    const void* kernel = reinterpret_cast<const void*>(k_norm_bwd<T, N, TPR, VPT, BLOCK, AHEAD>);
-    size_t smem = RowSum<TPR, BLOCK>::kBytes +
-                  (N * sizeof(T) >= 4 ? size_t(AHEAD + 1) * 2 * VPT * BLOCK * N * sizeof(T) : 0);
-    if (TPR < BLOCK && smem < size_t(BLOCK) * 16 * 2 * sizeof(float)) smem = size_t(BLOCK) * 16 * 2 * sizeof(float);
-    if (!allow_shared(kernel, smem)) return DL_ERR_CUDA;
-    constexpr int at_once = BLOCK / TPR;
-    int grid = grid_for(kernel, BLOCK, smem, (a.rows + at_once - 1) / at_once);
+int launch(BwdArgs<T> a, cudaStream_t s) {
+    constexpr int EPT = 16;
+    using Geo = BwdGeometry<T, N, TPR, EPT, BLOCK>;
+    const void* kernel = reinterpret_cast<const void*>(k_norm_bwd<T, N, TPR, EPT, BLOCK>);
+    if (!allow_shared(kernel, Geo::kBytes)) return DL_ERR_CUDA;
+    const int64_t rounds = (a.rows + Geo::kGroups - 1) / Geo::kGroups;
+    int64_t grid = grid_for(kernel, BLOCK, Geo::kBytes, rounds);
     if (grid > kMostBlocks) grid = kMostBlocks;
-    k_norm_bwd<T, N, TPR, VPT, BLOCK, AHEAD><<<grid, BLOCK, smem, s>>>(a);
+    a.run = (rounds + grid - 1) / grid * Geo::kGroups;
+    grid = (a.rows + a.run - 1) / a.run;
+    k_norm_bwd<T, N, TPR, EPT, BLOCK><<<static_cast<int>(grid), BLOCK, Geo::kBytes, s>>>(a);
     const int st = launch_status();
-    return st == DL_OK ? grid : st;
+    return st == DL_OK ? static_cast<int>(grid) : st;
 }
 
 template <typename T, int N>
@@ -346,8 +414,9 @@ extern "C" int dl_layernorm_backward(const void* dy, int64_t dy_stride, const vo
     auto call = [&](auto zero) {
         using T = decltype(zero);
         return backward<T>(BwdArgs<T>{static_cast<const T*>(dy), static_cast<const T*>(x),
-                                      static_cast<T*>(dx), weight, mean, rstd, part, dy_stride,
-                                      x_stride, dx_stride, rows, width, param_type, rms, false},
+                                      static_cast<T*>(dx), weight, mean, rstd, part,
+                                      static_cast<uint32_t*>(d_workspace), dy_stride, x_stride,
+                                      dx_stride, rows, 0, width, param_type, rms, false},
                            s);
     };
     int parts = 0;

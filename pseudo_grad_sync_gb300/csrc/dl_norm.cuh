@@ -15,24 +15,61 @@
 
 namespace dl {
 
-template <typename T, int N>
-__device__ __forceinline__ void unpack(const Pack<T, N>& p, float (&v)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = to_f32(p.v[i]);
+// two 16-bit elements, the first in the low half
+__device__ __forceinline__ float2 unpack2(uint32_t w, __nv_bfloat16) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w, __half) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-// Stores `count` leading elements of a pack; `vec`: the address is a multiple of the pack's size.
+// The packs of a thread as pairs of elements: neighbours of one pack, or for
+// packs of one element those of two packs in a row.
 template <typename T, int N>
-__device__ __forceinline__ void store_pack(T* dst, const float (&v)[N], int count, bool vec) {
+__device__ __forceinline__ float2 pair_of(const Pack<T, N>* q, int p) {
+    if constexpr (N == 1) {
+        return make_float2(to_f32(q[2 * p].v[0]), to_f32(q[2 * p + 1].v[0]));
+    } else {
+        constexpr int H = N / 2;
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t w = reinterpret_cast<const uint32_t*>(q[p / H].v)[p % H];
+            return unpack2(w, T());
+        } else {
+            return make_float2(q[p / H].v[2 * (p % H)], q[p / H].v[2 * (p % H) + 1]);
+        }
+    }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> pack_of(const float2* v) {
     Pack<T, N> p;
+    if constexpr (N == 1) {
+        p.v[0] = from_f32<T>(v[0].x);
+    } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) p.v[i] = from_f32<T>(v[i]);
-    if (vec && count >= N)
-        *reinterpret_cast<Pack<T, N>*>(dst) = p;
-    else
+        for (int i = 0; i < N / 2; ++i)
+            p.v[2 * i] = from_f32<T>(v[i].x), p.v[2 * i + 1] = from_f32<T>(v[i].y);
+    }
+    return p;
+}
+
+// Stores a thread's pairs: `all` its packs are whole and aligned, or else the
+// elements below the width one by one.
+template <typename T, int N, int TPR, int VPT>
+__device__ __forceinline__ void store_row(T* row, const float2 (&v)[VPT * N / 2], int t, int width, bool all) {
+    if constexpr (N > 1) {
+        if (all) {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (i < count) dst[i] = p.v[i];
+            for (int k = 0; k < VPT; ++k)
+                *reinterpret_cast<Pack<T, N>*>(row + (k * TPR + t) * N) = pack_of<T, N>(v + k * N / 2);
+            return;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < VPT * N; ++e) {
+        const int c = ((e / N) * TPR + t) * N + e % N;
+        if (c < width) row[c] = from_f32<T>(e % 2 ? v[e / 2].y : v[e / 2].x);
+    }
 }
 
 __device__ __forceinline__ float load_param(const void* p, int32_t type, int64_t i) {
@@ -40,51 +77,67 @@ __device__ __forceinline__ float load_param(const void* p, int32_t type, int64_t
                           : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(p) + i));
 }
 
-// Sum of one or two values over the TPR threads of a row. Rows of more than a
-// warp pass through shared memory: red holds two sets of partial sums used in
-// turn, so that one barrier per sum is enough (the set written now was read
-// before the barrier of the sum before this one).
+// Sums over the TPR threads of a row, in two halves, so that other rows' work
+// can lie between them: give() leaves the warp's sums, take() joins the warps
+// of the row. Rows of more than a warp need a block barrier between the two;
+// there are two sets of slots, used in turn.
 template <int TPR, int BLOCK>
 struct RowSum {
     static constexpr int kW = TPR / 32;
+    static constexpr bool kShared = TPR > 32;
+    static constexpr size_t kBytes = kShared ? 2 * (BLOCK / 32) * sizeof(float2) : 0;
     float2* red;
-    int set = 0;
-    static constexpr size_t kBytes = TPR > 32 ? 2 * (BLOCK / 32) * sizeof(float2) : 0;
-    __device__ __forceinline__ float2 operator()(float2 v) {
-        constexpr int L = TPR < 32 ? TPR : 32;
+    float2 own;
+    __device__ __forceinline__ void give(float2 v, int set) {
+        if constexpr (kShared) {
+            // after the first exchange the lower half of the warp has only x
+            // left to sum and the upper half only y
+            const bool up = threadIdx.x & 16;
+            float k = (up ? v.y : v.x) + __shfl_xor_sync(kFull, up ? v.x : v.y, 16);
 #pragma unroll
-        for (int sh = L / 2; sh; sh >>= 1) {
-            v.x += __shfl_xor_sync(kFull, v.x, sh);
-            v.y += __shfl_xor_sync(kFull, v.y, sh);
-        }
-        if constexpr (TPR > 32) {
-            float2* r = red + set * (BLOCK / 32);
-            set ^= 1;
-            if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
-            __syncthreads();
-            const float2* mine = r + (threadIdx.x / TPR) * kW;
-            v = mine[0];
+            for (int sh = 8; sh; sh >>= 1) k += __shfl_xor_sync(kFull, k, sh);
+            if ((threadIdx.x & 15) == 0)
+                reinterpret_cast<float*>(red + set * (BLOCK / 32) + (threadIdx.x >> 5))[up] = k;
+        } else {
 #pragma unroll
-            for (int w = 1; w < kW; ++w) v.x += mine[w].x, v.y += mine[w].y;
+            for (int sh = TPR / 2; sh; sh >>= 1)
+                v = add2(v, make_float2(__shfl_xor_sync(kFull, v.x, sh), __shfl_xor_sync(kFull, v.y, sh)));
+            own = v;
         }
-        return v;
     }
-    __device__ __forceinline__ float operator()(float x) {
-        constexpr int L = TPR < 32 ? TPR : 32;
+    __device__ __forceinline__ float2 take(int set) const {
+        if constexpr (kShared) {
+            const float4* mine = reinterpret_cast<const float4*>(red + set * (BLOCK / 32) + (threadIdx.x / TPR) * kW);
+            float2 v = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int sh = L / 2; sh; sh >>= 1) x += __shfl_xor_sync(kFull, x, sh);
-        if constexpr (TPR > 32) {
-            float* r = reinterpret_cast<float*>(red + set * (BLOCK / 32));
-            set ^= 1;
-            if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = x;
-            __syncthreads();
-            const float* mine = r + (threadIdx.x / TPR) * kW;
-            x = mine[0];
-#pragma unroll
-            for (int w = 1; w < kW; ++w) x += mine[w];
+            for (int w = 0; w < kW / 2; ++w) {
+                const float4 q = mine[w];
+                v = add2(v, add2(make_float2(q.x, q.y), make_float2(q.z, q.w)));
+            }
+            return v;
+        } else {
+            return own;
         }
-        return x;
     }
 };
+
+// s / n with its rounding corrected by the remainder (inv = 1 / n): a
+// constant row's mean is then the constant itself, whatever the width.
+__device__ __forceinline__ float divided(float s, float n, float inv) {
+    const float q = s * inv;
+    return fmaf(fmaf(-q, n, s), inv, q);
+}
+
+// Sum over the whole block, for rows that a block reads several times.
+__device__ __forceinline__ float2 block_sum(float2 v, float2* red) {
+    for (int sh = 16; sh; sh >>= 1)
+        v = add2(v, make_float2(__shfl_xor_sync(kFull, v.x, sh), __shfl_xor_sync(kFull, v.y, sh)));
+    __syncthreads();  // red may still be read from the sum before
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = make_float2(0.f, 0.f);
+    for (int w = 0; w < static_cast<int>(blockDim.x / 32); ++w) v = add2(v, red[w]);
+    return v;
+}
 
 }  // namespace dl
