@@ -30,95 +30,36 @@ struct BwdArgs {
 
 constexpr int kStatRows = 512;  // rows whose mean and rstd a block holds at a time
 
-// How rows come in. Bulk copies of whole rows (rows of more than a warp, 16-byte
-// aligned) are issued by one thread into stages that the whole block reads;
-// otherwise every thread copies, or loads, what it works on itself.
-template <typename T, int N, int TPR, int EPT, int BLOCK>
+template <typename T, int TPR, int BLOCK, bool BULK>
 struct BwdGeometry {
-    static constexpr int kVecs = EPT / N, kGroups = BLOCK / TPR;
-    static constexpr bool kBulk = TPR > 32 && N > 1;
-    static constexpr bool kAsync = !kBulk && N * sizeof(T) >= 4;
-    static constexpr int kStages = kBulk || kAsync ? (sizeof(T) == 4 ? 3 : 4) : 0;
-    static constexpr size_t kStage = size_t(2) * BLOCK * EPT * sizeof(T);  // dy and x of a round
-    static constexpr size_t kRing = kStages * kStage;
-    static constexpr size_t kSums = kGroups > 1 ? size_t(BLOCK) * EPT * 2 * sizeof(float) : 0;
+    static constexpr int kEPT = 16, kGroups = BLOCK / TPR, kStages = sizeof(T) == 4 ? 3 : 4;
+    using Ring = RowRing<T, TPR, kEPT, BLOCK, 2, kStages>;
+    static constexpr size_t kSums = kGroups > 1 ? size_t(BLOCK) * kEPT * 2 * sizeof(float) : 0;
     static constexpr size_t kFixed = 128 + kStatRows * sizeof(float2) + RowSum<TPR, BLOCK>::kBytes;
-    static constexpr size_t kBytes = kFixed + (kRing > kSums ? kRing : kSums);
+    static constexpr size_t kBytes = kFixed + (BULK && Ring::kBytes > kSums ? Ring::kBytes : kSums);
 };
 
-// A block takes a run of consecutive rows, in rounds of one row per group of
-// TPR threads: the row's terms of its two sums and of the thread's columns'
-// sums, the exchange of the row sums (one barrier), then dx from the packs,
-// still in registers. The ring's other stages are in flight meanwhile.
-template <typename T, int N, int TPR, int EPT, int BLOCK>
+// A round: the row's terms of its two sums and of the thread's columns' sums,
+// the exchange of the row sums (one barrier), then dx from the packs, still
+// in registers.
+template <typename T, int N, int TPR, int BLOCK, bool BULK>
 __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdArgs<T> a) {
-    using Geo = BwdGeometry<T, N, TPR, EPT, BLOCK>;
-    constexpr int VPT = Geo::kVecs, kGroups = Geo::kGroups, kStages = Geo::kStages;
-    constexpr int kPairs = EPT / 2;
+    using Geo = BwdGeometry<T, TPR, BLOCK, BULK>;
+    constexpr int EPT = Geo::kEPT, VPT = EPT / N, kGroups = Geo::kGroups, kPairs = EPT / 2;
     extern __shared__ __align__(128) unsigned char smem[];
     using P = Pack<T, N>;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem);
     float2* stats = reinterpret_cast<float2*>(smem + 128);
     RowSum<TPR, BLOCK> sum{stats + kStatRows};
-    unsigned char* ring = smem + Geo::kFixed;
     const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
     const int64_t begin = a.run * blockIdx.x, end = min(a.rows, begin + a.run);
     auto column = [&](int k) { return (k * TPR + t) * N; };
-    // this thread's pack k of array `which` in a stage
-    auto slot = [&](int stage, int which, int k) {
-        if constexpr (Geo::kBulk)
-            return reinterpret_cast<P*>(ring + stage * Geo::kStage) + ((group * 2 + which) * VPT + k) * TPR + t;
-        else
-            return reinterpret_cast<P*>(ring + stage * Geo::kStage) + (which * VPT + k) * BLOCK + threadIdx.x;
-    };
-    // bytes of a row that a bulk copy takes; the owner of a last, partial
-    // pack copies that one itself
-    const uint32_t row_bytes = static_cast<uint32_t>(a.width * sizeof(T)) & ~15u;
-    const bool tail = Geo::kBulk && a.width % N != 0 && [&] {
-        const int c = a.width / N * N;
-        return t == (c / N) % TPR;
-    }();
-    auto issue = [&](int64_t first, int stage) {  // the rows of the round from `first` on
-        if constexpr (Geo::kBulk) {
-            if (threadIdx.x == 0) {
-                const int64_t left = end - first;
-                const int n = left <= 0 ? 0 : left < kGroups ? static_cast<int>(left) : kGroups;
-                if (n > 0) {
-                    fence_proxy_async();
-                    mbar_arrive_expect_tx(full + stage, 2u * n * row_bytes);
-                    if (row_bytes)
-                        for (int j = 0; j < n; ++j) {
-                            unsigned char* to = ring + stage * Geo::kStage + j * 2 * (TPR * EPT * sizeof(T));
-                            bulk_copy_g2s(to, a.dy + (first + j) * a.ds, row_bytes, full + stage);
-                            bulk_copy_g2s(to + TPR * EPT * sizeof(T), a.x + (first + j) * a.xs, row_bytes, full + stage);
-                        }
-                }
-            }
-        } else if constexpr (Geo::kAsync) {
-            const int64_t r = first + group;
-            if (r < end) {
+    typename Geo::Ring ring{smem + Geo::kFixed, reinterpret_cast<uint64_t*>(smem), a.status, end,
+                            static_cast<uint32_t>(a.width * sizeof(T)) & ~15u};
+    if constexpr (BULK) {
+        ring.init();
 #pragma unroll
-                for (int k = 0; k < VPT; ++k) {
-                    const int c = column(k);
-                    if (c < a.width) {
-                        const int valid = static_cast<int>(min(N, a.width - c) * sizeof(T));
-                        copy_async<N * sizeof(T)>(slot(stage, 0, k), a.dy + r * a.ds + c, valid);
-                        copy_async<N * sizeof(T)>(slot(stage, 1, k), a.x + r * a.xs + c, valid);
-                    }
-                }
-            }
-            copy_commit();
-        }
-    };
-    if constexpr (Geo::kBulk) {
-        if (threadIdx.x == 0) {
-            for (int i = 0; i < kStages; ++i) mbar_init(full + i, 1);
-            fence_barrier_init();
-        }
-        __syncthreads();
+        for (int i = 0; i < Geo::kStages - 1; ++i) ring.issue(i, begin + i * kGroups, a.dy, a.ds, a.x, a.xs);
     }
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(begin + i * kGroups, i);
     float2 w[kPairs], dw[kPairs], db[kPairs];
 #pragma unroll
     for (int p = 0; p < kPairs; ++p) {
@@ -133,9 +74,7 @@ __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdA
     }
     const bool whole = a.vec_out && column(VPT - 1) + N <= a.width;
     const float inv = 1.0f / static_cast<float>(a.width);
-    bool ok = true;
-    int stage = 0, set = 0, at = kStatRows;
-    uint32_t parity = 0;
+    int set = 0, at = kStatRows;
     for (int64_t first = begin; first < end; first += kGroups, at += kGroups) {
         const int64_t r = first + group;
         const bool in = r < end;
@@ -146,39 +85,26 @@ __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdA
             __syncthreads();
             at = 0;
         }
-        // the round's packs and statistics; zeros past the width and the rows
-        P dyp[VPT], xp[VPT];
         const float2 st = stats[at + group];
         const float mu = in ? st.x : 0.f, rs = in ? st.y : 0.f;
-        if constexpr (Geo::kBulk) {
-            if (ok && !mbar_wait_bounded(full + stage, parity)) {
-                ok = false;  // no wait and no copy after this; the status word says so
-                atomicOr(a.status, kDevErrCopyTimeout);
-            }
-        } else if constexpr (Geo::kAsync) {
-            copy_wait<kStages - 2>();
-            issue(first + (kStages - 1) * kGroups, stage == 0 ? kStages - 1 : stage - 1);  // read one round ago
-        }
+        P dyp[VPT], xp[VPT];
+        if constexpr (BULK) ring.wait();
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int c = column(k);
-            const bool there = in && c < a.width;
-            if constexpr (kStages > 0) {
-                if (there) dyp[k] = *slot(stage, 0, k), xp[k] = *slot(stage, 1, k);
-                if (Geo::kBulk && tail && there && c + N > a.width) {
+            const P* from0 = BULK ? reinterpret_cast<const P*>(ring.row(ring.stage, group, 0)) + k * TPR + t
+                                  : reinterpret_cast<const P*>(a.dy + r * a.ds + c);
+            const P* from1 = BULK ? reinterpret_cast<const P*>(ring.row(ring.stage, group, 1)) + k * TPR + t
+                                  : reinterpret_cast<const P*>(a.x + r * a.xs + c);
+            if (in && c + N <= a.width) {
+                dyp[k] = *from0, xp[k] = *from1;
+            } else {  // a last, partial pack; zeros past the width and the rows
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        const bool el = c + i < a.width;
-                        dyp[k].v[i] = el ? a.dy[r * a.ds + c + i] : from_f32<T>(0.f);
-                        xp[k].v[i] = el ? a.x[r * a.xs + c + i] : from_f32<T>(0.f);
-                    }
+                for (int i = 0; i < N; ++i) {
+                    const bool el = in && c + i < a.width;
+                    dyp[k].v[i] = el ? a.dy[r * a.ds + c + i] : from_f32<T>(0.f);
+                    xp[k].v[i] = el ? a.x[r * a.xs + c + i] : from_f32<T>(0.f);
                 }
-            } else {
-                if (there) dyp[k].v[0] = a.dy[r * a.ds + c], xp[k].v[0] = a.x[r * a.xs + c];
-            }
-            if (!there) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) dyp[k].v[i] = xp[k].v[i] = from_f32<T>(0.f);
             }
         }
         float2 s2 = make_float2(0.f, 0.f), q2 = s2;
@@ -193,14 +119,11 @@ __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdA
             db[p] = add2(db[p], g);
         }
         sum.give(make_float2(s2.x + s2.y, q2.x + q2.y), set);
-        if constexpr (RowSum<TPR, BLOCK>::kShared) __syncthreads();
-        // every thread has read this round's stage
-        if constexpr (Geo::kBulk) {
-            const int next = stage == 0 ? kStages - 1 : stage - 1;
-            if (ok) issue(first + (kStages - 1) * kGroups, next);
-            parity ^= stage == kStages - 1;
+        if constexpr (RowSum<TPR, BLOCK>::kShared || BULK) __syncthreads();
+        if constexpr (BULK) {  // every thread has read this round's stage, and the one before it long ago
+            ring.issue(ring.before(), first + (Geo::kStages - 1) * kGroups, a.dy, a.ds, a.x, a.xs);
+            ring.advance();
         }
-        if constexpr (kStages > 0) stage = stage + 1 == kStages ? 0 : stage + 1;
         const float2 total = sum.take(set);
         set ^= 1;
         if (in) {
@@ -214,11 +137,7 @@ __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdA
             store_row<T, N, TPR, VPT>(a.dx + r * a.os, out, t, a.width, whole);
         }
     }
-    if constexpr (Geo::kBulk) {
-        if (!ok && threadIdx.x == 0)  // copies in flight land before the block ends
-            for (int i = 0; i < kStages; ++i)
-                mbar_wait_bounded(full + i, parity ^ (i < stage));
-    }
+    if constexpr (BULK) ring.drain();
     // the block's sums over its rows
     float* part = a.part + int64_t(blockIdx.x) * 2 * a.width;
     if constexpr (kGroups == 1) {
@@ -234,9 +153,8 @@ __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdA
             }
     } else {
         constexpr int kCols = TPR * EPT;
-        if constexpr (Geo::kAsync) copy_wait<0>();
         __syncthreads();  // the ring's last reads and copies are done
-        float* acc = reinterpret_cast<float*>(ring);  // [groups][2][columns]
+        float* acc = reinterpret_cast<float*>(smem + Geo::kFixed);  // [groups][2][columns]
 #pragma unroll
         for (int p = 0; p < kPairs; ++p)
 #pragma unroll
@@ -336,20 +254,30 @@ __global__ void __launch_bounds__(kThreads) k_norm_dw_wide(const __grid_constant
 }
 
 // launches the pass; returns the number of partial sums or a negative status
-template <typename T, int N, int TPR, int BLOCK>
+// 0 when nothing was launched: fewer than two rounds for a block of the bulk form
+template <typename T, int N, int TPR, int BLOCK, bool BULK>
 int launch(BwdArgs<T> a, cudaStream_t s) {
-    constexpr int EPT = 16;
-    using Geo = BwdGeometry<T, N, TPR, EPT, BLOCK>;
-    const void* kernel = reinterpret_cast<const void*>(k_norm_bwd<T, N, TPR, EPT, BLOCK>);
+    using Geo = BwdGeometry<T, TPR, BLOCK, BULK>;
+    const void* kernel = reinterpret_cast<const void*>(k_norm_bwd<T, N, TPR, BLOCK, BULK>);
     if (!allow_shared(kernel, Geo::kBytes)) return DL_ERR_CUDA;
     const int64_t rounds = (a.rows + Geo::kGroups - 1) / Geo::kGroups;
     int64_t grid = grid_for(kernel, BLOCK, Geo::kBytes, rounds);
     if (grid > kMostBlocks) grid = kMostBlocks;
+    if (BULK && rounds <= grid) return 0;
     a.run = (rounds + grid - 1) / grid * Geo::kGroups;
     grid = (a.rows + a.run - 1) / a.run;
-    k_norm_bwd<T, N, TPR, EPT, BLOCK><<<static_cast<int>(grid), BLOCK, Geo::kBytes, s>>>(a);
+    k_norm_bwd<T, N, TPR, BLOCK, BULK><<<static_cast<int>(grid), BLOCK, Geo::kBytes, s>>>(a);
     const int st = launch_status();
     return st == DL_OK ? static_cast<int>(grid) : st;
+}
+
+template <typename T, int N, int TPR, int BLOCK>
+int launch(const BwdArgs<T>& a, cudaStream_t s) {
+    if constexpr (N > 1) {
+        const int parts = launch<T, N, TPR, BLOCK, true>(a, s);
+        if (parts != 0) return parts;
+    }
+    return launch<T, N, TPR, BLOCK, false>(a, s);
 }
 
 template <typename T, int N>

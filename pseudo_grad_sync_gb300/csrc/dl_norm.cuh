@@ -6,9 +6,11 @@
 // contiguous. A block of 256 threads (512 for the widest rows) works on
 // several rows at once when TPR is smaller.
 //
-// Rows stream in: each thread keeps the packs of the next AHEAD rows of its
-// own in flight with asynchronous copies into a ring in shared memory that no
-// other thread reads, so no barrier belongs to the loads.
+// A block takes a run of consecutive rows in rounds of one row per group of
+// TPR threads. Long runs of 16-byte aligned rows come in by bulk copies into a
+// ring of stages in shared memory, issued by one warp; the barrier of the row
+// sums also tells that a stage has been read. Short runs and other alignments
+// are loaded straight into registers.
 #pragma once
 
 #include "dl_types.cuh"
@@ -139,5 +141,69 @@ __device__ __forceinline__ float2 block_sum(float2 v, float2* red) {
     for (int w = 0; w < static_cast<int>(blockDim.x / 32); ++w) v = add2(v, red[w]);
     return v;
 }
+
+// The ring of a block's rounds: each stage holds ARRAYS arrays' rows of one
+// round, [group][array][TPR * EPT elements].
+template <typename T, int TPR, int EPT, int BLOCK, int ARRAYS, int STAGES>
+struct RowRing {
+    static constexpr int kGroups = BLOCK / TPR;
+    static constexpr size_t kRow = size_t(TPR) * EPT * sizeof(T);
+    static constexpr size_t kStage = kGroups * ARRAYS * kRow;
+    static constexpr size_t kBytes = STAGES * kStage;
+    unsigned char* base;
+    uint64_t* full;  // a barrier per stage
+    uint32_t* status;
+    int64_t end;  // of the block's rows
+    // bytes of a row that a bulk copy takes: a last, partial pack is loaded by its owner
+    uint32_t bytes;
+    int stage = 0;
+    uint32_t parity = 0;
+    bool ok = true;
+
+    __device__ __forceinline__ void init() {
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < STAGES; ++i) mbar_init(full + i, 1);
+            fence_barrier_init();
+        }
+        __syncthreads();
+    }
+    __device__ __forceinline__ unsigned char* row(int st, int group, int which) const {
+        return base + st * kStage + (group * ARRAYS + which) * kRow;
+    }
+    // Warp 0: copies the rows of the round from `first` on, a lane per row.
+    __device__ __forceinline__ void issue(int st, int64_t first, const T* p0, int64_t s0, const T* p1, int64_t s1) {
+        if (threadIdx.x >= 32 || !ok) return;
+        const int64_t left = end - first;
+        if (left <= 0) return;
+        const int n = left < kGroups ? static_cast<int>(left) : kGroups, j = threadIdx.x;
+        if (j == 0) {
+            fence_proxy_async();
+            mbar_arrive_expect_tx(full + st, n * ARRAYS * bytes);
+        }
+        __syncwarp();
+        if (j < n && bytes) {
+            bulk_copy_g2s(row(st, j, 0), p0 + (first + j) * s0, bytes, full + st);
+            if (ARRAYS > 1) bulk_copy_g2s(row(st, j, 1), p1 + (first + j) * s1, bytes, full + st);
+        }
+    }
+    // Until the current stage holds its round. A wait that runs out sets the
+    // status word; the block then neither waits nor copies any more and its
+    // outputs are undefined.
+    __device__ __forceinline__ void wait() {
+        if (!ok) return;
+        ok = __all_sync(kFull, mbar_wait_bounded(full + stage, parity));
+        if (!ok) atomicOr(status, kDevErrCopyTimeout);
+    }
+    __device__ __forceinline__ int before() const { return stage == 0 ? STAGES - 1 : stage - 1; }
+    __device__ __forceinline__ void advance() {
+        parity ^= stage == STAGES - 1;
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
+    }
+    // After a wait that ran out: copies in flight land before the block ends.
+    __device__ __forceinline__ void drain() {
+        if (!ok && threadIdx.x < 32)
+            for (int i = 0; i < STAGES; ++i) mbar_wait_bounded(full + i, parity ^ (i < stage));
+    }
+};
 
 }  // namespace dl
