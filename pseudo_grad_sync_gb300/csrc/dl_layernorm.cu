@@ -16,50 +16,41 @@ struct FwdArgs {
     const void* bias;
     float* mean;
     float* rstd;
+    uint32_t* status;
     int64_t xs, ys, rows;
+    int64_t run;  // rows of a block
     int width;
     int32_t ptype;
     float eps;
     bool rms, vec_out;
 };
 
-// Rows in flight per thread beyond the three being worked on. Threads of 32
-// fp32 elements take none: their ring would pass 227 KB.
-template <typename T, int EPT>
-constexpr int kRowsAhead = EPT * sizeof(T) > 64 ? 0 : 2;
+template <typename T, int TPR, int EPT, int BLOCK, bool BULK>
+struct FwdGeometry {
+    static constexpr int kGroups = BLOCK / TPR, kStages = EPT * sizeof(T) > 64 ? 3 : 4;
+    using Ring = RowRing<T, TPR, EPT, BLOCK, 1, kStages>;
+    static constexpr size_t kFixed = 128 + RowSum<TPR, BLOCK>::kBytes;
+    static constexpr size_t kBytes = kFixed + (BULK ? Ring::kBytes : 0);
+};
 
-// A block's rounds take one row of each group of TPR threads. A round sums
-// its row, sums the squared deviations of the row before (whose mean is known
-// by then) and finishes the row before that: the two sums of a round travel
-// together, with one barrier, and the wait for it is spent on other rows.
-template <typename T, int N, int TPR, int VPT, int BLOCK>
+// A round: the row's sum, a barrier, the sum of its squared deviations, a
+// barrier, and the result from the deviations, still in registers.
+template <typename T, int N, int TPR, int EPT, int BLOCK, bool BULK>
 __global__ void __launch_bounds__(BLOCK) k_norm_fwd(const __grid_constant__ FwdArgs<T> a) {
-    constexpr int kAhead = kRowsAhead<T, VPT * N>, kStages = kAhead + 3;
-    constexpr bool kAsync = N * sizeof(T) >= 4 && kAhead > 0;
-    constexpr int kGroups = BLOCK / TPR, kPairs = VPT * N / 2;
-    extern __shared__ __align__(16) unsigned char smem[];
+    using Geo = FwdGeometry<T, TPR, EPT, BLOCK, BULK>;
+    constexpr int VPT = EPT / N, kGroups = Geo::kGroups, kPairs = EPT / 2;
+    constexpr bool kBarrier = RowSum<TPR, BLOCK>::kShared;
+    extern __shared__ __align__(128) unsigned char smem[];
     using P = Pack<T, N>;
-    RowSum<TPR, BLOCK> sum{reinterpret_cast<float2*>(smem)};
-    P* ring = reinterpret_cast<P*>(smem + RowSum<TPR, BLOCK>::kBytes) + threadIdx.x;
-    const int t = threadIdx.x % TPR;
-    const int64_t step = int64_t(gridDim.x) * kGroups;  // from one of a group's rows to its next
-    const int64_t r0 = int64_t(blockIdx.x) * kGroups;
-    const int64_t mine = r0 + threadIdx.x / TPR;
-    auto issue = [&](int64_t r, int stage) {
-        if (r < a.rows) {
+    RowSum<TPR, BLOCK> sum{reinterpret_cast<float2*>(smem + 128)};
+    const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
+    const int64_t begin = a.run * blockIdx.x, end = min(a.rows, begin + a.run);
+    typename Geo::Ring ring{smem + Geo::kFixed, reinterpret_cast<uint64_t*>(smem), a.status, end,
+                            static_cast<uint32_t>(a.width * sizeof(T)) & ~15u};
+    if constexpr (BULK) {
+        ring.init();
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int c = (k * TPR + t) * N;
-                if (c < a.width)
-                    copy_async<N * sizeof(T)>(ring + (stage * VPT + k) * BLOCK, a.x + r * a.xs + c,
-                                              static_cast<int>(min(N, a.width - c) * sizeof(T)));
-            }
-        }
-        copy_commit();
-    };
-    if constexpr (kAsync) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) issue(mine + i * step, i);
+        for (int i = 0; i < Geo::kStages - 1; ++i) ring.issue(i, begin + i * kGroups, a.x, a.xs, a.x, a.xs);
     }
     float2 w[kPairs], b[kPairs];
     uint32_t valid = 0;  // a bit per element below the width
@@ -76,87 +67,73 @@ __global__ void __launch_bounds__(BLOCK) k_norm_fwd(const __grid_constant__ FwdA
         }
         w[p] = make_float2(f[0], f[1]), b[p] = make_float2(g[0], g[1]);
     }
-    const bool whole = valid == (VPT * N == 32 ? ~0u : (1u << (VPT * N % 32)) - 1u);
+    const bool whole = valid == (EPT == 32 ? ~0u : (1u << (EPT % 32)) - 1u);
     const float width = static_cast<float>(a.width), inv = 1.0f / width;
-    // row r's deviations from mu; zeros past the width (where the ring's slots are stale)
-    auto read = [&](int64_t r, int stage, float mu, float2 (&x)[kPairs]) {
-        P raw[VPT];
+    int set = 0;
+    for (int64_t first = begin; first < end; first += kGroups) {
+        const int64_t r = first + group;
+        const bool in = r < end;
+        float2 x[kPairs];
+        if constexpr (BULK) ring.wait();
+        {
+            P raw[VPT];
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            if constexpr (kAsync) {
-                raw[k] = ring[(stage * VPT + k) * BLOCK];
-            } else {
+            for (int k = 0; k < VPT; ++k) {
                 const int c = (k * TPR + t) * N;
+                const P* from = BULK ? reinterpret_cast<const P*>(ring.row(ring.stage, group, 0)) + k * TPR + t
+                                     : reinterpret_cast<const P*>(a.x + r * a.xs + c);
+                if (in && c + N <= a.width) {
+                    raw[k] = *from;
+                } else {  // a last, partial pack; zeros past the width and the rows
 #pragma unroll
-                for (int i = 0; i < N; ++i) raw[k].v[i] = from_f32<T>(0.f);
-                if (r >= 0 && r < a.rows) {
-                    if (N > 1 && c + N <= a.width) {
-                        raw[k] = *reinterpret_cast<const P*>(a.x + r * a.xs + c);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < N; ++i)
-                            if (c + i < a.width) raw[k].v[i] = a.x[r * a.xs + c + i];
-                    }
+                    for (int i = 0; i < N; ++i)
+                        raw[k].v[i] = in && c + i < a.width ? a.x[r * a.xs + c + i] : from_f32<T>(0.f);
                 }
             }
-        }
 #pragma unroll
-        for (int p = 0; p < kPairs; ++p) x[p] = add2(pair_of<T, N>(raw, p), both(-mu));
-        if (!whole) {
-#pragma unroll
-            for (int p = 0; p < kPairs; ++p) {
-                if (!(valid >> (2 * p) & 1)) x[p].x = 0.f;
-                if (!(valid >> (2 * p + 1) & 1)) x[p].y = 0.f;
-            }
+            for (int p = 0; p < kPairs; ++p) x[p] = pair_of<T, N>(raw, p);
         }
-    };
-    int stage = 0, stage1 = kStages - 1, stage2 = kStages - 2, set = 0;  // of this row and the two before
-    float mu = 0.f;                                                      // of the row before
-    const int64_t rounds = r0 < a.rows ? (a.rows - r0 + step - 1) / step : 0;
-    int64_t r = mine;
-    for (int64_t i = 0; i < rounds + 2; ++i, r += step) {
-        const float2 total = sum.take(set ^ 1);
-        float2 x[kPairs], part = make_float2(0.f, 0.f);
-        if constexpr (kAsync) {
-            copy_wait<kAhead - 1>();
-            issue(r + kAhead * step, stage + kAhead < kStages ? stage + kAhead : stage + kAhead - kStages);
-        }
-        if (!a.rms && i < rounds) {
-            read(r, stage, 0.f, x);
+        float mu = 0.f;
+        if (!a.rms) {
             float2 s = x[0];
 #pragma unroll
             for (int p = 1; p < kPairs; ++p) s = add2(s, x[p]);
-            part.x = s.x + s.y;
-        }
-        const float mu2 = mu;
-        if (i >= 1 && i <= rounds) {
-            mu = a.rms ? 0.f : divided(total.x, width, inv);
-            read(r - step, stage1, mu, x);
-            float2 q = mul2(x[0], x[0]);
+            sum.give(s.x + s.y, set);
+            if constexpr (kBarrier) __syncthreads();
+            mu = divided(sum.take1(set), width, inv);
+            set ^= 1;
 #pragma unroll
-            for (int p = 1; p < kPairs; ++p) q = fma2(x[p], x[p], q);
-            part.y = q.x + q.y;
-        }
-        sum.give(part, set);
-        if (i >= 2) {
-            const int64_t row = r - 2 * step;
-            const float rs = rsqrtf(fmaf(total.y, inv, a.eps));
-            read(row, stage2, mu2, x);
-            if (row < a.rows) {
+            for (int p = 0; p < kPairs; ++p) x[p] = add2(x[p], both(-mu));
+            if (!whole) {
 #pragma unroll
-                for (int p = 0; p < kPairs; ++p) x[p] = fma2(mul2(x[p], both(rs)), w[p], b[p]);
-                store_row<T, N, TPR, VPT>(a.y + row * a.ys, x, t, a.width, whole && a.vec_out);
-                if (t == 0) {
-                    if (!a.rms) a.mean[row] = mu2;
-                    a.rstd[row] = rs;
+                for (int p = 0; p < kPairs; ++p) {
+                    if (!(valid >> (2 * p) & 1)) x[p].x = 0.f;
+                    if (!(valid >> (2 * p + 1) & 1)) x[p].y = 0.f;
                 }
             }
         }
-        if constexpr (RowSum<TPR, BLOCK>::kShared) __syncthreads();
+        float2 q = mul2(x[0], x[0]);
+#pragma unroll
+        for (int p = 1; p < kPairs; ++p) q = fma2(x[p], x[p], q);
+        sum.give(q.x + q.y, set);
+        if constexpr (kBarrier || BULK) __syncthreads();
+        if constexpr (BULK) {  // every thread has read this round's stage, and the one before it long ago
+            ring.issue(ring.before(), first + (Geo::kStages - 1) * kGroups, a.x, a.xs, a.x, a.xs);
+            ring.advance();
+        }
+        const float rs = rsqrtf(fmaf(sum.take1(set), inv, a.eps));
         set ^= 1;
-        stage2 = stage1, stage1 = stage;
-        stage = stage + 1 == kStages ? 0 : stage + 1;
+        if (in) {
+#pragma unroll
+            for (int p = 0; p < kPairs; ++p) x[p] = fma2(mul2(x[p], both(rs)), w[p], b[p]);
+            store_row<T, N, TPR, VPT>(a.y + r * a.ys, x, t, a.width, whole && a.vec_out);
+            if (t == 0) {
+                if (!a.rms) a.mean[r] = mu;
+                a.rstd[r] = rs;
+            }
+        }
     }
+    if constexpr (BULK) ring.drain();
 }
 
 // Rows too wide for a block's registers: the row is read three times (from
@@ -189,30 +166,43 @@ __global__ void __launch_bounds__(1024) k_norm_fwd_wide(const __grid_constant__ 
     }
 }
 
-template <typename T, int N, int TPR, int VPT, int BLOCK>
+// false when nothing was launched: fewer than two rounds for a block of the bulk form
+template <typename T, int N, int TPR, int EPT, int BLOCK, bool BULK>
+bool launch(FwdArgs<T> a, cudaStream_t s, int* status) {
+    using Geo = FwdGeometry<T, TPR, EPT, BLOCK, BULK>;
+    const void* kernel = reinterpret_cast<const void*>(k_norm_fwd<T, N, TPR, EPT, BLOCK, BULK>);
+    *status = DL_ERR_CUDA;
+    if (!allow_shared(kernel, Geo::kBytes)) return true;
+    const int64_t rounds = (a.rows + Geo::kGroups - 1) / Geo::kGroups;
+    int64_t grid = grid_for(kernel, BLOCK, Geo::kBytes, rounds);
+    if (BULK && rounds <= grid) return false;
+    if (BULK && library_status_word(&a.status) != DL_OK) return true;
+    a.run = (rounds + grid - 1) / grid * Geo::kGroups;
+    grid = (a.rows + a.run - 1) / a.run;
+    k_norm_fwd<T, N, TPR, EPT, BLOCK, BULK><<<static_cast<int>(grid), BLOCK, Geo::kBytes, s>>>(a);
+    *status = launch_status();
+    return true;
+}
+
+template <typename T, int N, int TPR, int EPT, int BLOCK>
 int launch(const FwdArgs<T>& a, cudaStream_t s) {
-    const void* kernel = reinterpret_cast<const void*>(k_norm_fwd<T, N, TPR, VPT, BLOCK>);
-    const size_t smem = RowSum<TPR, BLOCK>::kBytes +
-                        (N * sizeof(T) >= 4 && kRowsAhead<T, VPT * N> > 0
-                             ? size_t(kRowsAhead<T, VPT * N> + 3) * VPT * BLOCK * N * sizeof(T)
-                             : 0);
-    if (!allow_shared(kernel, smem)) return DL_ERR_CUDA;
-    constexpr int at_once = BLOCK / TPR;
-    const int grid = grid_for(kernel, BLOCK, smem, (a.rows + at_once - 1) / at_once);
-    k_norm_fwd<T, N, TPR, VPT, BLOCK><<<grid, BLOCK, smem, s>>>(a);
-    return launch_status();
+    int status;
+    if constexpr (N > 1)
+        if (launch<T, N, TPR, EPT, BLOCK, true>(a, s, &status)) return status;
+    launch<T, N, TPR, EPT, BLOCK, false>(a, s, &status);
+    return status;
 }
 
 // 16 elements per thread up to 8192 columns, 32 above.
 template <typename T, int N>
 int by_width(const FwdArgs<T>& a, cudaStream_t s) {
-    if (a.width <= 128) return launch<T, N, 8, 16 / N, 256>(a, s);
-    if (a.width <= 512) return launch<T, N, 32, 16 / N, 256>(a, s);
-    if (a.width <= 1024) return launch<T, N, 64, 16 / N, 256>(a, s);
-    if (a.width <= 2048) return launch<T, N, 128, 16 / N, 256>(a, s);
-    if (a.width <= 4096) return launch<T, N, 256, 16 / N, 256>(a, s);
-    if (a.width <= 8192) return launch<T, N, 512, 16 / N, 512>(a, s);
-    if (a.width <= 16384) return launch<T, N, 512, 32 / N, 512>(a, s);
+    if (a.width <= 128) return launch<T, N, 8, 16, 256>(a, s);
+    if (a.width <= 512) return launch<T, N, 32, 16, 256>(a, s);
+    if (a.width <= 1024) return launch<T, N, 64, 16, 256>(a, s);
+    if (a.width <= 2048) return launch<T, N, 128, 16, 256>(a, s);
+    if (a.width <= 4096) return launch<T, N, 256, 16, 256>(a, s);
+    if (a.width <= 8192) return launch<T, N, 512, 16, 512>(a, s);
+    if (a.width <= 16384) return launch<T, N, 512, 32, 512>(a, s);
     const int64_t most = int64_t(sm_count()) * 2;
     k_norm_fwd_wide<T><<<static_cast<int>(a.rows < most ? a.rows : most), 1024, 0, s>>>(a);
     return launch_status();
@@ -222,8 +212,8 @@ template <typename T>
 int forward(const void* x, int64_t xs, int64_t rows, int width, const void* w, const void* b,
             int32_t pt, float eps, bool rms, void* y, int64_t ys, float* mean, float* rstd,
             cudaStream_t s) {
-    FwdArgs<T> a{static_cast<const T*>(x), static_cast<T*>(y), w, b, mean, rstd, xs, ys, rows, width,
-                 pt, eps, rms, false};
+    FwdArgs<T> a{static_cast<const T*>(x), static_cast<T*>(y), w, b, mean, rstd, nullptr, xs, ys,
+                 rows, 0, width, pt, eps, rms, false};
     a.vec_out = aligned16(y) && ys * sizeof(T) % 16 == 0;
     if (aligned16(x) && xs * sizeof(T) % 16 == 0) return by_width<T, 16 / sizeof(T)>(a, s);
     return by_width<T, 1>(a, s);

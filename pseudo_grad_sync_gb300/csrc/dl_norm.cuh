@@ -107,6 +107,30 @@ struct RowSum {
             own = v;
         }
     }
+    // single sums
+    __device__ __forceinline__ void give(float x, int set) {
+        constexpr int L = TPR < 32 ? TPR : 32;
+#pragma unroll
+        for (int sh = L / 2; sh; sh >>= 1) x += __shfl_xor_sync(kFull, x, sh);
+        if constexpr (kShared) {
+            if ((threadIdx.x & 31) == 0)
+                reinterpret_cast<float*>(red + set * (BLOCK / 32))[threadIdx.x >> 5] = x;
+        } else {
+            own.x = x;
+        }
+    }
+    __device__ __forceinline__ float take1(int set) const {
+        if constexpr (kShared) {
+            const float2* mine = reinterpret_cast<const float2*>(
+                reinterpret_cast<const float*>(red + set * (BLOCK / 32)) + (threadIdx.x / TPR) * kW);
+            float2 v = mine[0];
+#pragma unroll
+            for (int w = 1; w < kW / 2; ++w) v = add2(v, mine[w]);
+            return v.x + v.y;
+        } else {
+            return own.x;
+        }
+    }
     __device__ __forceinline__ float2 take(int set) const {
         if constexpr (kShared) {
             const float4* mine = reinterpret_cast<const float4*>(red + set * (BLOCK / 32) + (threadIdx.x / TPR) * kW);
