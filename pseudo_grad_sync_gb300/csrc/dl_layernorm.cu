@@ -27,16 +27,17 @@ struct FwdArgs {
 
 template <typename T, int TPR, int EPT, int BLOCK, bool BULK>
 struct FwdGeometry {
-    static constexpr int kGroups = BLOCK / TPR, kStages = EPT * sizeof(T) > 64 ? 3 : 4;
+    static constexpr int kGroups = BLOCK / TPR, kStages = 3;
     using Ring = RowRing<T, TPR, EPT, BLOCK, 1, kStages>;
     static constexpr size_t kFixed = 128 + RowSum<TPR, BLOCK>::kBytes;
     static constexpr size_t kBytes = kFixed + (BULK ? Ring::kBytes : 0);
 };
 
 // A round: the row's sum, a barrier, the sum of its squared deviations, a
-// barrier, and the result from the deviations, still in registers.
-template <typename T, int N, int TPR, int EPT, int BLOCK, bool BULK>
-__global__ void __launch_bounds__(BLOCK) k_norm_fwd(const __grid_constant__ FwdArgs<T> a) {
+// barrier, and the result from the deviations, still in registers. FULL: the
+// threads' packs cover the width exactly and y's rows are aligned.
+template <typename T, int N, int TPR, int EPT, int BLOCK, bool BULK, bool FULL>
+__global__ void __launch_bounds__(BLOCK, 512 / BLOCK) k_norm_fwd(const __grid_constant__ FwdArgs<T> a) {
     using Geo = FwdGeometry<T, TPR, EPT, BLOCK, BULK>;
     constexpr int VPT = EPT / N, kGroups = Geo::kGroups, kPairs = EPT / 2;
     constexpr bool kBarrier = RowSum<TPR, BLOCK>::kShared;
@@ -67,23 +68,23 @@ __global__ void __launch_bounds__(BLOCK) k_norm_fwd(const __grid_constant__ FwdA
         }
         w[p] = make_float2(f[0], f[1]), b[p] = make_float2(g[0], g[1]);
     }
-    const bool whole = valid == (EPT == 32 ? ~0u : (1u << (EPT % 32)) - 1u);
+    const bool whole = FULL || valid == (EPT == 32 ? ~0u : (1u << (EPT % 32)) - 1u);
     const float width = static_cast<float>(a.width), inv = 1.0f / width;
     int set = 0;
     for (int64_t first = begin; first < end; first += kGroups) {
         const int64_t r = first + group;
-        const bool in = r < end;
+        const bool in = kGroups == 1 || r < end;
         float2 x[kPairs];
         if constexpr (BULK) ring.wait();
         {
             P raw[VPT];
+            const P* from = (BULK ? reinterpret_cast<const P*>(ring.row(ring.stage, group, 0))
+                                  : reinterpret_cast<const P*>(a.x + r * a.xs)) + t;
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 const int c = (k * TPR + t) * N;
-                const P* from = BULK ? reinterpret_cast<const P*>(ring.row(ring.stage, group, 0)) + k * TPR + t
-                                     : reinterpret_cast<const P*>(a.x + r * a.xs + c);
-                if (in && c + N <= a.width) {
-                    raw[k] = *from;
+                if (FULL || (in && c + N <= a.width)) {
+                    raw[k] = from[k * TPR];  // FULL: a stage's rows past the last are stale and not used
                 } else {  // a last, partial pack; zeros past the width and the rows
 #pragma unroll
                     for (int i = 0; i < N; ++i)
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(BLOCK) k_norm_fwd(const __grid_constant__ FwdA
         if (in) {
 #pragma unroll
             for (int p = 0; p < kPairs; ++p) x[p] = fma2(mul2(x[p], both(rs)), w[p], b[p]);
-            store_row<T, N, TPR, VPT>(a.y + r * a.ys, x, t, a.width, whole && a.vec_out);
+            store_row<T, N, TPR, VPT, FULL>(a.y + r * a.ys, x, t, a.width, a.vec_out);
             if (t == 0) {
                 if (!a.rms) a.mean[r] = mu;
                 a.rstd[r] = rs;
@@ -167,10 +168,10 @@ __global__ void __launch_bounds__(1024) k_norm_fwd_wide(const __grid_constant__ 
 }
 
 // false when nothing was launched: fewer than two rounds for a block of the bulk form
-template <typename T, int N, int TPR, int EPT, int BLOCK, bool BULK>
+template <typename T, int N, int TPR, int EPT, int BLOCK, bool BULK, bool FULL>
 bool launch(FwdArgs<T> a, cudaStream_t s, int* status) {
     using Geo = FwdGeometry<T, TPR, EPT, BLOCK, BULK>;
-    const void* kernel = reinterpret_cast<const void*>(k_norm_fwd<T, N, TPR, EPT, BLOCK, BULK>);
+    const void* kernel = reinterpret_cast<const void*>(k_norm_fwd<T, N, TPR, EPT, BLOCK, BULK, FULL>);
     *status = DL_ERR_CUDA;
     if (!allow_shared(kernel, Geo::kBytes)) return true;
     const int64_t rounds = (a.rows + Geo::kGroups - 1) / Geo::kGroups;
@@ -179,7 +180,7 @@ bool launch(FwdArgs<T> a, cudaStream_t s, int* status) {
     if (BULK && library_status_word(&a.status) != DL_OK) return true;
     a.run = (rounds + grid - 1) / grid * Geo::kGroups;
     grid = (a.rows + a.run - 1) / a.run;
-    k_norm_fwd<T, N, TPR, EPT, BLOCK, BULK><<<static_cast<int>(grid), BLOCK, Geo::kBytes, s>>>(a);
+    k_norm_fwd<T, N, TPR, EPT, BLOCK, BULK, FULL><<<static_cast<int>(grid), BLOCK, Geo::kBytes, s>>>(a);
     *status = launch_status();
     return true;
 }
@@ -187,21 +188,24 @@ bool launch(FwdArgs<T> a, cudaStream_t s, int* status) {
 template <typename T, int N, int TPR, int EPT, int BLOCK>
 int launch(const FwdArgs<T>& a, cudaStream_t s) {
     int status;
-    if constexpr (N > 1)
-        if (launch<T, N, TPR, EPT, BLOCK, true>(a, s, &status)) return status;
-    launch<T, N, TPR, EPT, BLOCK, false>(a, s, &status);
+    if constexpr (N > 1) {
+        const bool full = a.width == TPR * EPT && a.vec_out;
+        if (full ? launch<T, N, TPR, EPT, BLOCK, true, true>(a, s, &status)
+                 : launch<T, N, TPR, EPT, BLOCK, true, false>(a, s, &status))
+            return status;
+    }
+    launch<T, N, TPR, EPT, BLOCK, false, false>(a, s, &status);
     return status;
 }
 
-// 16 elements per thread up to 8192 columns, 32 above.
+// 32 elements per thread: half of a round's work is the same for a thread of 16
 template <typename T, int N>
 int by_width(const FwdArgs<T>& a, cudaStream_t s) {
-    if (a.width <= 128) return launch<T, N, 8, 16, 256>(a, s);
-    if (a.width <= 512) return launch<T, N, 32, 16, 256>(a, s);
-    if (a.width <= 1024) return launch<T, N, 64, 16, 256>(a, s);
-    if (a.width <= 2048) return launch<T, N, 128, 16, 256>(a, s);
-    if (a.width <= 4096) return launch<T, N, 256, 16, 256>(a, s);
-    if (a.width <= 8192) return launch<T, N, 512, 16, 512>(a, s);
+    if (a.width <= 256) return launch<T, N, 8, 32, 256>(a, s);
+    if (a.width <= 1024) return launch<T, N, 32, 32, 256>(a, s);
+    if (a.width <= 2048) return launch<T, N, 64, 32, 256>(a, s);
+    if (a.width <= 4096) return launch<T, N, 128, 32, 256>(a, s);
+    if (a.width <= 8192) return launch<T, N, 256, 32, 256>(a, s);
     if (a.width <= 16384) return launch<T, N, 512, 32, 512>(a, s);
     const int64_t most = int64_t(sm_count()) * 2;
     k_norm_fwd_wide<T><<<static_cast<int>(a.rows < most ? a.rows : most), 1024, 0, s>>>(a);

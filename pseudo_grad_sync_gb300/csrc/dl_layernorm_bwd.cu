@@ -41,8 +41,9 @@ struct BwdGeometry {
 
 // A round: the row's terms of its two sums and of the thread's columns' sums,
 // the exchange of the row sums (one barrier), then dx from the packs, still
-// in registers.
-template <typename T, int N, int TPR, int BLOCK, bool BULK>
+// in registers. FULL: the threads' packs cover the width exactly and dx's rows
+// are aligned.
+template <typename T, int N, int TPR, int BLOCK, bool BULK, bool FULL>
 __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdArgs<T> a) {
     using Geo = BwdGeometry<T, TPR, BLOCK, BULK>;
     constexpr int EPT = Geo::kEPT, VPT = EPT / N, kGroups = Geo::kGroups, kPairs = EPT / 2;
@@ -72,12 +73,11 @@ __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdA
         w[p] = make_float2(f[0], f[1]);
         dw[p] = db[p] = make_float2(0.f, 0.f);
     }
-    const bool whole = a.vec_out && column(VPT - 1) + N <= a.width;
     const float inv = 1.0f / static_cast<float>(a.width);
     int set = 0, at = kStatRows;
     for (int64_t first = begin; first < end; first += kGroups, at += kGroups) {
         const int64_t r = first + group;
-        const bool in = r < end;
+        const bool in = kGroups == 1 || r < end;
         if (at == kStatRows) {  // the next rows' statistics
             __syncthreads();
             for (int i = threadIdx.x; i < kStatRows && first + i < end; i += BLOCK)
@@ -89,15 +89,15 @@ __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdA
         const float mu = in ? st.x : 0.f, rs = in ? st.y : 0.f;
         P dyp[VPT], xp[VPT];
         if constexpr (BULK) ring.wait();
+        const P* from0 = (BULK ? reinterpret_cast<const P*>(ring.row(ring.stage, group, 0))
+                               : reinterpret_cast<const P*>(a.dy + r * a.ds)) + t;
+        const P* from1 = (BULK ? reinterpret_cast<const P*>(ring.row(ring.stage, group, 1))
+                               : reinterpret_cast<const P*>(a.x + r * a.xs)) + t;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int c = column(k);
-            const P* from0 = BULK ? reinterpret_cast<const P*>(ring.row(ring.stage, group, 0)) + k * TPR + t
-                                  : reinterpret_cast<const P*>(a.dy + r * a.ds + c);
-            const P* from1 = BULK ? reinterpret_cast<const P*>(ring.row(ring.stage, group, 1)) + k * TPR + t
-                                  : reinterpret_cast<const P*>(a.x + r * a.xs + c);
-            if (in && c + N <= a.width) {
-                dyp[k] = *from0, xp[k] = *from1;
+            if (in && (FULL || c + N <= a.width)) {
+                dyp[k] = from0[k * TPR], xp[k] = from1[k * TPR];
             } else {  // a last, partial pack; zeros past the width and the rows
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdA
 #pragma unroll
             for (int p = 0; p < kPairs; ++p)
                 out[p] = fma2(mul2(pair_of<T, N>(dyp, p), w[p]), r2, fma2(pair_of<T, N>(xp, p), c1, c0));
-            store_row<T, N, TPR, VPT>(a.dx + r * a.os, out, t, a.width, whole);
+            store_row<T, N, TPR, VPT, FULL>(a.dx + r * a.os, out, t, a.width, a.vec_out);
         }
     }
     if constexpr (BULK) ring.drain();
@@ -255,10 +255,10 @@ __global__ void __launch_bounds__(kThreads) k_norm_dw_wide(const __grid_constant
 
 // launches the pass; returns the number of partial sums or a negative status
 // 0 when nothing was launched: fewer than two rounds for a block of the bulk form
-template <typename T, int N, int TPR, int BLOCK, bool BULK>
+template <typename T, int N, int TPR, int BLOCK, bool BULK, bool FULL>
 int launch(BwdArgs<T> a, cudaStream_t s) {
     using Geo = BwdGeometry<T, TPR, BLOCK, BULK>;
-    const void* kernel = reinterpret_cast<const void*>(k_norm_bwd<T, N, TPR, BLOCK, BULK>);
+    const void* kernel = reinterpret_cast<const void*>(k_norm_bwd<T, N, TPR, BLOCK, BULK, FULL>);
     if (!allow_shared(kernel, Geo::kBytes)) return DL_ERR_CUDA;
     const int64_t rounds = (a.rows + Geo::kGroups - 1) / Geo::kGroups;
     int64_t grid = grid_for(kernel, BLOCK, Geo::kBytes, rounds);
@@ -266,7 +266,7 @@ int launch(BwdArgs<T> a, cudaStream_t s) {
     if (BULK && rounds <= grid) return 0;
     a.run = (rounds + grid - 1) / grid * Geo::kGroups;
     grid = (a.rows + a.run - 1) / a.run;
-    k_norm_bwd<T, N, TPR, BLOCK, BULK><<<static_cast<int>(grid), BLOCK, Geo::kBytes, s>>>(a);
+    k_norm_bwd<T, N, TPR, BLOCK, BULK, FULL><<<static_cast<int>(grid), BLOCK, Geo::kBytes, s>>>(a);
     const int st = launch_status();
     return st == DL_OK ? static_cast<int>(grid) : st;
 }
@@ -274,19 +274,20 @@ int launch(BwdArgs<T> a, cudaStream_t s) {
 template <typename T, int N, int TPR, int BLOCK>
 int launch(const BwdArgs<T>& a, cudaStream_t s) {
     if constexpr (N > 1) {
-        const int parts = launch<T, N, TPR, BLOCK, true>(a, s);
+        const bool full = a.width == TPR * 16 && a.vec_out;
+        const int parts = full ? launch<T, N, TPR, BLOCK, true, true>(a, s) : launch<T, N, TPR, BLOCK, true, false>(a, s);
         if (parts != 0) return parts;
     }
-    return launch<T, N, TPR, BLOCK, false>(a, s);
+    return launch<T, N, TPR, BLOCK, false, false>(a, s);
 }
 
 template <typename T, int N>
 int by_width(const BwdArgs<T>& a, cudaStream_t s) {
     if (a.width <= 128) return launch<T, N, 8, 256>(a, s);
-    if (a.width <= 512) return launch<T, N, 32, 256>(a, s);
-    if (a.width <= 1024) return launch<T, N, 64, 256>(a, s);
-    if (a.width <= 2048) return launch<T, N, 128, 256>(a, s);
-    if (a.width <= 4096) return launch<T, N, 256, 256>(a, s);
+    if (a.width <= 512) return launch<T, N, 32, 512>(a, s);
+    if (a.width <= 1024) return launch<T, N, 64, 512>(a, s);
+    if (a.width <= 2048) return launch<T, N, 128, 512>(a, s);
+    if (a.width <= 4096) return launch<T, N, 256, 512>(a, s);
     if (a.width <= 8192) return launch<T, N, 512, 512>(a, s);
     // the sums first: dx may overwrite dy
     k_norm_dw_wide<T><<<dim3((a.width + 31) / 32, kWideParts), kThreads, 0, s>>>(a);

@@ -42,35 +42,46 @@ __device__ __forceinline__ float2 pair_of(const Pack<T, N>* q, int p) {
     }
 }
 
+__device__ __forceinline__ uint32_t pack2(float2 v, __nv_bfloat16) {
+    const __nv_bfloat162 p = __float22bfloat162_rn(v);
+    return *reinterpret_cast<const uint32_t*>(&p);
+}
+__device__ __forceinline__ uint32_t pack2(float2 v, __half) {
+    const __half2 p = __float22half2_rn(v);
+    return *reinterpret_cast<const uint32_t*>(&p);
+}
+
 template <typename T, int N>
 __device__ __forceinline__ Pack<T, N> pack_of(const float2* v) {
     Pack<T, N> p;
     if constexpr (N == 1) {
         p.v[0] = from_f32<T>(v[0].x);
+    } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) reinterpret_cast<uint32_t*>(p.v)[i] = pack2(v[i], T());
     } else {
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i)
-            p.v[2 * i] = from_f32<T>(v[i].x), p.v[2 * i + 1] = from_f32<T>(v[i].y);
+        for (int i = 0; i < N / 2; ++i) p.v[2 * i] = v[i].x, p.v[2 * i + 1] = v[i].y;
     }
     return p;
 }
 
-// Stores a thread's pairs: `all` its packs are whole and aligned, or else the
-// elements below the width one by one.
-template <typename T, int N, int TPR, int VPT>
-__device__ __forceinline__ void store_row(T* row, const float2 (&v)[VPT * N / 2], int t, int width, bool all) {
-    if constexpr (N > 1) {
-        if (all) {
+// Stores a thread's pairs: whole packs at once where the rows are aligned
+// (`vec`), the elements of a last, partial pack one by one.
+template <typename T, int N, int TPR, int VPT, bool FULL>
+__device__ __forceinline__ void store_row(T* row, const float2 (&v)[VPT * N / 2], int t, int width, bool vec) {
 #pragma unroll
-            for (int k = 0; k < VPT; ++k)
-                *reinterpret_cast<Pack<T, N>*>(row + (k * TPR + t) * N) = pack_of<T, N>(v + k * N / 2);
-            return;
+    for (int k = 0; k < VPT; ++k) {
+        const int c = (k * TPR + t) * N;
+        if (FULL || (N > 1 && vec && c + N <= width)) {
+            *(reinterpret_cast<Pack<T, N>*>(row) + k * TPR + t) = pack_of<T, N>(v + k * N / 2);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int e = k * N + i;
+                if (c + i < width) row[c + i] = from_f32<T>(e % 2 ? v[e / 2].y : v[e / 2].x);
+            }
         }
-    }
-#pragma unroll
-    for (int e = 0; e < VPT * N; ++e) {
-        const int c = ((e / N) * TPR + t) * N + e % N;
-        if (c < width) row[c] = from_f32<T>(e % 2 ? v[e / 2].y : v[e / 2].x);
     }
 }
 
@@ -170,7 +181,9 @@ __device__ __forceinline__ float2 block_sum(float2 v, float2* red) {
 // round, [group][array][TPR * EPT elements].
 template <typename T, int TPR, int EPT, int BLOCK, int ARRAYS, int STAGES>
 struct RowRing {
+    static constexpr long kPolls = 1L << 17;  // of a wait: about a second
     static constexpr int kGroups = BLOCK / TPR;
+    static_assert(kGroups <= 32, "a lane of warp 0 copies a row");
     static constexpr size_t kRow = size_t(TPR) * EPT * sizeof(T);
     static constexpr size_t kStage = kGroups * ARRAYS * kRow;
     static constexpr size_t kBytes = STAGES * kStage;
@@ -196,9 +209,9 @@ struct RowRing {
     }
     // Warp 0: copies the rows of the round from `first` on, a lane per row.
     __device__ __forceinline__ void issue(int st, int64_t first, const T* p0, int64_t s0, const T* p1, int64_t s1) {
-        if (threadIdx.x >= 32 || !ok) return;
+        if (threadIdx.x >= 32) return;
         const int64_t left = end - first;
-        if (left <= 0) return;
+        if (left <= 0 || !ok) return;
         const int n = left < kGroups ? static_cast<int>(left) : kGroups, j = threadIdx.x;
         if (j == 0) {
             fence_proxy_async();
@@ -215,7 +228,7 @@ struct RowRing {
     // outputs are undefined.
     __device__ __forceinline__ void wait() {
         if (!ok) return;
-        ok = __all_sync(kFull, mbar_wait_bounded(full + stage, parity));
+        ok = __all_sync(kFull, mbar_wait_bounded(full + stage, parity, kPolls));
         if (!ok) atomicOr(status, kDevErrCopyTimeout);
     }
     __device__ __forceinline__ int before() const { return stage == 0 ? STAGES - 1 : stage - 1; }
@@ -226,7 +239,7 @@ struct RowRing {
     // After a wait that ran out: copies in flight land before the block ends.
     __device__ __forceinline__ void drain() {
         if (!ok && threadIdx.x < 32)
-            for (int i = 0; i < STAGES; ++i) mbar_wait_bounded(full + i, parity ^ (i < stage));
+            for (int i = 0; i < STAGES; ++i) mbar_wait_bounded(full + i, parity ^ (i < stage), kPolls);
     }
 };
 

@@ -440,7 +440,27 @@ def test_layernorm(dl, width, kind, param):
         _backward_case(dl, rng, x, w, mean, rstd, rms, bias, kind, param, pad, rows == 37)
 
 
-def _backward_case(dl, rng, x, w, mean, rstd, rms, bias, kind, param, pad, accumulate):
+@pytest.mark.parametrize("width", WIDTHS)
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_layernorm_long_runs_of_rows(dl, width, kind, monkeypatch):
+    """The same with two blocks, so that each takes many rounds: the rings of
+    copies wrap around, the last round is partial, and the statistics are
+    fetched in several pieces."""
+    monkeypatch.setenv("DL_GRID_LIMIT", "2")
+    rng = np.random.default_rng(1000 + width)
+    for rows, pad, rms in ((1337 if width <= 2048 else 203, 0, False), (90, 64, True)):
+        x = _rows(rng, rows, width, kind, pad)
+        w, b = (to_cuda(rng.standard_normal(width)) for _ in range(2))
+        y, mean, rstd = dl.layernorm_forward(x, w, b, EPS, rms)
+        x64, w64, b64 = np64(x), np64(w), np64(b)
+        yr, mr, rr = ref.norm64(x64, w64, b64, EPS, rms)
+        h = (x64 - mr[:, None]) * rr[:, None]
+        assert np.all(abs(np64(y) - yr) <= _forward_tol(x64, w64, b64, yr, h, rr, kind)), (rows, pad)
+        # two blocks: a chain of additions is at most half of the rows
+        _backward_case(dl, rng, x, w, mean, rstd, rms, True, kind, "f32", pad, False, 64 + rows / 2)
+
+
+def _backward_case(dl, rng, x, w, mean, rstd, rms, bias, kind, param, pad, accumulate, chain=None):
     rows, width = x.shape
     dy = _rows(rng, rows, width, kind, pad, 1e-2)
     flat = to_cuda(rng.standard_normal(2 * width + 9), param)
@@ -462,7 +482,7 @@ def _backward_case(dl, rng, x, w, mean, rstd, rms, bias, kind, param, pad, accum
                                           + abs(h) * (off_along + 4 * along) + herr * along)
     assert np.all(abs(np64(dx) - want) <= tol + 2.0 ** -24 * (kind == "f16") + 2.0 ** -130)
     # sums over rows: no chain of additions longer than 64 + rows / 8
-    chain = 64 + rows / 8
+    chain = chain or 64 + rows / 8
     up = UT[param]
     old = np64(start[3:3 + width]) if accumulate else 0.0
     tw = U * (chain * (abs(dy64) * abs(h)).sum(0) + (abs(dy64) * herr).sum(0) + 2 * abs(old))
