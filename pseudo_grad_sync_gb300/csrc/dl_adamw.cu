@@ -776,7 +776,9 @@ extern "C" int dl_grad_norm(const void* const* grads, const int64_t* numel, int3
             a.chunk_end[0] = 0;
             a.n = 1;
         }
-        int grid = grid_for(kernel, kThreads, 0, chunks ? chunks : 1);
+        static Resident resident[2];
+        int grid = resident[grad_type].grid(kernel, kThreads, 0, chunks ? chunks : 1);
+        if (grid == 0) return DL_ERR_CUDA;
         if (grid > kNormBlocks) grid = kNormBlocks;
         void* args[] = {&a};
         if (cudaLaunchKernel(kernel, dim3(grid), dim3(kThreads), args, 0,
@@ -862,8 +864,9 @@ extern "C" int dl_adamw_step(const dl_adamw_job* jobs, int32_t n_jobs, int32_t g
         int64_t grid = work;
         if (by8) {  // as many warps as the GPU holds, each with one run of slots
             smem = kWarps * kStages * (grad_type == DL_F32 ? sizeof(Stage<float>) : sizeof(Stage<__nv_bfloat16>));
-            if (!allow_shared(kernel, smem)) return DL_ERR_CUDA;
-            grid = grid_for(kernel, kThreads, smem, (work + kWarps - 1) / kWarps);
+            static Resident resident[2];
+            grid = resident[grad_type].grid(kernel, kThreads, smem, (work + kWarps - 1) / kWarps);
+            if (grid == 0) return DL_ERR_CUDA;
             a.run = (work + grid * kWarps - 1) / (grid * kWarps);
             if (a.run > kMostRun) {
                 a.run = kMostRun;

@@ -46,8 +46,10 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) k_norm_fwd(const __grid_co
     RowSum<TPR, BLOCK> sum{reinterpret_cast<float2*>(smem + 128)};
     const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
     const int64_t begin = a.run * blockIdx.x, end = min(a.rows, begin + a.run);
-    typename Geo::Ring ring{smem + Geo::kFixed, reinterpret_cast<uint64_t*>(smem), a.status, end,
-                            static_cast<uint32_t>(a.width * sizeof(T)) & ~15u};
+    const uint32_t bytes = static_cast<uint32_t>(a.width * sizeof(T)) & ~15u;
+    const bool together = bytes == a.width * sizeof(T) && a.xs == a.width;
+    typename Geo::Ring ring{smem + Geo::kFixed, reinterpret_cast<uint64_t*>(smem), a.status, end, bytes,
+                            together ? bytes : static_cast<uint32_t>(Geo::Ring::kRow)};
     if constexpr (BULK) {
         ring.init();
 #pragma unroll
@@ -62,13 +64,19 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) k_norm_fwd(const __grid_co
         for (int i = 0; i < 2; ++i) {
             const int e = 2 * p + i, c = ((e / N) * TPR + t) * N + e % N;
             const bool in = c < a.width;
-            valid |= static_cast<uint32_t>(in) << e;
+            if (!FULL) valid |= static_cast<uint32_t>(in) << e;
             f[i] = in ? load_param(a.weight, a.ptype, c) : 0.f;
             g[i] = in && a.bias ? load_param(a.bias, a.ptype, c) : 0.f;
         }
         w[p] = make_float2(f[0], f[1]), b[p] = make_float2(g[0], g[1]);
     }
-    const bool whole = FULL || valid == (EPT == 32 ? ~0u : (1u << (EPT % 32)) - 1u);
+    // 1 for packs with elements below the width, 0 for the others: their zeros
+    // have no deviation
+    float has[VPT];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) has[k] = (k * TPR + t) * N < a.width ? 1.f : 0.f;
+    // a last, partial pack; the elements of a pack of one are covered by `has`
+    const bool cut = !FULL && N > 1 && a.width % N != 0 && (a.width / N) % TPR == t;
     const float width = static_cast<float>(a.width), inv = 1.0f / width;
     int set = 0;
     for (int64_t first = begin; first < end; first += kGroups) {
@@ -104,8 +112,10 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) k_norm_fwd(const __grid_co
             mu = divided(sum.take1(set), width, inv);
             set ^= 1;
 #pragma unroll
-            for (int p = 0; p < kPairs; ++p) x[p] = add2(x[p], both(-mu));
-            if (!whole) {
+            for (int p = 0; p < kPairs; ++p)
+                x[p] = FULL ? add2(x[p], both(-mu))
+                            : fma2(make_float2(has[2 * p / N], has[(2 * p + 1) / N]), both(-mu), x[p]);
+            if (cut) {
 #pragma unroll
                 for (int p = 0; p < kPairs; ++p) {
                     if (!(valid >> (2 * p) & 1)) x[p].x = 0.f;
@@ -173,9 +183,10 @@ bool launch(FwdArgs<T> a, cudaStream_t s, int* status) {
     using Geo = FwdGeometry<T, TPR, EPT, BLOCK, BULK>;
     const void* kernel = reinterpret_cast<const void*>(k_norm_fwd<T, N, TPR, EPT, BLOCK, BULK, FULL>);
     *status = DL_ERR_CUDA;
-    if (!allow_shared(kernel, Geo::kBytes)) return true;
+    static Resident resident;
     const int64_t rounds = (a.rows + Geo::kGroups - 1) / Geo::kGroups;
-    int64_t grid = grid_for(kernel, BLOCK, Geo::kBytes, rounds);
+    int64_t grid = resident.grid(kernel, BLOCK, Geo::kBytes, rounds);
+    if (grid == 0) return true;
     if (BULK && rounds <= grid) return false;
     if (BULK && library_status_word(&a.status) != DL_OK) return true;
     a.run = (rounds + grid - 1) / grid * Geo::kGroups;
@@ -201,6 +212,8 @@ int launch(const FwdArgs<T>& a, cudaStream_t s) {
 // 32 elements per thread: half of a round's work is the same for a thread of 16
 template <typename T, int N>
 int by_width(const FwdArgs<T>& a, cudaStream_t s) {
+    if (a.width <= 64) return launch<T, N, 8, 8, 256>(a, s);
+    if (a.width <= 128) return launch<T, N, 8, 16, 256>(a, s);
     if (a.width <= 256) return launch<T, N, 8, 32, 256>(a, s);
     if (a.width <= 1024) return launch<T, N, 32, 32, 256>(a, s);
     if (a.width <= 2048) return launch<T, N, 64, 32, 256>(a, s);

@@ -30,12 +30,12 @@ struct BwdArgs {
 
 constexpr int kStatRows = 512;  // rows whose mean and rstd a block holds at a time
 
-template <typename T, int TPR, int BLOCK, bool BULK>
+template <typename T, int TPR, int BLOCK, bool BULK, int CLUSTER>
 struct BwdGeometry {
     static constexpr int kEPT = 16, kGroups = BLOCK / TPR, kStages = sizeof(T) == 4 ? 3 : 4;
     using Ring = RowRing<T, TPR, kEPT, BLOCK, 2, kStages>;
     static constexpr size_t kSums = kGroups > 1 ? size_t(BLOCK) * kEPT * 2 * sizeof(float) : 0;
-    static constexpr size_t kFixed = 128 + kStatRows * sizeof(float2) + RowSum<TPR, BLOCK>::kBytes;
+    static constexpr size_t kFixed = 128 + kStatRows * sizeof(float2) + RowSum<TPR, BLOCK, CLUSTER>::kBytes;
     static constexpr size_t kBytes = kFixed + (BULK && Ring::kBytes > kSums ? Ring::kBytes : kSums);
 };
 
@@ -43,23 +43,31 @@ struct BwdGeometry {
 // the exchange of the row sums (one barrier), then dx from the packs, still
 // in registers. FULL: the threads' packs cover the width exactly and dx's rows
 // are aligned.
-template <typename T, int N, int TPR, int BLOCK, bool BULK, bool FULL>
+template <typename T, int N, int TPR, int BLOCK, bool BULK, bool FULL, int CLUSTER>
 __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdArgs<T> a) {
-    using Geo = BwdGeometry<T, TPR, BLOCK, BULK>;
+    using Geo = BwdGeometry<T, TPR, BLOCK, BULK, CLUSTER>;
     constexpr int EPT = Geo::kEPT, VPT = EPT / N, kGroups = Geo::kGroups, kPairs = EPT / 2;
     extern __shared__ __align__(128) unsigned char smem[];
     using P = Pack<T, N>;
     float2* stats = reinterpret_cast<float2*>(smem + 128);
-    RowSum<TPR, BLOCK> sum{stats + kStatRows};
+    RowSum<TPR, BLOCK, CLUSTER> sum{stats + kStatRows};
     const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
-    const int64_t begin = a.run * blockIdx.x, end = min(a.rows, begin + a.run);
+    // the block's rows, and with a cluster its part of their columns
+    const int64_t part_of = blockIdx.x / CLUSTER, begin = a.run * part_of, end = min(a.rows, begin + a.run);
+    const int off = CLUSTER > 1 ? static_cast<int>(blockIdx.x % CLUSTER) * TPR * EPT : 0;
+    const int width = CLUSTER > 1 ? max(0, min(a.width - off, TPR * EPT)) : a.width;
+    const T* const dy = a.dy + off;
+    const T* const x = a.x + off;
     auto column = [&](int k) { return (k * TPR + t) * N; };
-    typename Geo::Ring ring{smem + Geo::kFixed, reinterpret_cast<uint64_t*>(smem), a.status, end,
-                            static_cast<uint32_t>(a.width * sizeof(T)) & ~15u};
+    const uint32_t bytes = static_cast<uint32_t>(width * sizeof(T)) & ~15u;
+    const bool together = bytes == width * sizeof(T) && a.ds == width && a.xs == width;
+    typename Geo::Ring ring{smem + Geo::kFixed, reinterpret_cast<uint64_t*>(smem), a.status, end, bytes,
+                            together ? bytes : static_cast<uint32_t>(Geo::Ring::kRow)};
+    if constexpr (CLUSTER > 1) sum.barrier();  // the other block runs before its memory is written
     if constexpr (BULK) {
         ring.init();
 #pragma unroll
-        for (int i = 0; i < Geo::kStages - 1; ++i) ring.issue(i, begin + i * kGroups, a.dy, a.ds, a.x, a.xs);
+        for (int i = 0; i < Geo::kStages - 1; ++i) ring.issue(i, begin + i * kGroups, dy, a.ds, x, a.xs);
     }
     float2 w[kPairs], dw[kPairs], db[kPairs];
 #pragma unroll
@@ -68,7 +76,7 @@ __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdA
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int e = 2 * p + i, c = column(e / N) + e % N;
-            f[i] = c < a.width ? load_param(a.weight, a.ptype, c) : 0.f;
+            f[i] = c < width ? load_param(a.weight, a.ptype, off + c) : 0.f;
         }
         w[p] = make_float2(f[0], f[1]);
         dw[p] = db[p] = make_float2(0.f, 0.f);
@@ -90,20 +98,20 @@ __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdA
         P dyp[VPT], xp[VPT];
         if constexpr (BULK) ring.wait();
         const P* from0 = (BULK ? reinterpret_cast<const P*>(ring.row(ring.stage, group, 0))
-                               : reinterpret_cast<const P*>(a.dy + r * a.ds)) + t;
+                               : reinterpret_cast<const P*>(dy + r * a.ds)) + t;
         const P* from1 = (BULK ? reinterpret_cast<const P*>(ring.row(ring.stage, group, 1))
-                               : reinterpret_cast<const P*>(a.x + r * a.xs)) + t;
+                               : reinterpret_cast<const P*>(x + r * a.xs)) + t;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int c = column(k);
-            if (in && (FULL || c + N <= a.width)) {
+            if (in && (FULL || c + N <= width)) {
                 dyp[k] = from0[k * TPR], xp[k] = from1[k * TPR];
             } else {  // a last, partial pack; zeros past the width and the rows
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    const bool el = in && c + i < a.width;
-                    dyp[k].v[i] = el ? a.dy[r * a.ds + c + i] : from_f32<T>(0.f);
-                    xp[k].v[i] = el ? a.x[r * a.xs + c + i] : from_f32<T>(0.f);
+                    const bool el = in && c + i < width;
+                    dyp[k].v[i] = el ? dy[r * a.ds + c + i] : from_f32<T>(0.f);
+                    xp[k].v[i] = el ? x[r * a.xs + c + i] : from_f32<T>(0.f);
                 }
             }
         }
@@ -119,9 +127,9 @@ __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdA
             db[p] = add2(db[p], g);
         }
         sum.give(make_float2(s2.x + s2.y, q2.x + q2.y), set);
-        if constexpr (RowSum<TPR, BLOCK>::kShared || BULK) __syncthreads();
+        if constexpr (RowSum<TPR, BLOCK, CLUSTER>::kShared || BULK) sum.barrier();
         if constexpr (BULK) {  // every thread has read this round's stage, and the one before it long ago
-            ring.issue(ring.before(), first + (Geo::kStages - 1) * kGroups, a.dy, a.ds, a.x, a.xs);
+            ring.issue(ring.before(), first + (Geo::kStages - 1) * kGroups, dy, a.ds, x, a.xs);
             ring.advance();
         }
         const float2 total = sum.take(set);
@@ -134,19 +142,19 @@ __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdA
 #pragma unroll
             for (int p = 0; p < kPairs; ++p)
                 out[p] = fma2(mul2(pair_of<T, N>(dyp, p), w[p]), r2, fma2(pair_of<T, N>(xp, p), c1, c0));
-            store_row<T, N, TPR, VPT, FULL>(a.dx + r * a.os, out, t, a.width, a.vec_out);
+            store_row<T, N, TPR, VPT, FULL>(a.dx + off + r * a.os, out, t, width, a.vec_out);
         }
     }
     if constexpr (BULK) ring.drain();
     // the block's sums over its rows
-    float* part = a.part + int64_t(blockIdx.x) * 2 * a.width;
+    float* part = a.part + part_of * 2 * a.width + off;
     if constexpr (kGroups == 1) {
 #pragma unroll
         for (int p = 0; p < kPairs; ++p)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int e = 2 * p + i, c = column(e / N) + e % N;
-                if (c < a.width) {
+                if (c < width) {
                     part[c] = i ? dw[p].y : dw[p].x;
                     part[a.width + c] = i ? db[p].y : db[p].x;
                 }
@@ -206,7 +214,7 @@ __global__ void __launch_bounds__(kThreads)
         static_cast<__nv_bfloat16*>(out)[c] = __float2bfloat16_rn(s);
 }
 
-// Rows wider than 8192 columns: dx row by row, read again for the second
+// Rows wider than 16384 columns: dx row by row, read again for the second
 // phase, and the sums by strips of 32 columns in a pass of their own.
 template <typename T>
 __global__ void __launch_bounds__(1024) k_norm_dx_wide(const __grid_constant__ BwdArgs<T> a) {
@@ -255,40 +263,58 @@ __global__ void __launch_bounds__(kThreads) k_norm_dw_wide(const __grid_constant
 
 // launches the pass; returns the number of partial sums or a negative status
 // 0 when nothing was launched: fewer than two rounds for a block of the bulk form
-template <typename T, int N, int TPR, int BLOCK, bool BULK, bool FULL>
-int launch(BwdArgs<T> a, cudaStream_t s) {
-    using Geo = BwdGeometry<T, TPR, BLOCK, BULK>;
-    const void* kernel = reinterpret_cast<const void*>(k_norm_bwd<T, N, TPR, BLOCK, BULK, FULL>);
-    if (!allow_shared(kernel, Geo::kBytes)) return DL_ERR_CUDA;
+template <typename T, int N, int TPR, int BLOCK, int CLUSTER, bool BULK, bool FULL>
+int launch_form(BwdArgs<T> a, cudaStream_t s) {
+    using Geo = BwdGeometry<T, TPR, BLOCK, BULK, CLUSTER>;
+    auto* kernel = k_norm_bwd<T, N, TPR, BLOCK, BULK, FULL, CLUSTER>;
+    static Resident resident;
     const int64_t rounds = (a.rows + Geo::kGroups - 1) / Geo::kGroups;
-    int64_t grid = grid_for(kernel, BLOCK, Geo::kBytes, rounds);
-    if (grid > kMostBlocks) grid = kMostBlocks;
-    if (BULK && rounds <= grid) return 0;
-    a.run = (rounds + grid - 1) / grid * Geo::kGroups;
-    grid = (a.rows + a.run - 1) / a.run;
-    k_norm_bwd<T, N, TPR, BLOCK, BULK, FULL><<<static_cast<int>(grid), BLOCK, Geo::kBytes, s>>>(a);
-    const int st = launch_status();
-    return st == DL_OK ? static_cast<int>(grid) : st;
+    int64_t parts = resident.grid(reinterpret_cast<const void*>(kernel), BLOCK, Geo::kBytes, rounds * CLUSTER);
+    if (parts == 0) return DL_ERR_CUDA;
+    parts = parts < CLUSTER ? 1 : parts / CLUSTER;
+    if (parts > kMostBlocks) parts = kMostBlocks;
+    if (BULK && rounds <= parts) return 0;
+    a.run = (rounds + parts - 1) / parts * Geo::kGroups;
+    parts = (a.rows + a.run - 1) / a.run;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3(static_cast<unsigned>(parts * CLUSTER));
+    config.blockDim = dim3(BLOCK);
+    config.dynamicSmemBytes = Geo::kBytes;
+    config.stream = s;
+    cudaLaunchAttribute cluster;
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = CLUSTER;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    config.attrs = &cluster;
+    config.numAttrs = CLUSTER > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&config, kernel, a) != cudaSuccess) {
+        cudaGetLastError();
+        return DL_ERR_CUDA;
+    }
+    return static_cast<int>(parts);
 }
 
-template <typename T, int N, int TPR, int BLOCK>
+template <typename T, int N, int TPR, int BLOCK, int CLUSTER = 1>
 int launch(const BwdArgs<T>& a, cudaStream_t s) {
     if constexpr (N > 1) {
-        const bool full = a.width == TPR * 16 && a.vec_out;
-        const int parts = full ? launch<T, N, TPR, BLOCK, true, true>(a, s) : launch<T, N, TPR, BLOCK, true, false>(a, s);
+        const bool full = a.width == TPR * 16 * CLUSTER && a.vec_out;
+        const int parts = full ? launch_form<T, N, TPR, BLOCK, CLUSTER, true, true>(a, s)
+                               : launch_form<T, N, TPR, BLOCK, CLUSTER, true, false>(a, s);
         if (parts != 0) return parts;
     }
-    return launch<T, N, TPR, BLOCK, false, false>(a, s);
+    return launch_form<T, N, TPR, BLOCK, CLUSTER, false, false>(a, s);
 }
 
 template <typename T, int N>
 int by_width(const BwdArgs<T>& a, cudaStream_t s) {
     if (a.width <= 128) return launch<T, N, 8, 256>(a, s);
+    if (a.width <= 256) return launch<T, N, 16, 512>(a, s);
     if (a.width <= 512) return launch<T, N, 32, 512>(a, s);
     if (a.width <= 1024) return launch<T, N, 64, 512>(a, s);
     if (a.width <= 2048) return launch<T, N, 128, 512>(a, s);
     if (a.width <= 4096) return launch<T, N, 256, 512>(a, s);
     if (a.width <= 8192) return launch<T, N, 512, 512>(a, s);
+    if (a.width <= 16384) return launch<T, N, 512, 512, 2>(a, s);
     // the sums first: dx may overwrite dy
     k_norm_dw_wide<T><<<dim3((a.width + 31) / 32, kWideParts), kThreads, 0, s>>>(a);
     const int64_t most = int64_t(sm_count()) * 2;

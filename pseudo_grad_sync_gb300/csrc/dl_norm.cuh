@@ -93,14 +93,23 @@ __device__ __forceinline__ float load_param(const void* p, int32_t type, int64_t
 // Sums over the TPR threads of a row, in two halves, so that other rows' work
 // can lie between them: give() leaves the warp's sums, take() joins the warps
 // of the row. Rows of more than a warp need a block barrier between the two;
-// there are two sets of slots, used in turn.
-template <int TPR, int BLOCK>
+// there are two sets of slots, used in turn. With CLUSTER blocks per row every
+// warp leaves its sums in each block's slots, and the barrier is the cluster's.
+template <int TPR, int BLOCK, int CLUSTER = 1>
 struct RowSum {
-    static constexpr int kW = TPR / 32;
+    static constexpr int kW = TPR / 32 * CLUSTER;            // warps of a row
+    static constexpr int kSlots = BLOCK / 32 * CLUSTER;      // of a set
     static constexpr bool kShared = TPR > 32;
-    static constexpr size_t kBytes = kShared ? 2 * (BLOCK / 32) * sizeof(float2) : 0;
+    static constexpr size_t kBytes = kShared ? 2 * kSlots * sizeof(float2) : 0;
+    static_assert(CLUSTER == 1 || TPR == BLOCK, "a cluster shares one row");
     float2* red;
     float2 own;
+    __device__ __forceinline__ static void barrier() {
+        if constexpr (CLUSTER > 1)
+            asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        else
+            __syncthreads();
+    }
     __device__ __forceinline__ void give(float2 v, int set) {
         if constexpr (kShared) {
             // after the first exchange the lower half of the warp has only x
@@ -109,8 +118,19 @@ struct RowSum {
             float k = (up ? v.y : v.x) + __shfl_xor_sync(kFull, up ? v.x : v.y, 16);
 #pragma unroll
             for (int sh = 8; sh; sh >>= 1) k += __shfl_xor_sync(kFull, k, sh);
-            if ((threadIdx.x & 15) == 0)
-                reinterpret_cast<float*>(red + set * (BLOCK / 32) + (threadIdx.x >> 5))[up] = k;
+            if ((threadIdx.x & 15) == 0) {
+                if constexpr (CLUSTER == 1) {
+                    reinterpret_cast<float*>(red + set * kSlots + (threadIdx.x >> 5))[up] = k;
+                } else {
+                    const int slot = static_cast<int>(blockIdx.x % CLUSTER) * (BLOCK / 32) + (threadIdx.x >> 5);
+                    const uint32_t to = smem_addr(reinterpret_cast<float*>(red + set * kSlots + slot) + up);
+#pragma unroll
+                    for (int c = 0; c < CLUSTER; ++c)
+                        asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
+                                     "st.shared::cluster.f32 [a], %2;\n\t}" ::"r"(to), "r"(c), "f"(k)
+                                     : "memory");
+                }
+            }
         } else {
 #pragma unroll
             for (int sh = TPR / 2; sh; sh >>= 1)
@@ -125,7 +145,7 @@ struct RowSum {
         for (int sh = L / 2; sh; sh >>= 1) x += __shfl_xor_sync(kFull, x, sh);
         if constexpr (kShared) {
             if ((threadIdx.x & 31) == 0)
-                reinterpret_cast<float*>(red + set * (BLOCK / 32))[threadIdx.x >> 5] = x;
+                reinterpret_cast<float*>(red + set * kSlots)[threadIdx.x >> 5] = x;
         } else {
             own.x = x;
         }
@@ -133,7 +153,7 @@ struct RowSum {
     __device__ __forceinline__ float take1(int set) const {
         if constexpr (kShared) {
             const float2* mine = reinterpret_cast<const float2*>(
-                reinterpret_cast<const float*>(red + set * (BLOCK / 32)) + (threadIdx.x / TPR) * kW);
+                reinterpret_cast<const float*>(red + set * kSlots) + (threadIdx.x / TPR) * kW);
             float2 v = mine[0];
 #pragma unroll
             for (int w = 1; w < kW / 2; ++w) v = add2(v, mine[w]);
@@ -144,7 +164,7 @@ struct RowSum {
     }
     __device__ __forceinline__ float2 take(int set) const {
         if constexpr (kShared) {
-            const float4* mine = reinterpret_cast<const float4*>(red + set * (BLOCK / 32) + (threadIdx.x / TPR) * kW);
+            const float4* mine = reinterpret_cast<const float4*>(red + set * kSlots + (threadIdx.x / TPR) * kW);
             float2 v = make_float2(0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kW / 2; ++w) {
@@ -178,7 +198,8 @@ __device__ __forceinline__ float2 block_sum(float2 v, float2* red) {
 }
 
 // The ring of a block's rounds: each stage holds ARRAYS arrays' rows of one
-// round, [group][array][TPR * EPT elements].
+// round. Rows that follow each other in memory come in one copy per array,
+// others in one copy per row.
 template <typename T, int TPR, int EPT, int BLOCK, int ARRAYS, int STAGES>
 struct RowRing {
     static constexpr long kPolls = 1L << 17;  // of a wait: about a second
@@ -193,6 +214,7 @@ struct RowRing {
     int64_t end;  // of the block's rows
     // bytes of a row that a bulk copy takes: a last, partial pack is loaded by its owner
     uint32_t bytes;
+    uint32_t pitch;  // between a stage's rows: `bytes` when they come in one copy, else kRow
     int stage = 0;
     uint32_t parity = 0;
     bool ok = true;
@@ -205,7 +227,7 @@ struct RowRing {
         __syncthreads();
     }
     __device__ __forceinline__ unsigned char* row(int st, int group, int which) const {
-        return base + st * kStage + (group * ARRAYS + which) * kRow;
+        return base + st * kStage + which * (kGroups * kRow) + group * pitch;
     }
     // Warp 0: copies the rows of the round from `first` on, a lane per row.
     __device__ __forceinline__ void issue(int st, int64_t first, const T* p0, int64_t s0, const T* p1, int64_t s1) {
@@ -218,9 +240,10 @@ struct RowRing {
             mbar_arrive_expect_tx(full + st, n * ARRAYS * bytes);
         }
         __syncwarp();
-        if (j < n && bytes) {
-            bulk_copy_g2s(row(st, j, 0), p0 + (first + j) * s0, bytes, full + st);
-            if (ARRAYS > 1) bulk_copy_g2s(row(st, j, 1), p1 + (first + j) * s1, bytes, full + st);
+        const uint32_t size = pitch == kRow ? bytes : n * bytes;
+        if (j < (pitch == kRow ? n : 1) && bytes) {
+            bulk_copy_g2s(row(st, j, 0), p0 + (first + j) * s0, size, full + st);
+            if (ARRAYS > 1) bulk_copy_g2s(row(st, j, 1), p1 + (first + j) * s1, size, full + st);
         }
     }
     // Until the current stage holds its round. A wait that runs out sets the

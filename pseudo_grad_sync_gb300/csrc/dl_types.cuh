@@ -4,6 +4,9 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
+#include <stdlib.h>
+
+#include <atomic>
 
 #include "dl_common.cuh"
 
@@ -80,15 +83,48 @@ __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
     return floats2(r);
 }
 
-// Lets a kernel use `bytes` of dynamic shared memory; false (and no error
-// left behind for a later call) when the device refuses.
-inline bool allow_shared(const void* kernel, size_t bytes) {
-    if (bytes <= 48 * 1024 || cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(bytes)) == cudaSuccess)
-        return true;
-    cudaGetLastError();
-    return false;
-}
+// Launch geometry of one kernel with its threads and dynamic shared memory:
+// the blocks that fit the current device at once, asked for on the first call
+// per device (allowing the shared memory on the way) and kept; 0 (and no
+// error left behind for a later call) when the device refuses. One object per
+// kernel: a static local of the function that launches it.
+class Resident {
+public:
+    int blocks(const void* kernel, int threads, size_t smem) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
+        int b = kept_[dev].load(std::memory_order_acquire);
+        if (b == 0) {
+            if ((smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                          static_cast<int>(smem)) != cudaSuccess)) {
+                cudaGetLastError();
+                return 0;
+            }
+            int per_sm = 0;
+            if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess) {
+                cudaGetLastError();
+                return 0;
+            }
+            b = per_sm * sm_count();
+            kept_[dev].store(b, std::memory_order_release);
+        }
+        return b;
+    }
+    // a persistent grid: no more blocks than work items, or than DL_GRID_LIMIT
+    // (environment; tests use it to make single blocks cover much)
+    int grid(const void* kernel, int threads, size_t smem, int64_t work_items) {
+        int64_t g = blocks(kernel, threads, smem);
+        if (const char* cap = getenv("DL_GRID_LIMIT")) {
+            const long v = strtol(cap, nullptr, 10);
+            if (v > 0 && v < g) g = v;
+        }
+        return static_cast<int>(work_items < g ? work_items : g);
+    }
+
+private:
+    static constexpr int kDevices = 64;
+    std::atomic<int> kept_[kDevices] = {};
+};
 
 // p is a multiple of a (a power of two); null is
 inline bool aligned_to(const void* p, size_t a) {

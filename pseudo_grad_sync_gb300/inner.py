@@ -21,7 +21,7 @@ import math
 
 import torch
 
-from . import (Fragment, _check, _cuda, _Fragment, _need, _need_all, _ptr, _stream, _F32, _U8, lib,
+from . import (Fragment, _cuda, _Fragment, _need, _need_all, _F32, _U8, DLError, lib,
                new_workspace)
 
 DL_F32, DL_BF16, DL_F16, DL_E4M3 = 0, 1, 2, 3
@@ -32,6 +32,34 @@ DL_ADAMW_BLOCK = 128
 _TYPE = {torch.float32: DL_F32, torch.bfloat16: DL_BF16, torch.float16: DL_F16}
 _GRADS = (torch.float32, torch.bfloat16)
 _PARAMS = (torch.float32, torch.bfloat16)
+
+
+# These calls run at every layer and step, some for microseconds: their own
+# time counts. Handles are therefore taken as integers (the declared argument
+# types convert them), and the current stream without making a Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on(stream, device):
+    """cudaStream_t of stream, or of the device's current stream."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None or device.index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device.index)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _buffer(t, dtype, n, name):
+    """_need and the device check of one buffer, for the frequent case."""
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.numel() >= n
+            and t.is_contiguous()):
+        return
+    _need(t, (dtype,), n, name)
+    _cuda(t)
 
 
 class _AdamWJob(ctypes.Structure):
@@ -107,12 +135,12 @@ def grad_norm(grads, max_norm=math.inf, out=None, workspace=None, stream=None):
         out = torch.empty(2, dtype=torch.float32, device=G.grads[0].device)
     if workspace is None:
         workspace = new_workspace(grad_norm_workspace_bytes(), out.device)
-    _need(out, _F32, 2, "out")
-    _need(workspace, _U8, 0, "workspace")
-    _cuda(out, workspace)
-    _check("dl_grad_norm", lib().dl_grad_norm(
-        G._ptrs, G._numel, len(G.grads), G.type, max_norm, out.data_ptr(), workspace.data_ptr(),
-        workspace.numel(), _stream(stream)))
+    _buffer(out, torch.float32, 2, "out")
+    _buffer(workspace, torch.uint8, 0, "workspace")
+    st = lib().dl_grad_norm(G._ptrs, G._numel, len(G.grads), G.type, max_norm, out.data_ptr(),
+                            workspace.data_ptr(), workspace.numel(), _on(stream, out.device))
+    if st:
+        raise DLError("dl_grad_norm", st)
     return out
 
 
@@ -170,6 +198,9 @@ class AdamWJobs:
         _cuda(*lists.values())
         self.buffers = lists
         self._cfg = _AdamWConfig()
+        self._cfg_ref = ctypes.byref(self._cfg)
+        used = [t for x in lists.values() for t in x if t is not None]
+        self.device = used[0].device if used else torch.device("cuda", torch.cuda.current_device())
 
 
 def adamw_step(jobs: AdamWJobs, step, lr=4e-4, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1,
@@ -179,14 +210,14 @@ def adamw_step(jobs: AdamWJobs, step, lr=4e-4, betas=(0.9, 0.95), eps=1e-8, weig
     a coefficient that is not finite skips the step on the device. seed: of
     the 8-bit states' rounding; it may stay the same over a run."""
     if clip is not None:
-        _need(clip, _F32, 2, "clip")
-        _cuda(clip)
+        _buffer(clip, torch.float32, 2, "clip")
     c = jobs._cfg
-    c.lr, c.beta1, c.beta2, c.eps, c.weight_decay = lr, betas[0], betas[1], eps, weight_decay
-    c.step, c.seed = int(step), int(seed) & (2**64 - 1)
-    _check("dl_adamw_step", lib().dl_adamw_step(
-        jobs._jobs, len(jobs.frags), jobs.grad_type, jobs.state_type, ctypes.byref(c), _ptr(clip),
-        _stream(stream)))
+    c.lr, (c.beta1, c.beta2), c.eps, c.weight_decay = lr, betas, eps, weight_decay
+    c.step, c.seed = step, seed & (2**64 - 1)
+    st = lib().dl_adamw_step(jobs._jobs, len(jobs.frags), jobs.grad_type, jobs.state_type,
+                             jobs._cfg_ref, _at(clip), _on(stream, jobs.device))
+    if st:
+        raise DLError("dl_adamw_step", st)
 
 
 class InnerAdamW:
@@ -248,11 +279,11 @@ def layernorm_workspace_bytes(rows: int, width: int) -> int:
 
 
 def _rows(t, name, like=None):
-    """(tensor, row stride) of rows of a last dimension with stride 1; the
-    leading dimensions must fold into one."""
+    """(device address, row stride) of rows of a last dimension with stride 1;
+    the leading dimensions must fold into one."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dtype not in _TYPE or (like is not None and t.dtype != like.dtype):
+    if t.dtype not in _TYPE or (like is not None and t.dtype is not like.dtype):
         want = like.dtype if like is not None else "float32, bfloat16 or float16"
         raise TypeError(f"{name}: dtype {t.dtype}, expected {want}")
     if like is not None and t.shape != like.shape:
@@ -260,27 +291,47 @@ def _rows(t, name, like=None):
     if t.dim() == 0:
         raise ValueError(f"{name}: needs at least one dimension")
     width = t.shape[-1]
-    if t.is_contiguous():
-        return t, width
-    if t.dim() != 2:
-        try:
-            t = t.view(-1, width)
-        except RuntimeError:
-            raise ValueError(f"{name}: the leading dimensions do not fold into rows") from None
-    if t.stride(1) != 1 and width > 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    if t.shape[0] > 1 and t.stride(0) < width:
-        raise ValueError(f"{name}: rows overlap (stride {t.stride(0)}, width {width})")
-    return t, max(t.stride(0), width)
+    if width < 1:
+        raise ValueError(f"{name}: the last dimension is empty")
+    stride = width
+    if not t.is_contiguous():
+        if t.dim() != 2:
+            try:
+                t = t.view(-1, width)
+            except RuntimeError:
+                raise ValueError(f"{name}: the leading dimensions do not fold into rows") from None
+        if t.stride(1) != 1 and width > 1:
+            raise ValueError(f"{name}: the last dimension must be contiguous")
+        if t.shape[0] > 1 and t.stride(0) < width:
+            raise ValueError(f"{name}: rows overlap (stride {t.stride(0)}, width {width})")
+        stride = max(t.stride(0), width)
+    if not t.is_cuda:
+        return None, stride  # refused by the caller, after its other checks
+    return t.data_ptr(), stride
 
 
 def _params(weight, bias, width):
-    _need(weight, _PARAMS, width, "weight")
-    if weight is None or weight.numel() != width:
+    """Type code of the parameters; their device is checked by the caller."""
+    if not isinstance(weight, torch.Tensor) or weight.numel() != width:
         raise ValueError(f"weight: expected {width} elements")
-    if bias is not None:
+    if weight.dtype not in _PARAMS or not weight.is_contiguous():
+        _need(weight, _PARAMS, width, "weight")
+    if bias is not None and (bias.dtype is not weight.dtype or bias.numel() < width
+                             or not bias.is_contiguous()):
         _need(bias, (weight.dtype,), width, "bias")
     return _TYPE[weight.dtype]
+
+
+def _stats(mean, rstd, rows, rms):
+    """Checks of the rows' statistics; returns mean, or None for the RMS norm."""
+    if rms:
+        mean = None
+    elif mean is None:
+        raise ValueError("mean: missing (rms=False)")
+    else:
+        _need(mean, _F32, rows, "mean")
+    _need(rstd, _F32, rows, "rstd")
+    return mean
 
 
 def layernorm_forward(x, weight, bias=None, eps=1e-5, rms=False, y=None, mean=None, rstd=None,
@@ -288,28 +339,36 @@ def layernorm_forward(x, weight, bias=None, eps=1e-5, rms=False, y=None, mean=No
     """Layer norm over the last dimension (dl_layernorm_forward). Returns
     (y, mean, rstd), mean None with rms=True. x: float32, bfloat16 or float16
     with a contiguous last dimension; weight, bias: float32 or bfloat16."""
-    xr, xs = _rows(x, "x")
-    width = x.shape[-1]
-    if width < 1:
-        raise ValueError("x: the last dimension is empty")
+    xp, xs = _rows(x, "x")
+    shape = x.shape
+    width = shape[-1]
     rows = x.numel() // width
     ptype = _params(weight, bias, width)
+    device = x.device
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    yr, ys = _rows(y, "y", x)
-    if rstd is None:
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    if rms:
-        mean = None
-    elif mean is None:
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    _need(mean, _F32, rows, "mean")
-    _need(rstd, _F32, rows, "rstd")
-    _cuda(x, weight, bias, y, mean, rstd)
-    _check("dl_layernorm_forward", lib().dl_layernorm_forward(
-        xr.data_ptr(), xs, _TYPE[x.dtype], rows, width, weight.data_ptr(), _ptr(bias), ptype, eps,
-        DL_NORM_RMS if rms else 0, yr.data_ptr(), ys, _ptr(mean), rstd.data_ptr(),
-        _stream(stream)))
+        y = torch.empty(shape, dtype=x.dtype, device=device)
+        yp, ys = (y.data_ptr() if xp is not None else None), width
+    else:
+        yp, ys = _rows(y, "y", x)
+    if rstd is None and (rms or mean is None):
+        # both statistics in one allocation
+        both = torch.empty((1 if rms else 2, *shape[:-1]), dtype=torch.float32, device=device)
+        rstd = both[0]
+        mean = None if rms else both[1]
+    else:
+        if rstd is None:
+            rstd = torch.empty(shape[:-1], dtype=torch.float32, device=device)
+        if mean is None and not rms:
+            mean = torch.empty(shape[:-1], dtype=torch.float32, device=device)
+        mean = _stats(mean, rstd, rows, rms)
+    if xp is None or yp is None or not (weight.is_cuda and rstd.is_cuda and (
+            bias is None or bias.is_cuda) and (mean is None or mean.is_cuda)):
+        _cuda(x, weight, bias, y, mean, rstd)
+    st = lib().dl_layernorm_forward(xp, xs, _TYPE[x.dtype], rows, width, weight.data_ptr(),
+                                    _at(bias), ptype, eps, DL_NORM_RMS if rms else 0, yp, ys,
+                                    _at(mean), rstd.data_ptr(), _on(stream, device))
+    if st:
+        raise DLError("dl_layernorm_forward", st)
     return y, mean, rstd
 
 
@@ -320,40 +379,41 @@ def layernorm_backward(dy, x, weight, mean, rstd, dweight=None, dbias=None, rms=
     gradient buffer; with accumulate=True the sums are added to what they
     hold. Without a dweight both are allocated (dbias only with bias=True);
     a call that passes dweight alone computes no dbias."""
-    xr, xs = _rows(x, "x")
-    dyr, ds = _rows(dy, "dy", x)
+    xp, xs = _rows(x, "x")
+    dyp, ds = _rows(dy, "dy", x)
     width = x.shape[-1]
-    if width < 1:
-        raise ValueError("x: the last dimension is empty")
     rows = x.numel() // width
     ptype = _params(weight, None, width)
+    device = x.device
     if dweight is None:
         if accumulate:
             raise ValueError("accumulate: needs the dweight to add to")
-        dweight = torch.empty(width, dtype=weight.dtype, device=x.device)
+        dweight = torch.empty(width, dtype=weight.dtype, device=device)
         if dbias is None and bias:
-            dbias = torch.empty(width, dtype=weight.dtype, device=x.device)
+            dbias = torch.empty(width, dtype=weight.dtype, device=device)
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    dxr, os = _rows(dx, "dx", x)
+        dx = torch.empty(x.shape, dtype=x.dtype, device=device)
+        dxp, os = (dx.data_ptr() if xp is not None else None), width
+    else:
+        dxp, os = _rows(dx, "dx", x)
     if workspace is None:
         workspace = torch.empty(layernorm_workspace_bytes(rows, width), dtype=torch.uint8,
-                                device=x.device)
-    if rms:
-        mean = None
-    elif mean is None:
-        raise ValueError("mean: missing (rms=False)")
-    _need(mean, _F32, rows, "mean")
-    _need(rstd, _F32, rows, "rstd")
+                                device=device)
+    mean = _stats(mean, rstd, rows, rms)
     _need(dweight, (weight.dtype,), width, "dweight")
     _need(dbias, (weight.dtype,), width, "dbias")
     _need(workspace, _U8, 0, "workspace")
-    _cuda(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace)
+    if xp is None or dyp is None or dxp is None or not (
+            weight.is_cuda and rstd.is_cuda and dweight.is_cuda and workspace.is_cuda
+            and (mean is None or mean.is_cuda) and (dbias is None or dbias.is_cuda)):
+        _cuda(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace)
     flags = (DL_NORM_RMS if rms else 0) | (DL_NORM_ACCUMULATE if accumulate else 0)
-    _check("dl_layernorm_backward", lib().dl_layernorm_backward(
-        dyr.data_ptr(), ds, xr.data_ptr(), xs, _TYPE[x.dtype], rows, width, weight.data_ptr(),
-        ptype, _ptr(mean), rstd.data_ptr(), flags, dxr.data_ptr(), os, dweight.data_ptr(),
-        _ptr(dbias), workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    st = lib().dl_layernorm_backward(
+        dyp, ds, xp, xs, _TYPE[x.dtype], rows, width, weight.data_ptr(), ptype, _at(mean),
+        rstd.data_ptr(), flags, dxp, os, dweight.data_ptr(), _at(dbias), workspace.data_ptr(),
+        workspace.numel(), _on(stream, device))
+    if st:
+        raise DLError("dl_layernorm_backward", st)
     return dx, dweight, dbias
 
 
