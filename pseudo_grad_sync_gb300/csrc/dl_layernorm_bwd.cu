@@ -146,6 +146,8 @@ __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdA
         }
     }
     if constexpr (BULK) ring.drain();
+    // the join's blocks may take the place of those that end from here on
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // the block's sums over its rows
     float* part = a.part + part_of * 2 * a.width + off;
     if constexpr (kGroups == 1) {
@@ -191,15 +193,16 @@ __global__ void __launch_bounds__(kThreads)
     const int c = blockIdx.x * 32 + lane;
     const float* from = part + int64_t(blockIdx.y) * width + c;
     float s = 0.f;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // until the partial sums are all there
     if (c < width) {
         int p = warp;
         for (; p + 3 * kWarps < parts; p += 4 * kWarps) {
             float v[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) v[u] = __ldg(from + int64_t(p + u * kWarps) * 2 * width);
+            for (int u = 0; u < 4; ++u) v[u] = __ldcg(from + int64_t(p + u * kWarps) * 2 * width);
             s += (v[0] + v[1]) + (v[2] + v[3]);
         }
-        for (; p < parts; p += kWarps) s += __ldg(from + int64_t(p) * 2 * width);
+        for (; p < parts; p += kWarps) s += __ldcg(from + int64_t(p) * 2 * width);
     }
     red[warp][lane] = s;
     __syncthreads();
@@ -378,7 +381,21 @@ extern "C" int dl_layernorm_backward(const void* dy, int64_t dy_stride, const vo
     if (rows > 0)
         parts = x_type == DL_F32 ? call(float()) : x_type == DL_BF16 ? call(__nv_bfloat16()) : call(__half());
     if (parts < 0) return parts;
-    k_norm_join<<<dim3((width + 31) / 32, dbias ? 2 : 1), kThreads, 0, s>>>(part, parts, width, param_type,
-                                                                          accumulate, dweight, dbias);
-    return launch_status();
+    // Launched while the pass before it runs (its blocks wait for that pass's
+    // end): the launch's latency is not added to the call.
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3((width + 31) / 32, dbias ? 2 : 1);
+    config.blockDim = dim3(kThreads);
+    config.stream = s;
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    config.attrs = &early;
+    config.numAttrs = 1;
+    if (cudaLaunchKernelEx(&config, k_norm_join, static_cast<const float*>(part), parts, static_cast<int>(width),
+                           param_type, accumulate, dweight, dbias) != cudaSuccess) {
+        cudaGetLastError();
+        return DL_ERR_CUDA;
+    }
+    return DL_OK;
 }

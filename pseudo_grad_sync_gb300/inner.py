@@ -310,6 +310,12 @@ def _rows(t, name, like=None):
     return t.data_ptr(), stride
 
 
+def _empty_like(x):
+    """A contiguous tensor of x's shape and type."""
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype,
+                                                                     device=x.device)
+
+
 def _params(weight, bias, width):
     """Type code of the parameters; their device is checked by the caller."""
     if not isinstance(weight, torch.Tensor) or weight.numel() != width:
@@ -346,20 +352,18 @@ def layernorm_forward(x, weight, bias=None, eps=1e-5, rms=False, y=None, mean=No
     ptype = _params(weight, bias, width)
     device = x.device
     if y is None:
-        y = torch.empty(shape, dtype=x.dtype, device=device)
+        y = _empty_like(x)
         yp, ys = (y.data_ptr() if xp is not None else None), width
     else:
         yp, ys = _rows(y, "y", x)
-    if rstd is None and (rms or mean is None):
-        # both statistics in one allocation
-        both = torch.empty((1 if rms else 2, *shape[:-1]), dtype=torch.float32, device=device)
-        rstd = both[0]
-        mean = None if rms else both[1]
-    else:
-        if rstd is None:
-            rstd = torch.empty(shape[:-1], dtype=torch.float32, device=device)
-        if mean is None and not rms:
-            mean = torch.empty(shape[:-1], dtype=torch.float32, device=device)
+    given = rstd is not None or mean is not None
+    if rstd is None:
+        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=device)
+    if rms:
+        mean = None
+    elif mean is None:
+        mean = torch.empty(shape[:-1], dtype=torch.float32, device=device)
+    if given:
         mean = _stats(mean, rstd, rows, rms)
     if xp is None or yp is None or not (weight.is_cuda and rstd.is_cuda and (
             bias is None or bias.is_cuda) and (mean is None or mean.is_cuda)):
@@ -392,7 +396,7 @@ def layernorm_backward(dy, x, weight, mean, rstd, dweight=None, dbias=None, rms=
         if dbias is None and bias:
             dbias = torch.empty(width, dtype=weight.dtype, device=device)
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=device)
+        dx = _empty_like(x)
         dxp, os = (dx.data_ptr() if xp is not None else None), width
     else:
         dxp, os = _rows(dx, "dx", x)
