@@ -533,6 +533,9 @@ int dl_adamw_step(const dl_adamw_job* jobs, int32_t n_jobs, int32_t grad_type, i
  * Pointers need the alignment of their elements only (weights may lie
  * anywhere in a fragment's flat buffer); 16-byte aligned rows are faster.
  * y may be x itself (same stride). rows = 0 is a no-op; width >= 1.
+ * Long calls stage rows by bulk copies whose waits are bounded; a wait that
+ * runs out sets a bit in the library's own status word (as this call has no
+ * workspace), read with dl_read_device_status(NULL, ...).
  */
 int dl_layernorm_forward(const void* x, int64_t x_stride, int32_t x_type, int64_t rows,
                          int32_t width, const void* weight, const void* bias, int32_t param_type,
@@ -555,7 +558,9 @@ size_t dl_layernorm_workspace_bytes(int64_t rows, int32_t width);
  *                ignored with DL_NORM_RMS)
  *   dweight      device [width] of param_type, in/out
  *   dbias        the same, or NULL where there is no bias
- *   d_workspace  device scratch of dl_layernorm_workspace_bytes(rows, width) bytes
+ *   d_workspace  device scratch of dl_layernorm_workspace_bytes(rows, width)
+ *                bytes; its first word is the device status word, the rest
+ *                needs no initialisation
  * rows = 0 writes zero gradients (accumulating: leaves them).
  */
 int dl_layernorm_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,

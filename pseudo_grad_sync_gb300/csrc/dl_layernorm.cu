@@ -36,6 +36,14 @@ struct FwdGeometry {
 // A round: the row's sum, a barrier, the sum of its squared deviations, a
 // barrier, and the result from the deviations, still in registers. FULL: the
 // threads' packs cover the width exactly and y's rows are aligned.
+//
+// Bound by HBM on paper (two passes of the row's bytes); what it fights is
+// the latency of two dependent sums per row. 32 elements per thread halve the
+// instructions per element against 16 (92 us at three blocks per SM); two
+// blocks of 256 threads per SM work on four rows of 4096 at once; three
+// stages (two: 120 us, four: 101 us).
+// 32768 x 4096 bf16: 88 us, 6.1 TB/s (90% of the copy rate); fp32 180 us (88%).
+// A few rows (5 x 2048): 3.9 us on the device.
 template <typename T, int N, int TPR, int EPT, int BLOCK, bool BULK, bool FULL>
 __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) k_norm_fwd(const __grid_constant__ FwdArgs<T> a) {
     using Geo = FwdGeometry<T, TPR, EPT, BLOCK, BULK>;
