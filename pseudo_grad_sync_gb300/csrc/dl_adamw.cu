@@ -551,8 +551,7 @@ __device__ __forceinline__ void shifted(const Pack<__nv_bfloat16, 4>* q, float2 
 }
 
 // `count` whole blocks from element `begin` (begin % 4 == A), slot `slot` on.
-// For A > 0 the first quad's leading A elements must be this warp's own or
-// not be written by anyone else.
+// For A > 0 the A elements before `begin` are of a block that this warp did.
 template <typename G, int A>
 __device__ __forceinline__ void run_blocks(const AdamArgs& a, const AdamJob& J, float coef, float keep,
                                            int64_t begin, int64_t slot, int count, int lane,
@@ -584,9 +583,21 @@ __device__ __forceinline__ void run_blocks(const AdamArgs& a, const AdamJob& J, 
         copy_commit();
     }
     uint64_t counter = a.key + ((J.slot0 + slot) * (kBlock / 4) + lane) * kGolden;
-    // what the previous block's last lane left of a quad (lane 0 only)
+    // What the block before left of this block's first quad (lane 0 only): the
+    // warp wrote it, and lane 0 writes it again with the rest of the quad.
     float left[A + 1];
     uint32_t left_m = 0, left_s = 0;
+    if constexpr (A > 0) {
+        __syncwarp();
+        if (lane == 0) {
+#pragma unroll
+            for (int k = 0; k < A; ++k) {
+                left[k] = th[k];
+                left_m |= uint32_t(m8[k]) << (8 * (4 - A + k));
+                left_s |= uint32_t(s8[k]) << (8 * (4 - A + k));
+            }
+        }
+    }
     Stage<G>* st = ring;                     // the block's stage
     Stage<G>* freed = ring + (kStages - 1);  // the one of the block before
 #pragma unroll 1
@@ -608,7 +619,6 @@ __device__ __forceinline__ void run_blocks(const AdamArgs& a, const AdamJob& J, 
         counter += (kBlock / 4) * kGolden;
         float out[4] = {q.th[0].x, q.th[0].y, q.th[1].x, q.th[1].y};
         const int o = i * kBlock;
-        bool whole = true;
         if constexpr (A > 0) {
             // quads as they lie in memory: the lane before gives the first A elements
             const int from = (lane + 31) & 31;
@@ -618,7 +628,6 @@ __device__ __forceinline__ void run_blocks(const AdamArgs& a, const AdamJob& J, 
 #pragma unroll
             for (int k = 0; k < A; ++k) got[k] = __shfl_sync(kFull, own[4 - A + k], from);
             const uint32_t pm = __shfl_sync(kFull, q.cm, from), ps = __shfl_sync(kFull, q.cs, from);
-            whole = lane > 0 || i > 0;
 #pragma unroll
             for (int k = 0; k < 4; ++k) out[k] = k < A ? (lane ? got[k] : left[k]) : own[k - A];
             q.cm = __funnelshift_l(lane ? pm : left_m, q.cm, 8 * A);
@@ -627,20 +636,10 @@ __device__ __forceinline__ void run_blocks(const AdamArgs& a, const AdamJob& J, 
             for (int k = 0; k < A; ++k) left[k] = got[k];
             left_m = pm, left_s = ps;
         }
-        if (whole) {
-            store4(th + o, out);
-            *reinterpret_cast<uint32_t*>(m8 + o) = q.cm;
-            *reinterpret_cast<uint32_t*>(s8 + o) = q.cs;
-            if (copy) store4(copy + o, out);
-        } else {
-#pragma unroll
-            for (int k = A; k < 4; ++k) {
-                th[o + k] = out[k];
-                m8[o + k] = static_cast<uint8_t>(q.cm >> (8 * k));
-                s8[o + k] = static_cast<uint8_t>(q.cs >> (8 * k));
-                if (copy) copy[o + k] = __float2bfloat16_rn(out[k]);
-            }
-        }
+        store4(th + o, out);
+        *reinterpret_cast<uint32_t*>(m8 + o) = q.cm;
+        *reinterpret_cast<uint32_t*>(s8 + o) = q.cs;
+        if (copy) store4(copy + o, out);
         if (lane < 2) sc[i] = block_scale(lane ? stop : mtop);
     }
     if (A > 0 && lane == 0) {

@@ -226,6 +226,7 @@ int by_width(const FwdArgs<T>& a, cudaStream_t s) {
     if (a.width <= 1024) return launch<T, N, 32, 32, 256>(a, s);
     if (a.width <= 2048) return launch<T, N, 64, 32, 256>(a, s);
     if (a.width <= 4096) return launch<T, N, 128, 32, 256>(a, s);
+    if (a.width <= 6144) return launch<T, N, 192, 32, 384>(a, s);
     if (a.width <= 8192) return launch<T, N, 256, 32, 256>(a, s);
     if (a.width <= 16384) return launch<T, N, 512, 32, 512>(a, s);
     const int64_t most = int64_t(sm_count()) * 2;

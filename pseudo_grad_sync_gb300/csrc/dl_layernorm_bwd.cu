@@ -328,6 +328,7 @@ int by_width(const BwdArgs<T>& a, cudaStream_t s) {
     if (a.width <= 1024) return launch<T, N, 64, 512>(a, s);
     if (a.width <= 2048) return launch<T, N, 128, 512>(a, s);
     if (a.width <= 4096) return launch<T, N, 256, 512>(a, s);
+    if (a.width <= 6144) return launch<T, N, 384, 384>(a, s);
     if (a.width <= 8192) return launch<T, N, 512, 512>(a, s);
     if (a.width <= 16384) return launch<T, N, 512, 512, 2>(a, s);
     // the sums first: dx may overwrite dy

@@ -128,6 +128,9 @@ def grad_norm(grads, max_norm=math.inf, out=None, workspace=None, stream=None):
     device float32 tensor (norm, coefficient), the ``clip`` of adamw_step.
     workspace: of grad_norm_workspace_bytes(), zeroed when allocated
     (new_workspace); calls on different streams need their own."""
+    if stream is not None:  # what is allocated here belongs to that stream
+        with torch.cuda.stream(stream):
+            return grad_norm(grads, max_norm, out, workspace)
     G = grads if isinstance(grads, GradList) else GradList(grads)
     if out is None:
         if not G.grads:
@@ -138,7 +141,7 @@ def grad_norm(grads, max_norm=math.inf, out=None, workspace=None, stream=None):
     _buffer(out, torch.float32, 2, "out")
     _buffer(workspace, torch.uint8, 0, "workspace")
     st = lib().dl_grad_norm(G._ptrs, G._numel, len(G.grads), G.type, max_norm, out.data_ptr(),
-                            workspace.data_ptr(), workspace.numel(), _on(stream, out.device))
+                            workspace.data_ptr(), workspace.numel(), _on(None, out.device))
     if st:
         raise DLError("dl_grad_norm", st)
     return out
@@ -345,6 +348,9 @@ def layernorm_forward(x, weight, bias=None, eps=1e-5, rms=False, y=None, mean=No
     """Layer norm over the last dimension (dl_layernorm_forward). Returns
     (y, mean, rstd), mean None with rms=True. x: float32, bfloat16 or float16
     with a contiguous last dimension; weight, bias: float32 or bfloat16."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return layernorm_forward(x, weight, bias, eps, rms, y, mean, rstd)
     xp, xs = _rows(x, "x")
     shape = x.shape
     width = shape[-1]
@@ -370,7 +376,7 @@ def layernorm_forward(x, weight, bias=None, eps=1e-5, rms=False, y=None, mean=No
         _cuda(x, weight, bias, y, mean, rstd)
     st = lib().dl_layernorm_forward(xp, xs, _TYPE[x.dtype], rows, width, weight.data_ptr(),
                                     _at(bias), ptype, eps, DL_NORM_RMS if rms else 0, yp, ys,
-                                    _at(mean), rstd.data_ptr(), _on(stream, device))
+                                    _at(mean), rstd.data_ptr(), _on(None, device))
     if st:
         raise DLError("dl_layernorm_forward", st)
     return y, mean, rstd
@@ -383,6 +389,10 @@ def layernorm_backward(dy, x, weight, mean, rstd, dweight=None, dbias=None, rms=
     gradient buffer; with accumulate=True the sums are added to what they
     hold. Without a dweight both are allocated (dbias only with bias=True);
     a call that passes dweight alone computes no dbias."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return layernorm_backward(dy, x, weight, mean, rstd, dweight, dbias, rms, accumulate,
+                                      dx, workspace, bias)
     xp, xs = _rows(x, "x")
     dyp, ds = _rows(dy, "dy", x)
     width = x.shape[-1]
@@ -415,7 +425,7 @@ def layernorm_backward(dy, x, weight, mean, rstd, dweight=None, dbias=None, rms=
     st = lib().dl_layernorm_backward(
         dyp, ds, xp, xs, _TYPE[x.dtype], rows, width, weight.data_ptr(), ptype, _at(mean),
         rstd.data_ptr(), flags, dxp, os, dweight.data_ptr(), _at(dbias), workspace.data_ptr(),
-        workspace.numel(), _on(stream, device))
+        workspace.numel(), _on(None, device))
     if st:
         raise DLError("dl_layernorm_backward", st)
     return dx, dweight, dbias

@@ -656,6 +656,32 @@ def test_inner_calls_on_another_stream(dl):
         assert torch.equal(P[k][0].view(torch.uint8), Q[k][0].view(torch.uint8)), k
 
 
+def test_what_a_call_allocates_belongs_to_its_stream(dl):
+    """A call on a given stream without a workspace or outputs, while the
+    current stream is busy: its scratch is zeroed and used on that stream."""
+    s = torch.cuda.Stream()
+    g = to_cuda(np.random.default_rng(3).standard_normal(300_000))
+    x, w = g[:65536].view(64, 1024), to_cuda(np.ones(1024))
+    want, (y, mean, rstd) = dl.grad_norm([g], 1.0), dl.layernorm_forward(x, w)
+    d = dl.layernorm_backward(x, x, w, mean, rstd)
+    dl.grad_norm([g], 1.0, stream=s)  # the stream's first allocations
+    dl.layernorm_backward(x, x, w, *dl.layernorm_forward(x, w, stream=s)[1:], stream=s)
+    for size in (256, dl.grad_norm_workspace_bytes(), 1 << 20):  # blocks that are not zero when reused
+        torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)
+    a = dl.grad_norm([g], 1.0, stream=s)
+    y2, mean2, rstd2 = dl.layernorm_forward(x, w, stream=s)
+    d2 = dl.layernorm_backward(x, x, w, mean2, rstd2, stream=s)
+    s.synchronize()
+    busy = not torch.cuda.current_stream().query()
+    with torch.cuda.stream(s):
+        assert torch.equal(a, want) and torch.equal(y, y2) and torch.equal(rstd, rstd2)
+        assert all(torch.equal(p, q) for p, q in zip(d, d2))
+    assert busy  # the comparison did not wait for the current stream
+    torch.cuda.synchronize()
+
+
 def test_inner_calls_in_a_graph(dl):
     """Captured once and replayed: the clip, a step and a norm give what the
     same calls give outside a graph."""
