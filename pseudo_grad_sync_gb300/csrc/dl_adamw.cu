@@ -817,6 +817,11 @@ extern "C" int dl_grad_norm(const void* const* grads, const int64_t* numel, int3
         int grid = resident[grad_type].grid(kernel, kThreads, 0, chunks ? chunks : 1);
         if (grid == 0) return DL_ERR_CUDA;
         if (grid > kNormBlocks) grid = kNormBlocks;
+        // Half the blocks read as fast until a call is long, and their end
+        // (ticket, join of the partial sums) is shorter: 80 MB 22.0 -> 19.4 us,
+        // 320 MB 54.5 -> 52.7, but 2.2 GB 310 -> 318.
+        const int few = 4 * sm_count();
+        if (grid > few && chunks < int64_t(few) * 32) grid = few;
         void* args[] = {&a};
         if (cudaLaunchKernel(kernel, dim3(grid), dim3(kThreads), args, 0,
                              static_cast<cudaStream_t>(stream)) != cudaSuccess) {

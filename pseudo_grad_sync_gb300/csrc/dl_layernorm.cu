@@ -101,10 +101,13 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) k_norm_fwd(const __grid_co
                 const int c = (k * TPR + t) * N;
                 if (FULL || (in && c + N <= a.width)) {
                     raw[k] = from[k * TPR];  // FULL: a stage's rows past the last are stale and not used
-                } else {  // a last, partial pack; zeros past the width and the rows
+                } else {  // zeros past the width and the rows
 #pragma unroll
-                    for (int i = 0; i < N; ++i)
-                        raw[k].v[i] = in && c + i < a.width ? a.x[r * a.xs + c + i] : from_f32<T>(0.f);
+                    for (int i = 0; i < N; ++i) raw[k].v[i] = from_f32<T>(0.f);
+                    if (N > 1 && in && c < a.width)  // a last, partial pack
+#pragma unroll
+                        for (int i = 0; i < N - 1; ++i)
+                            if (c + i < a.width) raw[k].v[i] = a.x[r * a.xs + c + i];
                 }
             }
 #pragma unroll

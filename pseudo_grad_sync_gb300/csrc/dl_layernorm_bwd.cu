@@ -118,13 +118,16 @@ __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdA
             const int c = column(k);
             if (in && (FULL || c + N <= width)) {
                 dyp[k] = from0[k * TPR], xp[k] = from1[k * TPR];
-            } else {  // a last, partial pack; zeros past the width and the rows
+            } else {  // zeros past the width and the rows
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const bool el = in && c + i < width;
-                    dyp[k].v[i] = el ? dy[r * a.ds + c + i] : from_f32<T>(0.f);
-                    xp[k].v[i] = el ? x[r * a.xs + c + i] : from_f32<T>(0.f);
-                }
+                for (int i = 0; i < N; ++i) dyp[k].v[i] = xp[k].v[i] = from_f32<T>(0.f);
+                if (N > 1 && in && c < width)  // a last, partial pack
+#pragma unroll
+                    for (int i = 0; i < N - 1; ++i)
+                        if (c + i < width) {
+                            dyp[k].v[i] = dy[r * a.ds + c + i];
+                            xp[k].v[i] = x[r * a.xs + c + i];
+                        }
             }
         }
         float2 s2 = make_float2(0.f, 0.f), q2 = s2;
