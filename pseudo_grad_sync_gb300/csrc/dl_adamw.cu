@@ -713,8 +713,8 @@ __device__ __forceinline__ void any_block(const AdamArgs& a, const AdamJob& J, f
 // Runs of 32 blocks, scheduled by the hardware; equal shares for a persistent
 // grid took 1211 us, runs of 16 about 1600. Four blocks of threads per SM (64
 // registers) against three: 1107 and 1161 us.
-// 415M-element fragment (bf16 gradients and copy): 1101 us, 6.1 TB/s (90% of
-// the copy rate); 2000 ragged tensors (48M elements, fp32 gradients): 174 us,
+// 415M-element fragment (bf16 gradients and copy): 1110 us, 6.0 TB/s (89% of
+// the copy rate); 2000 ragged tensors (48M elements, fp32 gradients): 176 us,
 // 4.4 TB/s (65%): 310 instructions per block with the shifts, issued at the
 // same 65%, against 310 slots that HBM leaves there.
 template <typename G>

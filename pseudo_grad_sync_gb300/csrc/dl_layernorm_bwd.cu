@@ -53,8 +53,8 @@ struct BwdGeometry {
 // thread kept the shared-memory pipe at 63% and the call at 180 us. The row
 // sums' exchange halves its shuffles by giving each half of the warp one sum.
 // 32768 x 4096 bf16: 128 us with the join, 6.3 TB/s (92% of the copy rate);
-// fp32 255 us (93%); 8192 x 14336 bf16 212 us (49%: one barrier of the
-// cluster per row).
+// fp32 255 us (93%); 8192 x 14336 bf16 197 us (53%: one barrier of the
+// cluster per row; clusters of four blocks of 256 threads: 598 us).
 template <typename T, int N, int TPR, int BLOCK, bool BULK, bool FULL, int CLUSTER>
 __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdArgs<T> a) {
     using Geo = BwdGeometry<T, TPR, BLOCK, BULK, CLUSTER>;

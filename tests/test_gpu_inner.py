@@ -422,6 +422,7 @@ WIDTHS = [1, 2, 3, 8, 31, 33, 64, 100, 257, 512, 1000, 1024, 2047, 2048, 4096, 5
 def test_layernorm(dl, width, kind, param):
     rng = np.random.default_rng(width)
     for rows, pad, rms, bias in ((1, 0, False, True), (5, 1, True, False), (37, 64, False, False),
+                                 (23, 2, False, True),
                                  (300 if width <= 5001 else 160, 0, True, True)):
         x = _rows(rng, rows, width, kind, pad)
         w = to_cuda(1 + 0.3 * rng.standard_normal(width), param)
