@@ -89,6 +89,8 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) k_norm_fwd(const __grid_co
     int set = 0;
     for (int64_t first = begin; first < end; first += kGroups) {
         const int64_t r = first + group;
+        // unaligned 16384 x 5001 bf16 130 -> 106 us, but 32768 x 4096 fp32 178 -> 188 without the bound
+        if constexpr (!BULK && TPR >= 192) prefetch_rows(first + kGroups, kGroups, end, a.x, a.xs, a.width);
         const bool in = kGroups == 1 || r < end;
         float2 x[kPairs];
         if constexpr (BULK) ring.wait();

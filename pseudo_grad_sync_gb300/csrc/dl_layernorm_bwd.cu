@@ -97,6 +97,11 @@ __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdA
     int set = 0, at = kStatRows;
     for (int64_t first = begin; first < end; first += kGroups, at += kGroups) {
         const int64_t r = first + group;
+        // unaligned 32768 x 4096 bf16 257 -> 194 us, but 60000 x 501 53 -> 64 without the bound
+        if constexpr (!BULK && TPR >= 64) {
+            prefetch_rows(first + kGroups, kGroups, end, dy, a.ds, width);
+            prefetch_rows(first + kGroups, kGroups, end, x, a.xs, width);
+        }
         const bool in = kGroups == 1 || r < end;
         if (at == kStatRows) {  // the next rows' statistics
             __syncthreads();

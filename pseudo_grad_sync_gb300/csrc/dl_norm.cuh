@@ -197,6 +197,21 @@ __device__ __forceinline__ float2 block_sum(float2 v, float2* red) {
     return v;
 }
 
+// Rows loaded straight into registers: warp 0 has the next round's rows brought
+// to L2 meanwhile, a lane per row (the 16-byte aligned inside of each). It pays
+// where a round is few long rows.
+template <typename T>
+__device__ __forceinline__ void prefetch_rows(int64_t first, int groups, int64_t end, const T* p, int64_t stride,
+                                              int width) {
+    if (threadIdx.x >= 32) return;
+    const int64_t r = first + threadIdx.x;
+    if (static_cast<int>(threadIdx.x) >= groups || r >= end) return;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p + r * stride);
+    const uintptr_t lo = (at + 15) & ~uintptr_t(15), hi = (at + width * sizeof(T)) & ~uintptr_t(15);
+    if (hi > lo)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(lo), "r"(static_cast<uint32_t>(hi - lo))
+                     : "memory");
+}
 // The ring of a block's rounds: each stage holds ARRAYS arrays' rows of one
 // round. Rows that follow each other in memory come in one copy per array,
 // others in one copy per row.
