@@ -509,7 +509,7 @@ __device__ __forceinline__ void step_quad(const AdamArgs& a, float coef, float k
 // memory that asynchronous copies fill some blocks ahead; a stage holds the
 // aligned groups of four elements ("quads") that a block touches: 32, or 33
 // when the block starts A = 1, 2 or 3 elements into its first quad.
-constexpr int kStages = 4;
+constexpr int kStages = 5;
 constexpr int64_t kMostRun = 32;  // slots of a warp: 16 KB of theta (34 instead: 4% slower)
 
 template <typename G>
@@ -600,7 +600,7 @@ __device__ __forceinline__ void run_blocks(const AdamArgs& a, const AdamJob& J, 
     }
     Stage<G>* st = ring;                     // the block's stage
     Stage<G>* freed = ring + (kStages - 1);  // the one of the block before
-#pragma unroll 1
+#pragma unroll (A == 0 ? 2 : 1)
     for (int i = 0; i < count; ++i) {
         copy_wait<kStages - 2>();
         __syncwarp();  // the stage has every lane's copies, and `freed` every lane's reads
@@ -711,14 +711,17 @@ __device__ __forceinline__ void any_block(const AdamArgs& a, const AdamJob& J, f
 // of a tensor that starts off a multiple of four elements go through the same
 // ring as shifted quads (element by element: 233 us for the ragged set).
 // Runs of 32 blocks, scheduled by the hardware; equal shares for a persistent
-// grid took 1211 us, runs of 16 about 1600. Four blocks of threads per SM (64
-// registers) against three: 1107 and 1161 us.
-// 415M-element fragment (bf16 gradients and copy): 1110 us, 6.0 TB/s (89% of
-// the copy rate); 2000 ragged tensors (48M elements, fp32 gradients): 176 us,
-// 4.4 TB/s (65%): 310 instructions per block with the shifts, issued at the
-// same 65%, against 310 slots that HBM leaves there.
+// grid took 1211 us, runs of 16 about 1600. Three blocks of threads per SM (80
+// registers) with five stages against four (64) with four: the same 1115 us
+// there, but the 1.1B set with fp32 gradients 3221 against 3293 and the ragged
+// set 170 against 177. The loop of unshifted blocks is unrolled twice; the
+// shifted ones' is not (194 us: the instruction cache holds three of them).
+// 415M-element fragment (bf16 gradients and copy): 1115 us, 6.0 TB/s (88% of
+// the copy rate); 2000 ragged tensors (48M elements, fp32 gradients): 170 us,
+// 4.6 TB/s (67%): some 310 instructions per block with the shifts, against
+// 310 issue slots that HBM leaves there.
 template <typename G>
-__global__ void __launch_bounds__(kThreads, 4) k_adamw8(const __grid_constant__ AdamArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) k_adamw8(const __grid_constant__ AdamArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     const float coef = clip_coef(a);
     if (!isfinite(coef)) return;
