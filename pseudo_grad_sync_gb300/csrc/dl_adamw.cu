@@ -702,8 +702,8 @@ __device__ __forceinline__ void any_block(const AdamArgs& a, const AdamJob& J, f
 
 // States in 8 bits. A warp takes runs of blocks, a lane four elements of each.
 // Traffic is 12 bytes per element plus the gradient and the copy, so the
-// arithmetic counts: 277 instructions per block of 128 elements against about
-// 350 issue slots that HBM leaves (issue active 67%). Hence the packed fp32 pairs, the hardware's
+// arithmetic counts: 263 instructions per block of 128 elements against about
+// 350 issue slots that HBM leaves (issue active 64%). Hence the packed fp32 pairs, the hardware's
 // stochastic conversion (one instruction for four codes), power-of-two scales
 // (no division, folded into the betas), one hash per four elements, and a
 // rounded root in six instructions. Copies run kStages - 1 blocks ahead in the
@@ -718,8 +718,8 @@ __device__ __forceinline__ void any_block(const AdamArgs& a, const AdamJob& J, f
 // shifted ones' is not (194 us: the instruction cache holds three of them).
 // 415M-element fragment (bf16 gradients and copy): 1115 us, 6.0 TB/s (88% of
 // the copy rate); 2000 ragged tensors (48M elements, fp32 gradients): 170 us,
-// 4.6 TB/s (67%): some 310 instructions per block with the shifts, against
-// 310 issue slots that HBM leaves there.
+// 4.6 TB/s (67%): 298 instructions per block with the shifts, against some 310
+// issue slots that HBM leaves there.
 template <typename G>
 __global__ void __launch_bounds__(kThreads, 3) k_adamw8(const __grid_constant__ AdamArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
