@@ -471,7 +471,7 @@ typedef struct dl_adamw_job {
 } dl_adamw_job;
 
 typedef struct dl_adamw_config {
-    double lr;           /* >= 0 */
+    double lr;           /* >= 0; lr * weight_decay and lr / (1 - beta1^step) at most FLT_MAX */
     double beta1, beta2; /* in [0, 1) */
     double eps;          /* >= FLT_MIN */
     double weight_decay; /* >= 0 */

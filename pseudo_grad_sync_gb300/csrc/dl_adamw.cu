@@ -870,6 +870,7 @@ extern "C" int dl_adamw_step(const dl_adamw_job* jobs, int32_t n_jobs, int32_t g
     AdamArgs a;
     const double t = static_cast<double>(cfg->step);
     const double bc1 = 1.0 - pow(cfg->beta1, t), bc2 = 1.0 - pow(cfg->beta2, t);
+    if (cfg->lr * cfg->weight_decay > FLT_MAX || cfg->lr / bc1 > FLT_MAX) return DL_ERR_ARG;
     a.lr_wd = static_cast<float>(cfg->lr * cfg->weight_decay);
     a.step_size = static_cast<float>(cfg->lr / bc1);
     a.beta1 = static_cast<float>(cfg->beta1);

@@ -85,21 +85,22 @@ __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
 
 // Launch geometry of one kernel with its threads and dynamic shared memory:
 // the blocks that fit the current device at once, asked for on the first call
-// per device (allowing the shared memory on the way) and kept; 0 (and no
-// error left behind for a later call) when the device refuses. One object per
-// kernel: a static local of the function that launches it.
+// per device and kept; 0 (and no error left behind for a later call) when the
+// device refuses. The shared memory is allowed on every call, so a launch
+// after a device reset finds it so. One object per kernel: a static local of
+// the function that launches it.
 class Resident {
 public:
     int blocks(const void* kernel, int threads, size_t smem) {
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
+        if (smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     static_cast<int>(smem)) != cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
         int b = kept_[dev].load(std::memory_order_acquire);
         if (b == 0) {
-            if ((smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                          static_cast<int>(smem)) != cudaSuccess)) {
-                cudaGetLastError();
-                return 0;
-            }
             int per_sm = 0;
             if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess) {
                 cudaGetLastError();

@@ -75,7 +75,7 @@ def test_adamw_refusals(L):
     for bad in ({"lr": -1.0}, {"lr": math.nan}, {"lr": math.inf}, {"beta1": 1.0}, {"beta1": -0.1},
                 {"beta2": 1.0}, {"beta2": math.nan}, {"eps": 0.0}, {"eps": 1e-40},
                 {"eps": math.nan}, {"weight_decay": -1.0}, {"weight_decay": math.inf},
-                {"step": 0}, {"step": -5}):
+                {"lr": 1e30, "weight_decay": 1e30}, {"lr": 1e38}, {"step": 0}, {"step": -5}):
         assert _adamw(L, job, **bad) == -1, bad
     assert _adamw(L, job, clip=FAKE + 2) == -2
     for k in ("theta", "grad", "m", "v"):
