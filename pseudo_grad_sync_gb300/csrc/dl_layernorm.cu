@@ -93,10 +93,10 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) k_norm_fwd(const __grid_co
         if constexpr (!BULK && TPR >= 192) prefetch_rows(first + kGroups, kGroups, end, a.x, a.xs, a.width);
         const bool in = kGroups == 1 || r < end;
         float2 x[kPairs];
-        if constexpr (BULK) ring.wait();
+        if constexpr (BULK) ring.wait(first);
         {
             P raw[VPT];
-            const P* from = (BULK ? reinterpret_cast<const P*>(ring.row(ring.stage, group, 0))
+            const P* from = (BULK ? reinterpret_cast<const P*>(ring.row(ring.stage(), group, 0))
                                   : reinterpret_cast<const P*>(a.x + r * a.xs)) + t;
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {

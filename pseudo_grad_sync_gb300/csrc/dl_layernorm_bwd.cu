@@ -113,10 +113,10 @@ __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdA
         const float2 st = stats[at + group];
         const float mu = in ? st.x : 0.f, rs = in ? st.y : 0.f;
         P dyp[VPT], xp[VPT];
-        if constexpr (BULK) ring.wait();
-        const P* from0 = (BULK ? reinterpret_cast<const P*>(ring.row(ring.stage, group, 0))
+        if constexpr (BULK) ring.wait(first);
+        const P* from0 = (BULK ? reinterpret_cast<const P*>(ring.row(ring.stage(), group, 0))
                                : reinterpret_cast<const P*>(dy + r * a.ds)) + t;
-        const P* from1 = (BULK ? reinterpret_cast<const P*>(ring.row(ring.stage, group, 1))
+        const P* from1 = (BULK ? reinterpret_cast<const P*>(ring.row(ring.stage(), group, 1))
                                : reinterpret_cast<const P*>(x + r * a.xs)) + t;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {

@@ -13,6 +13,7 @@
 // are loaded straight into registers.
 #pragma once
 
+#include "dl_phase.h"
 #include "dl_types.cuh"
 
 namespace dl {
@@ -230,9 +231,7 @@ struct RowRing {
     // bytes of a row that a bulk copy takes: a last, partial pack is loaded by its owner
     uint32_t bytes;
     uint32_t pitch;  // between a stage's rows: `bytes` when they come in one copy, else kRow
-    int stage = 0;
-    uint32_t parity = 0;
-    bool ok = true;
+    RingPhase<STAGES> phase;
 
     __device__ __forceinline__ void init() {
         if (threadIdx.x == 0) {
@@ -248,7 +247,7 @@ struct RowRing {
     __device__ __forceinline__ void issue(int st, int64_t first, const T* p0, int64_t s0, const T* p1, int64_t s1) {
         if (threadIdx.x >= 32) return;
         const int64_t left = end - first;
-        if (left <= 0 || !ok) return;
+        if (left <= 0 || !phase.ok()) return;
         const int n = left < kGroups ? static_cast<int>(left) : kGroups, j = threadIdx.x;
         if (j == 0) {
             fence_proxy_async();
@@ -261,23 +260,25 @@ struct RowRing {
             if (ARRAYS > 1) bulk_copy_g2s(row(st, j, 1), p1 + (first + j) * s1, size, full + st);
         }
     }
-    // Until the current stage holds its round. A wait that runs out sets the
-    // status word; the block then neither waits nor copies any more and its
-    // outputs are undefined.
-    __device__ __forceinline__ void wait() {
-        if (!ok) return;
-        ok = __all_sync(kFull, mbar_wait_bounded(full + stage, parity, kPolls));
-        if (!ok) atomicOr(status, kDevErrCopyTimeout);
+    // the stage of the round being read, and the one of the round before it
+    __device__ __forceinline__ int stage() const { return phase.stage; }
+    __device__ __forceinline__ int before() const { return phase.before(); }
+    __device__ __forceinline__ void advance() { phase.advance(); }
+    // Until the current stage holds the round from row `first` on. A wait that
+    // runs out sets the status word; the warp then neither waits nor copies any
+    // more and the block's outputs are undefined.
+    __device__ __forceinline__ void wait(int64_t first) {
+        if (!phase.ok()) return;
+        if (__all_sync(kFull, mbar_wait_bounded(full + phase.stage, phase.parity, kPolls))) return;
+        phase.fail((end - first + kGroups - 1) / kGroups);
+        atomicOr(status, kDevErrCopyTimeout);
     }
-    __device__ __forceinline__ int before() const { return stage == 0 ? STAGES - 1 : stage - 1; }
-    __device__ __forceinline__ void advance() {
-        parity ^= stage == STAGES - 1;
-        stage = stage + 1 == STAGES ? 0 : stage + 1;
-    }
-    // After a wait that ran out: copies in flight land before the block ends.
+    // After a wait of warp 0 that ran out: the copies that it has in flight
+    // land (its wait for each is bounded too) before the block ends.
     __device__ __forceinline__ void drain() {
-        if (!ok && threadIdx.x < 32)
-            for (int i = 0; i < STAGES; ++i) mbar_wait_bounded(full + i, parity ^ (i < stage), kPolls);
+        if (threadIdx.x < 32)
+            for (int i = 0; i < phase.pending; ++i)
+                mbar_wait_bounded(full + phase.stage_of(i), phase.parity_of(i), kPolls);
     }
 };
 
