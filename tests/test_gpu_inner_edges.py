@@ -1,0 +1,141 @@
+"""The inner-step operators where they are easily wrong: geometries and paths
+that small cases do not reach, values at the ends of their ranges, and what a
+call leaves behind. Plain implementations in 64 bits, tolerances per element
+from the operators' fp32 arithmetic (u = 2^-24)."""
+import numpy as np
+import pytest
+
+import inner_ref as ref
+import test_gpu_inner as base
+from test_gpu_inner import HYPER, NORM_TOL, U, codes, dl, np64, to_cuda  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+# ----------------------------------------------------------------------------
+# layer norm: every launch geometry, in its aligned, partial and plain forms
+
+# rows of 129..256 and of 4097..6144 columns have threads per row of their own
+MORE_WIDTHS = [130, 200, 256, 4104, 5632, 6144]
+
+
+@pytest.mark.parametrize("width", MORE_WIDTHS)
+@pytest.mark.parametrize("kind,param", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16"),
+                                        ("f16", "f32")])
+def test_layernorm_of_more_widths(dl, width, kind, param):
+    base.test_layernorm(dl, width, kind, param)
+
+
+@pytest.mark.parametrize("width", MORE_WIDTHS)
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_long_runs_of_rows_of_more_widths(dl, width, kind, monkeypatch):
+    base.test_layernorm_long_runs_of_rows(dl, width, kind, monkeypatch)
+
+
+@pytest.mark.parametrize("width", [5, 61, 101, 203, 501, 1001, 2047, 4001, 5001, 6143, 8190, 11_007])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("limit", [None, "2"])
+def test_aligned_rows_that_end_inside_a_pack(dl, width, kind, limit, monkeypatch):
+    """Rows that start on 16 bytes and whose width is no multiple of a pack,
+    loaded straight (each row its own round) and through the copies' ring."""
+    if limit:
+        monkeypatch.setenv("DL_GRID_LIMIT", limit)
+    rng = np.random.default_rng(width)
+    pad, rows = -width % 8, 150
+    for rms in (False, True):
+        x = base._rows(rng, rows, width, kind, pad)
+        assert x.data_ptr() % 16 == 0 and x.stride(0) % 8 == 0
+        w, b = (to_cuda(rng.standard_normal(width)) for _ in range(2))
+        y, mean, rstd = dl.layernorm_forward(x, w, b, base.EPS, rms)
+        x64, w64, b64 = np64(x), np64(w), np64(b)
+        yr, mr, rr = ref.norm64(x64, w64, b64, base.EPS, rms)
+        h = (x64 - mr[:, None]) * rr[:, None]
+        assert np.all(abs(np64(y) - yr) <= base._forward_tol(x64, w64, b64, yr, h, rr, kind)), rms
+        base._backward_case(dl, rng, x, w, mean, rstd, rms, True, kind, "f32", pad, False, 64 + rows)
+
+
+@pytest.mark.parametrize("width", [64, 256, 1024, 2048, 4096, 5632, 8192, 16_384])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_outputs_off_16_bytes_beside_aligned_inputs(dl, width, kind, monkeypatch):
+    """The outputs' rows may be aligned to their elements only while the
+    inputs come in whole packs: the same bits, and nothing beside them."""
+    rng = np.random.default_rng(width)
+    rows = 41
+    x, dy = base._rows(rng, rows, width, kind, 0), base._rows(rng, rows, width, kind, 0, 1e-2)
+    w, b = (to_cuda(rng.standard_normal(width)) for _ in range(2))
+    for limit in (None, "2"):
+        if limit:
+            monkeypatch.setenv("DL_GRID_LIMIT", limit)
+        want, mean, rstd = dl.layernorm_forward(x, w, b)
+        dx, dw, db = dl.layernorm_backward(dy, x, w, mean, rstd)
+        out = torch.full((rows, width + 3), 3.0, dtype=x.dtype, device="cuda")
+        y = out[:, 1:1 + width]
+        dl.layernorm_forward(x, w, b, y=y)
+        assert torch.equal(y, want)
+        _, dw2, db2 = dl.layernorm_backward(dy, x, w, mean, rstd, dx=y)
+        assert torch.equal(y, dx) and torch.equal(dw, dw2) and torch.equal(db, db2)
+        assert (out[:, 0] == 3).all() and (out[:, 1 + width:] == 3).all()
+
+
+# ----------------------------------------------------------------------------
+# 8-bit AdamW: long runs of blocks at every offset from four elements
+
+# tensors of more than ten blocks that start 0, 1, 3, 2, 2 and 0 elements past
+# a multiple of four, whole and partial last blocks, small ones between
+RUNS = [128 * 41 + 1, 128 * 37 + 2, 128 * 50 + 3, 128 * 45, 5, 1, 128 * 39 + 126, 0, 128 * 64, 130]
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("limit", ["1", "2"])
+@pytest.mark.parametrize("copy", [True, False])
+def test_adamw8_long_runs_of_blocks(dl, kind, limit, copy, monkeypatch):
+    """One or two blocks of threads: runs of many blocks per warp, so that the
+    rings refill and wrap, and blocks that start inside a group of four follow
+    one another. Codes and scales bit for bit from old states, theta and its
+    copy as ever."""
+    monkeypatch.setenv("DL_GRID_LIMIT", limit)
+    monkeypatch.setattr(base, "SHAPES", [RUNS, RUNS])
+    base.test_adamw_8(dl, kind, 0 if copy else 1)
+
+
+@pytest.mark.parametrize("start", [0, 1, 2, 3])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_adamw8_one_tensor_at_every_offset(dl, kind, start, monkeypatch):
+    """Runs of 32 blocks that end in the middle of the tensor: the next warp
+    goes on from there."""
+    monkeypatch.setenv("DL_GRID_LIMIT", "1")
+    monkeypatch.setattr(base, "SHAPES", [[start, 128 * 700 + 77]])
+    base.test_adamw_8(dl, kind, 0)
+
+
+def test_adamw8_long_runs_over_many_jobs(dl, monkeypatch):
+    monkeypatch.setenv("DL_GRID_LIMIT", "1")
+    base.test_adamw_many_jobs_counts_slots_and_splits_launches(dl)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_adamw8_long_runs_write_nothing_outside(dl, kind, monkeypatch):
+    monkeypatch.setenv("DL_GRID_LIMIT", "1")
+    base.test_adamw_writes_nothing_outside_its_buffers(dl, 8, kind)
+    # several long tensors between bytes of one value
+    F = dl.Fragment(RUNS)
+    pad, n, slots = 64, F.n, dl.adamw_scale_slots(F)
+
+    def guarded(count, dtype):
+        size = torch.empty(0, dtype=dtype).element_size()
+        raw = torch.full(((count + 2 * pad) * size,), 0x3C, dtype=torch.uint8, device="cuda")
+        return raw, raw.view(dtype)[pad:pad + count]
+    e4 = torch.float8_e4m3fn
+    raws, bufs = zip(*(guarded(c, d) for c, d in (
+        (n, torch.float32), (n, base.TYPES[kind]), (n, e4), (n, e4), (slots, torch.float32),
+        (slots, torch.float32), (n, torch.bfloat16))))
+    dl.adamw_step(dl.AdamWJobs([F], *([b] for b in bufs)), 1, **HYPER)
+    for raw, inside in zip(raws, bufs):
+        edge = pad * inside.element_size()
+        assert (raw[:edge] == 0x3C).all() and (raw[-edge:] == 0x3C).all()
+    slot = ref.places(RUNS) // ref.BLOCK
+    free = sorted(set(range(slots)) - set(slot.tolist()))
+    for b in bufs[4:6]:
+        assert (b[free].view(torch.int32) == 0x3C3C3C3C).all()
