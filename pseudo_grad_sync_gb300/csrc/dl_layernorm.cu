@@ -157,7 +157,6 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) k_norm_fwd(const __grid_co
             }
         }
     }
-    if constexpr (BULK) ring.drain();
 }
 
 // Rows too wide for a block's registers: the row is read three times (from

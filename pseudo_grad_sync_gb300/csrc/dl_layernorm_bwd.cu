@@ -165,7 +165,6 @@ __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdA
             store_row<T, N, TPR, VPT, FULL>(a.dx + off + r * a.os, out, t, width, a.vec_out);
         }
     }
-    if constexpr (BULK) ring.drain();
     // the join's blocks may take the place of those that end from here on
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // the block's sums over its rows

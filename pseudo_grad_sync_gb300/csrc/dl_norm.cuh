@@ -232,6 +232,7 @@ struct RowRing {
     uint32_t bytes;
     uint32_t pitch;  // between a stage's rows: `bytes` when they come in one copy, else kRow
     RingPhase<STAGES> phase;
+    bool ok = true;
 
     __device__ __forceinline__ void init() {
         if (threadIdx.x == 0) {
@@ -247,7 +248,7 @@ struct RowRing {
     __device__ __forceinline__ void issue(int st, int64_t first, const T* p0, int64_t s0, const T* p1, int64_t s1) {
         if (threadIdx.x >= 32) return;
         const int64_t left = end - first;
-        if (left <= 0 || !phase.ok()) return;
+        if (left <= 0 || !ok) return;
         const int n = left < kGroups ? static_cast<int>(left) : kGroups, j = threadIdx.x;
         if (j == 0) {
             fence_proxy_async();
@@ -266,19 +267,17 @@ struct RowRing {
     __device__ __forceinline__ void advance() { phase.advance(); }
     // Until the current stage holds the round from row `first` on. A wait that
     // runs out sets the status word; the warp then neither waits nor copies any
-    // more and the block's outputs are undefined.
+    // more and the block's outputs are undefined. Warp 0, which issued them,
+    // first waits (bounded too) until its copies in flight have landed: the
+    // block never ends with one, nor reuses its memory under one.
     __device__ __forceinline__ void wait(int64_t first) {
-        if (!phase.ok()) return;
-        if (__all_sync(kFull, mbar_wait_bounded(full + phase.stage, phase.parity, kPolls))) return;
-        phase.fail((end - first + kGroups - 1) / kGroups);
+        if (!ok) return;
+        ok = __all_sync(kFull, mbar_wait_bounded(full + phase.stage, phase.parity, kPolls));
+        if (ok) return;
         atomicOr(status, kDevErrCopyTimeout);
-    }
-    // After a wait of warp 0 that ran out: the copies that it has in flight
-    // land (its wait for each is bounded too) before the block ends.
-    __device__ __forceinline__ void drain() {
-        if (threadIdx.x < 32)
-            for (int i = 0; i < phase.pending; ++i)
-                mbar_wait_bounded(full + phase.stage_of(i), phase.parity_of(i), kPolls);
+        if (threadIdx.x >= 32) return;
+        const int n = phase.in_flight((end - first + kGroups - 1) / kGroups);
+        for (int i = 0; i < n; ++i) mbar_wait_bounded(full + phase.stage_of(i), phase.parity_of(i), kPolls);
     }
 };
 

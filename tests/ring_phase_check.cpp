@@ -1,6 +1,6 @@
 // Steps dl::RingPhase (csrc/dl_phase.h) against a model of the barriers of a
 // ring of copies: for every number of rounds and every round whose wait runs
-// out, the waits that drain the ring meet exactly the copies in flight.
+// out, the waits that follow meet exactly the copies in flight.
 #include <cstdio>
 
 #include "dl_phase.h"
@@ -19,27 +19,28 @@ template <int S>
 int run(int rounds, int failing) {
     Model<S> m;
     dl::RingPhase<S> phase;
+    bool ok = true;
     auto issue = [&](int stage, int round) {
-        if (round < rounds && phase.ok()) ++m.issued[stage];
+        if (round < rounds && ok) ++m.issued[stage];
     };
     for (int i = 0; i < S - 1; ++i) issue(i, i);
     for (int r = 0; r < rounds; ++r) {
-        if (phase.ok()) {
+        if (ok) {
             if (phase.stage != r % S || phase.parity != unsigned(r / S & 1)) return 1;
             if (m.passes_at_once(phase.stage, phase.parity)) return 2;
-            if (r == failing)
-                phase.fail(rounds - r);
-            else
+            ok = r != failing;
+            if (ok)
                 m.landed[phase.stage] = m.issued[phase.stage];
+            else
+                for (int i = 0; i < phase.in_flight(rounds - r); ++i) {
+                    const int s = phase.stage_of(i);
+                    if (m.passes_at_once(s, phase.parity_of(i))) return 3;  // would not wait for its copy
+                    if (m.issued[s] != m.landed[s] + 1) return 4;           // waits for a copy nobody issued
+                    m.landed[s] = m.issued[s];
+                }
         }
         issue(phase.before(), r + S - 1);
         phase.advance();
-    }
-    for (int i = 0; i < phase.pending; ++i) {
-        const int s = phase.stage_of(i);
-        if (m.passes_at_once(s, phase.parity_of(i))) return 3;   // would not wait for its copy
-        if (m.issued[s] != m.landed[s] + 1) return 4;            // waits for a copy nobody issued
-        m.landed[s] = m.issued[s];
     }
     for (int s = 0; s < S; ++s)
         if (m.issued[s] != m.landed[s]) return 5;  // the block would end with a copy in flight
