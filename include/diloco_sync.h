@@ -560,7 +560,10 @@ size_t dl_layernorm_workspace_bytes(int64_t rows, int32_t width);
  *   dbias        the same, or NULL where there is no bias
  *   d_workspace  device scratch of dl_layernorm_workspace_bytes(rows, width)
  *                bytes; its first word is the device status word, the rest
- *                needs no initialisation
+ *                needs no initialisation. A wait that runs out sets its bit
+ *                there and in the library's own word (read with
+ *                dl_read_device_status(NULL, ...)), so that a caller who drops
+ *                the workspace after the call still learns of it.
  * rows = 0 writes zero gradients (accumulating: leaves them).
  */
 int dl_layernorm_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,

@@ -16,7 +16,7 @@ struct FwdArgs {
     const void* bias;
     float* mean;
     float* rstd;
-    uint32_t* status;
+    RingReport report;
     int64_t xs, ys, rows;
     int64_t run;  // rows of a block
     int width;
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) k_norm_fwd(const __grid_co
     const int64_t begin = a.run * blockIdx.x, end = min(a.rows, begin + a.run);
     const uint32_t bytes = static_cast<uint32_t>(a.width * sizeof(T)) & ~15u;
     const bool together = bytes == a.width * sizeof(T) && a.xs == a.width;
-    typename Geo::Ring ring{smem + Geo::kFixed, reinterpret_cast<uint64_t*>(smem), a.status, end, bytes,
+    typename Geo::Ring ring{smem + Geo::kFixed, reinterpret_cast<uint64_t*>(smem), a.report, end, bytes,
                             together ? bytes : static_cast<uint32_t>(Geo::Ring::kRow)};
     if constexpr (BULK) {
         ring.init();
@@ -203,7 +203,8 @@ bool launch(FwdArgs<T> a, cudaStream_t s, int* status) {
     int64_t grid = resident.grid(kernel, BLOCK, Geo::kBytes, rounds);
     if (grid == 0) return true;
     if (BULK && rounds <= grid) return false;
-    if (BULK && library_status_word(&a.status) != DL_OK) return true;
+    if (BULK && library_status_word(&a.report.word) != DL_OK) return true;
+    if (BULK) a.report.polls = wait_polls(kRowPolls);
     a.run = (rounds + grid - 1) / grid * Geo::kGroups;
     grid = (a.rows + a.run - 1) / a.run;
     k_norm_fwd<T, N, TPR, EPT, BLOCK, BULK, FULL><<<static_cast<int>(grid), BLOCK, Geo::kBytes, s>>>(a);
@@ -248,7 +249,7 @@ template <typename T>
 int forward(const void* x, int64_t xs, int64_t rows, int width, const void* w, const void* b,
             int32_t pt, float eps, bool rms, void* y, int64_t ys, float* mean, float* rstd,
             cudaStream_t s) {
-    FwdArgs<T> a{static_cast<const T*>(x), static_cast<T*>(y), w, b, mean, rstd, nullptr, xs, ys,
+    FwdArgs<T> a{static_cast<const T*>(x), static_cast<T*>(y), w, b, mean, rstd, {}, xs, ys,
                  rows, 0, width, pt, eps, rms, false};
     a.vec_out = aligned16(y) && ys * sizeof(T) % 16 == 0;
     if (aligned16(x) && xs * sizeof(T) % 16 == 0) return by_width<T, 16 / sizeof(T)>(a, s);

@@ -20,7 +20,7 @@ struct BwdArgs {
     const float* mean;
     const float* rstd;
     float* part;  // [blocks][2][width]
-    uint32_t* status;
+    RingReport report;
     int64_t ds, xs, os, rows;
     int64_t run;  // rows of a block
     int width;
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdA
     auto column = [&](int k) { return (k * TPR + t) * N; };
     const uint32_t bytes = static_cast<uint32_t>(width * sizeof(T)) & ~15u;
     const bool together = bytes == width * sizeof(T) && a.ds == width && a.xs == width;
-    typename Geo::Ring ring{smem + Geo::kFixed, reinterpret_cast<uint64_t*>(smem), a.status, end, bytes,
+    typename Geo::Ring ring{smem + Geo::kFixed, reinterpret_cast<uint64_t*>(smem), a.report, end, bytes,
                             together ? bytes : static_cast<uint32_t>(Geo::Ring::kRow)};
     if constexpr (CLUSTER > 1) sum.barrier();  // the other block runs before its memory is written
     if constexpr (BULK) {
@@ -298,6 +298,8 @@ int launch_form(BwdArgs<T> a, cudaStream_t s) {
     parts = parts < CLUSTER ? 1 : parts / CLUSTER;
     if (parts > kMostBlocks) parts = kMostBlocks;
     if (BULK && rounds <= parts) return 0;
+    if (BULK && library_status_word(&a.report.second) != DL_OK) return DL_ERR_CUDA;
+    if (BULK) a.report.polls = wait_polls(kRowPolls);
     a.run = (rounds + parts - 1) / parts * Geo::kGroups;
     parts = (a.rows + a.run - 1) / a.run;
     cudaLaunchConfig_t config = {};
@@ -399,8 +401,9 @@ extern "C" int dl_layernorm_backward(const void* dy, int64_t dy_stride, const vo
         using T = decltype(zero);
         return backward<T>(BwdArgs<T>{static_cast<const T*>(dy), static_cast<const T*>(x),
                                       static_cast<T*>(dx), weight, mean, rstd, part,
-                                      static_cast<uint32_t*>(d_workspace), dy_stride, x_stride,
-                                      dx_stride, rows, 0, width, param_type, rms, false},
+                                      RingReport{static_cast<uint32_t*>(d_workspace), nullptr, 0},
+                                      dy_stride, x_stride, dx_stride, rows, 0, width, param_type, rms,
+                                      false},
                            s);
     };
     int parts = 0;

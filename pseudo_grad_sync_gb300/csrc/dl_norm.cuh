@@ -213,12 +213,34 @@ __device__ __forceinline__ void prefetch_rows(int64_t first, int groups, int64_t
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(lo), "r"(static_cast<uint32_t>(hi - lo))
                      : "memory");
 }
+
+constexpr int kRowPolls = 1 << 17;  // of a wait for a round's rows: about a second
+
+// Where a ring reports a wait that ran out (either may be null), and after how
+// many polls one does.
+struct RingReport {
+    uint32_t* word;
+    uint32_t* second;
+    int polls;
+};
+
+// After a wait that ran out, out of line: sets the status words; warp 0 waits
+// for the copies that it has in flight with `left` rounds to go.
+template <int STAGES>
+__device__ __noinline__ void ring_failed(uint64_t* full, RingPhase<STAGES> phase, const RingReport& report,
+                                         int64_t left) {
+    if (report.word) atomicOr(report.word, kDevErrCopyTimeout);
+    if (report.second) atomicOr(report.second, kDevErrCopyTimeout);
+    if (threadIdx.x >= 32) return;
+    for (int i = 0; i < phase.in_flight(left); ++i)
+        mbar_wait_bounded(full + phase.stage_of(i), phase.parity_of(i), kRowPolls);
+}
+
 // The ring of a block's rounds: each stage holds ARRAYS arrays' rows of one
 // round. Rows that follow each other in memory come in one copy per array,
 // others in one copy per row.
 template <typename T, int TPR, int EPT, int BLOCK, int ARRAYS, int STAGES>
 struct RowRing {
-    static constexpr long kPolls = 1L << 17;  // of a wait: about a second
     static constexpr int kGroups = BLOCK / TPR;
     static_assert(kGroups <= 32, "a lane of warp 0 copies a row");
     static constexpr size_t kRow = size_t(TPR) * EPT * sizeof(T);
@@ -226,8 +248,8 @@ struct RowRing {
     static constexpr size_t kBytes = STAGES * kStage;
     unsigned char* base;
     uint64_t* full;  // a barrier per stage
-    uint32_t* status;
-    int64_t end;  // of the block's rows
+    const RingReport& report;  // of the kernel's arguments
+    int64_t end;               // of the block's rows
     // bytes of a row that a bulk copy takes: a last, partial pack is loaded by its owner
     uint32_t bytes;
     uint32_t pitch;  // between a stage's rows: `bytes` when they come in one copy, else kRow
@@ -266,18 +288,15 @@ struct RowRing {
     __device__ __forceinline__ int before() const { return phase.before(); }
     __device__ __forceinline__ void advance() { phase.advance(); }
     // Until the current stage holds the round from row `first` on. A wait that
-    // runs out sets the status word; the warp then neither waits nor copies any
+    // runs out sets the status words; the warp then neither waits nor copies any
     // more and the block's outputs are undefined. Warp 0, which issued them,
     // first waits (bounded too) until its copies in flight have landed: the
     // block never ends with one, nor reuses its memory under one.
     __device__ __forceinline__ void wait(int64_t first) {
         if (!ok) return;
-        ok = __all_sync(kFull, mbar_wait_bounded(full + phase.stage, phase.parity, kPolls));
+        ok = __all_sync(kFull, mbar_wait_bounded(full + phase.stage, phase.parity, report.polls));
         if (ok) return;
-        atomicOr(status, kDevErrCopyTimeout);
-        if (threadIdx.x >= 32) return;
-        const int n = phase.in_flight((end - first + kGroups - 1) / kGroups);
-        for (int i = 0; i < n; ++i) mbar_wait_bounded(full + phase.stage_of(i), phase.parity_of(i), kPolls);
+        ring_failed<STAGES>(full, phase, report, (end - first + kGroups - 1) / kGroups);
     }
 };
 

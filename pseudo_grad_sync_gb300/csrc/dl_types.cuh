@@ -127,6 +127,15 @@ private:
     std::atomic<int> kept_[kDevices] = {};
 };
 
+// Polls of the bounded waits for copies: `most`, or fewer by DL_WAIT_POLLS
+// (environment; tests use it to make waits run out)
+inline int wait_polls(int most) {
+    const char* v = getenv("DL_WAIT_POLLS");
+    if (!v) return most;
+    const long n = strtol(v, nullptr, 10);
+    return n >= 0 && n < most ? static_cast<int>(n) : most;
+}
+
 // p is a multiple of a (a power of two); null is
 inline bool aligned_to(const void* p, size_t a) {
     return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;

@@ -388,7 +388,9 @@ def layernorm_backward(dy, x, weight, mean, rstd, dweight=None, dbias=None, rms=
     dweight, dbias). dweight and dbias may be slices of a fragment's flat
     gradient buffer; with accumulate=True the sums are added to what they
     hold. Without a dweight both are allocated (dbias only with bias=True);
-    a call that passes dweight alone computes no dbias."""
+    a call that passes dweight alone computes no dbias. A copy that timed out
+    is reported by read_device_status(None), and by the workspace's status
+    word when the caller passed one."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return layernorm_backward(dy, x, weight, mean, rstd, dweight, dbias, rms, accumulate,

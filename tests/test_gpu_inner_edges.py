@@ -139,3 +139,48 @@ def test_adamw8_long_runs_write_nothing_outside(dl, kind, monkeypatch):
     free = sorted(set(range(slots)) - set(slot.tolist()))
     for b in bufs[4:6]:
         assert (b[free].view(torch.int32) == 0x3C3C3C3C).all()
+
+
+# ----------------------------------------------------------------------------
+# bounded waits
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("width", [64, 1000, 4096, 5632, 11_008])
+def test_a_wait_that_runs_out_is_reported(dl, kind, width, monkeypatch):
+    """With waits of no polls every wait for a copy runs out. The calls end and
+    say so: in the library's status word, and backward also in the workspace's.
+    The next calls are as ever."""
+    monkeypatch.setenv("DL_GRID_LIMIT", "2")
+    rng = np.random.default_rng(width)
+    x, dy = (base._rows(rng, 700, width, kind, 0) for _ in range(2))
+    w = to_cuda(rng.standard_normal(width))
+    y, mean, rstd = dl.layernorm_forward(x, w)
+    want = dl.layernorm_backward(dy, x, w, mean, rstd)
+    assert dl.read_device_status(None) == 0
+    monkeypatch.setenv("DL_WAIT_POLLS", "0")
+    dl.layernorm_forward(x, w)
+    assert dl.read_device_status(None) == 1 and dl.read_device_status(None) == 0
+    dl.layernorm_backward(dy, x, w, mean, rstd)
+    assert dl.read_device_status(None) == 1 and dl.read_device_status(None) == 0
+    ws = dl.new_workspace(dl.layernorm_workspace_bytes(700, width))
+    dl.layernorm_backward(dy, x, w, mean, rstd, workspace=ws)
+    assert dl.read_device_status(ws) == 1 and dl.read_device_status(None) == 1
+    monkeypatch.delenv("DL_WAIT_POLLS")
+    assert torch.equal(dl.layernorm_forward(x, w)[0], y)
+    again = dl.layernorm_backward(dy, x, w, mean, rstd, workspace=ws)
+    assert all(torch.equal(a, b) for a, b in zip(want, again))
+    assert dl.read_device_status(None) == 0 and dl.read_device_status(ws) == 0
+
+
+def test_a_gradient_pass_that_ran_out_is_reported(dl, monkeypatch):
+    """The same through the autograd operation, which has no workspace of its
+    caller's."""
+    monkeypatch.setenv("DL_GRID_LIMIT", "2")
+    x = torch.randn(300, 512, device="cuda", requires_grad=True)
+    w = torch.ones(512, device="cuda", requires_grad=True)
+    y = dl.layer_norm(x, w)
+    assert dl.read_device_status(None) == 0
+    monkeypatch.setenv("DL_WAIT_POLLS", "0")
+    y.sum().backward()
+    assert dl.read_device_status(None) == 1
