@@ -160,7 +160,8 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) k_norm_fwd(const __grid_co
 }
 
 // Rows too wide for a block's registers: the row is read three times (from
-// L2 after the first).
+// L2 after the first). Columns count in 64 bits: a step past a width near 2^31
+// would not fit 32.
 template <typename T>
 __global__ void __launch_bounds__(1024) k_norm_fwd_wide(const __grid_constant__ FwdArgs<T> a) {
     __shared__ float2 red[32];
@@ -169,16 +170,16 @@ __global__ void __launch_bounds__(1024) k_norm_fwd_wide(const __grid_constant__ 
         float mu = 0.f;
         if (!a.rms) {
             float s = 0.f;
-            for (int c = threadIdx.x; c < a.width; c += 1024) s += to_f32(xr[c]);
+            for (int64_t c = threadIdx.x; c < a.width; c += 1024) s += to_f32(xr[c]);
             mu = block_sum(make_float2(s, 0.f), red).x / a.width;
         }
         float q = 0.f;
-        for (int c = threadIdx.x; c < a.width; c += 1024) {
+        for (int64_t c = threadIdx.x; c < a.width; c += 1024) {
             const float d = to_f32(xr[c]) - mu;
             q = fmaf(d, d, q);
         }
         const float rs = rsqrtf(block_sum(make_float2(q, 0.f), red).x / a.width + a.eps);
-        for (int c = threadIdx.x; c < a.width; c += 1024) {
+        for (int64_t c = threadIdx.x; c < a.width; c += 1024) {
             const float h = (to_f32(xr[c]) - mu) * rs * load_param(a.weight, a.ptype, c);
             a.y[r * a.ys + c] = from_f32<T>(a.bias ? h + load_param(a.bias, a.ptype, c) : h);
         }

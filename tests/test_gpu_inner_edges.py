@@ -184,3 +184,16 @@ def test_a_gradient_pass_that_ran_out_is_reported(dl, monkeypatch):
     monkeypatch.setenv("DL_WAIT_POLLS", "0")
     y.sum().backward()
     assert dl.read_device_status(None) == 1
+
+
+def test_layernorm_of_the_widest_row(dl):
+    """2^31 - 1 columns: a constant row's deviations are zero, and nothing lies
+    beside it. (Sums of equal values are exact; the width and the sum both
+    round to powers of two, so the mean is the constant.)"""
+    width = 2 ** 31 - 1
+    x = torch.full((width,), 2.0, dtype=torch.bfloat16, device="cuda")
+    w = torch.full((width,), 0.5, dtype=torch.bfloat16, device="cuda")
+    out = torch.full((width + 64,), 3.0, dtype=torch.bfloat16, device="cuda")
+    y, mean, rstd = dl.layernorm_forward(x, w, y=out[:width])
+    assert float(mean) == 2.0 and abs(float(rstd) * base.EPS ** 0.5 - 1) < 1e-6
+    assert int(out[:width].count_nonzero()) == 0 and bool((out[width:] == 3).all())
