@@ -296,6 +296,8 @@ def _rows(t, name, like=None):
     width = t.shape[-1]
     if width < 1:
         raise ValueError(f"{name}: the last dimension is empty")
+    if width >= 2**31:  # ctypes would pass its low 32 bits
+        raise ValueError(f"{name}: a last dimension of {width}, at most 2^31 - 1")
     stride = width
     if not t.is_contiguous():
         if t.dim() != 2:
