@@ -435,6 +435,20 @@ def layernorm_backward(dy, x, weight, mean, rstd, dweight=None, dbias=None, rms=
     return dx, dweight, dbias
 
 
+class _LayerNormGradient(torch.autograd.Function):
+    """layernorm_backward in a graph that may be differentiated again
+    (create_graph=True): a second derivative is an error, not a silent zero.
+    Its inputs carry the history, so this holds for a constant dy too."""
+
+    @staticmethod
+    def forward(ctx, dy, x, weight, mean, rstd, rms, bias):
+        return layernorm_backward(dy, x, weight, mean, rstd, rms=rms, bias=bias)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("layer_norm: second derivatives are not implemented")
+
+
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps, rms):
@@ -445,13 +459,16 @@ class _LayerNorm(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy):
-        x, weight, mean, rstd = ctx.saved_tensors
         # a broadcast gradient (as of a sum) has rows that overlap
-        dx, dw, db = layernorm_backward(dy.contiguous(), x, weight, mean, rstd, rms=ctx.rms,
-                                        bias=ctx.bias)
+        args = (dy.contiguous(), *ctx.saved_tensors)
+        if torch.is_grad_enabled():
+            dx, dw, db = _LayerNormGradient.apply(*args, ctx.rms, ctx.bias)
+        else:
+            dx, dw, db = layernorm_backward(*args, rms=ctx.rms, bias=ctx.bias)
         return dx, dw, db, None, None
 
 
 def layer_norm(x, weight, bias=None, eps=1e-5, rms=False):
-    """layernorm_forward as a torch.autograd operation."""
+    """layernorm_forward as a torch.autograd operation. First derivatives only:
+    differentiating its gradients again (create_graph=True) raises."""
     return _LayerNorm.apply(x, weight, bias, eps, rms)
