@@ -455,6 +455,7 @@ class _LayerNorm(torch.autograd.Function):
         y, mean, rstd = layernorm_forward(x, weight, bias, eps, rms)
         ctx.save_for_backward(x, weight, mean, rstd)
         ctx.rms, ctx.bias = rms, bias is not None
+        ctx.shapes = weight.shape, None if bias is None else bias.shape
         return y
 
     @staticmethod
@@ -465,10 +466,13 @@ class _LayerNorm(torch.autograd.Function):
             dx, dw, db = _LayerNormGradient.apply(*args, ctx.rms, ctx.bias)
         else:
             dx, dw, db = layernorm_backward(*args, rms=ctx.rms, bias=ctx.bias)
-        return dx, dw, db, None, None
+        w_shape, b_shape = ctx.shapes  # the parameters may have leading ones
+        return dx, dw.view(w_shape), None if db is None else db.view(b_shape), None, None
 
 
 def layer_norm(x, weight, bias=None, eps=1e-5, rms=False):
     """layernorm_forward as a torch.autograd operation. First derivatives only:
     differentiating its gradients again (create_graph=True) raises."""
+    if bias is not None and bias.numel() != weight.numel():  # its gradient would not fit it
+        raise ValueError(f"bias: {bias.numel()} elements, expected {weight.numel()}")
     return _LayerNorm.apply(x, weight, bias, eps, rms)

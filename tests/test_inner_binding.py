@@ -94,3 +94,23 @@ def test_layer_norm_second_derivatives_are_refused(formulas, rms, constant, of):
     assert torch.isfinite(torch.autograd.grad(penalty(norm(*leaves)), leaves[0])[0]).all()
     with pytest.raises(RuntimeError, match="second derivatives are not implemented"):
         torch.autograd.grad(penalty(dl.layer_norm(*leaves, rms=rms)), leaves[0])
+
+
+def test_layer_norm_parameters_with_leading_ones(formulas):
+    """Their gradients have their shapes."""
+    leaves, c, norm = _case(False)
+    x, w, b = leaves
+    want = torch.autograd.grad((norm(x, w, b) * c).sum(), leaves)
+    for create_graph in (False, True):
+        w2, b2 = (t.detach().reshape(1, 1, 5).requires_grad_() for t in (w, b))
+        got = torch.autograd.grad((dl.layer_norm(x, w2, b2) * c).sum(), (x, w2, b2),
+                                  create_graph=create_graph)
+        assert got[1].shape == got[2].shape == (1, 1, 5)
+        assert all(torch.allclose(a.reshape(b.shape), b) for a, b in zip(got, want))
+
+
+def test_a_bias_of_another_length_has_no_gradient(formulas):
+    x, w = torch.zeros(4, 64), torch.ones(64)
+    for n in (1, 63, 65):
+        with pytest.raises(ValueError, match=f"bias: {n} elements, expected 64"):
+            dl.layer_norm(x, w, torch.zeros(n))
