@@ -227,7 +227,8 @@ class InnerAdamW:
     """AdamW over a learner's fragments with its states, clipping first.
 
     theta and grad: per-fragment lists of flat device buffers (a learner's
-    replica and the gradients that its backward passes write). bits: 32 or 8,
+    replica and the gradients that its backward passes write); what lies behind
+    a fragment's n elements is neither read nor written. bits: 32 or 8,
     the width of the states. max_norm: clip by the global gradient norm; a
     step whose gradients are not all finite is then skipped on the device
     (``steps`` still counts it). decay: per-fragment lists or arrays of T
@@ -238,7 +239,7 @@ class InnerAdamW:
                  weight_decay=0.1, decay=None, theta_bf16=None, max_norm=None, seed=0):
         if bits not in (32, 8):
             raise ValueError(f"bits: {bits}, expected 32 or 8")
-        frags, theta = list(frags), list(theta)
+        frags, theta, grad = list(frags), list(theta), list(grad)
         dev = theta[0].device
         self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
         self.max_norm, self.seed, self.steps = max_norm, seed, 0
@@ -257,7 +258,8 @@ class InnerAdamW:
                      for d in decay]
         self.jobs = AdamWJobs(frags, theta, grad, self.m, self.v, self.m_scale, self.v_scale,
                               theta_bf16, decay)
-        self.grads = GradList([g for g in grad if g.numel()])
+        # the norm of what is stepped: a buffer may be longer than its fragment
+        self.grads = GradList([g.view(-1)[:F.n] for F, g in zip(frags, grad) if F.n])
         self.clip = torch.ones(2, dtype=torch.float32, device=dev)
         self.workspace = new_workspace(grad_norm_workspace_bytes(), dev)
 

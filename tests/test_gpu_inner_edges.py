@@ -197,3 +197,53 @@ def test_layernorm_of_the_widest_row(dl):
     y, mean, rstd = dl.layernorm_forward(x, w, y=out[:width])
     assert float(mean) == 2.0 and abs(float(rstd) * base.EPS ** 0.5 - 1) < 1e-6
     assert int(out[:width].count_nonzero()) == 0 and bool((out[width:] == 3).all())
+
+
+# ----------------------------------------------------------------------------
+# InnerAdamW
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("behind", [float("nan"), float("inf"), 1e3])
+def test_the_clip_reads_the_fragments_only(dl, bits, behind):
+    """Buffers longer than their fragments (rounded up to 64 elements): what
+    lies behind enters neither the norm nor the step."""
+    rng = np.random.default_rng(3)
+    numels = [[100, 33], [0], [257]]
+    results = []
+    for extra in (False, True):
+        F = [dl.Fragment(n) for n in numels]
+        r = np.random.default_rng(4)
+        size = [-(-f.n // 64) * 64 if extra else f.n for f in F]
+        th, g = [], []
+        for f, s in zip(F, size):
+            for to, fill in ((th, 0.25), (g, behind)):
+                t = torch.full((s,), fill, device="cuda")
+                t[:f.n] = to_cuda(r.standard_normal(f.n))
+                to.append(t)
+        opt = dl.InnerAdamW(F, th, g, bits=bits, max_norm=0.5, **HYPER)
+        clip = opt.step()
+        norm = base._norm64([t[:f.n] for f, t in zip(F, g)])
+        assert abs(float(clip[0]) - norm) <= NORM_TOL * norm
+        results.append([clip] + [t[:f.n].clone() for f, t in zip(F, th)])
+        assert all((t[f.n:] == 0.25).all() for f, t in zip(F, th))
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+def test_inner_adamw_takes_generators_and_missing_buffers(dl):
+    """Buffers given as generators clip as lists do; an empty fragment needs no
+    gradient buffer."""
+    rng = np.random.default_rng(6)
+    numels = [[64], [0], [40]]
+    vals = [rng.standard_normal(sum(n)) for n in numels]
+    out = []
+    for lazily in (False, True):
+        F = [dl.Fragment(n) for n in numels]
+        th = [torch.ones(f.n, device="cuda") for f in F]
+        g = [to_cuda(v) if v.size else None for v in vals]
+        opt = dl.InnerAdamW(iter(F) if lazily else F, iter(th) if lazily else th,
+                            iter(g) if lazily else g, max_norm=0.1, **HYPER)
+        out.append([opt.step()] + th)
+        norm = base._norm64([t for t in g if t is not None])
+        assert abs(float(out[-1][0][0]) - norm) <= NORM_TOL * norm
+    assert all(torch.equal(a, b) for a, b in zip(*out))
