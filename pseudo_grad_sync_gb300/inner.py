@@ -264,14 +264,16 @@ class InnerAdamW:
         self.workspace = new_workspace(grad_norm_workspace_bytes(), dev)
 
     def step(self, lr=None, stream=None):
-        """Clip (with max_norm) and step; returns the device tensor (norm,
-        coefficient) or, without max_norm, None."""
-        self.steps += 1
+        """Clip (with max_norm) and step; returns ``clip``, the device tensor
+        (norm, coefficient), or, without max_norm, None. The next step writes
+        the same tensor: clone() what is to be kept. A call that raises is not
+        counted."""
         clip = None
         if self.max_norm is not None:
             clip = grad_norm(self.grads, self.max_norm, self.clip, self.workspace, stream)
-        adamw_step(self.jobs, self.steps, self.lr if lr is None else lr, self.betas, self.eps,
+        adamw_step(self.jobs, self.steps + 1, self.lr if lr is None else lr, self.betas, self.eps,
                    self.weight_decay, clip, self.seed, stream)
+        self.steps += 1
         return clip
 
 

@@ -247,3 +247,31 @@ def test_inner_adamw_takes_generators_and_missing_buffers(dl):
         norm = base._norm64([t for t in g if t is not None])
         assert abs(float(out[-1][0][0]) - norm) <= NORM_TOL * norm
     assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+def test_a_step_that_raised_is_not_counted(dl):
+    F = dl.Fragment([100])
+    th, g = torch.zeros(100, device="cuda"), torch.ones(100, device="cuda")
+    opt = dl.InnerAdamW([F], [th], [g], max_norm=1.0, **HYPER)
+    opt.step()
+    before = th.clone()
+    with pytest.raises(dl.DLError):
+        opt.step(lr=-1.0)
+    assert opt.steps == 1 and torch.equal(th, before)
+    opt.step()
+    assert opt.steps == 2
+
+
+def test_a_step_returns_the_clip_that_the_next_one_writes(dl):
+    F = dl.Fragment([1000])
+    th, g = torch.zeros(1000, device="cuda"), torch.ones(1000, device="cuda")
+    opt = dl.InnerAdamW([F], [th], [g], max_norm=1.0, **HYPER)
+    kept = []
+    for k in range(3):
+        g.fill_(k + 1.0)
+        clip = opt.step()
+        assert clip is opt.clip
+        kept.append(clip.clone())
+    for k, c in enumerate(kept):
+        n = (k + 1) * 1000 ** 0.5
+        assert abs(float(c[0]) / n - 1) <= NORM_TOL and abs(float(c[1]) * n - 1) <= 2 * NORM_TOL
