@@ -275,3 +275,31 @@ def test_a_step_returns_the_clip_that_the_next_one_writes(dl):
     for k, c in enumerate(kept):
         n = (k + 1) * 1000 ** 0.5
         assert abs(float(c[0]) / n - 1) <= NORM_TOL and abs(float(c[1]) * n - 1) <= 2 * NORM_TOL
+
+
+# ----------------------------------------------------------------------------
+# layer norm backward: rows on a large offset
+
+
+@pytest.mark.parametrize("offset", [0.0, 10.0, 100.0, 1000.0])
+@pytest.mark.parametrize("width", [100, 512, 4096, 11_008, 20_000])
+def test_dx_of_rows_on_an_offset(dl, width, offset):
+    """dy along xhat, so that dx is small against its terms. From the same
+    statistics: x - mean is rounded once (u of the difference, whatever the
+    offset) and xhat is off by 2 u; w dy by u; the row sums by 85 u of their
+    terms, so their means by 91 u with 1/width and their products; the products
+    of the last steps by 5 u of their terms, and the result by u."""
+    rng = np.random.default_rng(width)
+    rows = 16
+    x = to_cuda(offset + rng.standard_normal((rows, width)))
+    w = to_cuda(1 + 0.3 * rng.standard_normal(width))
+    _, mean, rstd = dl.layernorm_forward(x, w)
+    r = np64(rstd)[:, None]
+    h = (np64(x) - np64(mean)[:, None]) * r
+    dy = to_cuda((h + 0.05 * rng.standard_normal(h.shape)) / np64(w))
+    dx, _, _ = dl.layernorm_backward(dy, x, w, mean, rstd)
+    want, _, _, h = ref.norm64_backward(np64(dy), np64(x), np64(w), np64(mean), np64(rstd), False)
+    wdy = abs(np64(dy) * np64(w))
+    along = (wdy * abs(h)).mean(1, keepdims=True)
+    tol = U * (2 * abs(want) + r * (5 * wdy + 95 * wdy.mean(1, keepdims=True) + 100 * abs(h) * along))
+    assert np.all(abs(np64(dx) - want) <= tol), float((abs(np64(dx) - want) / tol).max())
