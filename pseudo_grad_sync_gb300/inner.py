@@ -38,6 +38,37 @@ _PARAMS = (torch.float32, torch.bfloat16)
 # time counts. Handles are therefore taken as integers (the declared argument
 # types convert them), and the current stream without making a Stream object.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+# The library launches on the current device. A call whose buffers live on
+# another one makes it current first (one comparison of indexes when not).
+
+
+def _away(device):
+    """Whether device is a GPU other than the current one."""
+    return device.type == "cuda" and device.index != _current()
+
+
+def _stream_of(stream, device):
+    """stream, which must be one of a call's device."""
+    if device.type == "cuda" and stream.device != device:
+        raise ValueError(f"stream of {stream.device}, buffers on {device}")
+    return stream
+
+
+def _one_device(*items):
+    """After _cuda: every tensor given (or in a list given) on one device."""
+    first = None
+    for it in items:
+        for t in (it if isinstance(it, (list, tuple)) else [it]):
+            if t is None:
+                continue
+            if first is None:
+                first = t.device
+            elif t.device != first:
+                raise ValueError(f"tensors must be on one device, found {first} and {t.device}")
+    return first
 
 
 def _on(stream, device):
@@ -53,13 +84,15 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _buffer(t, dtype, n, name):
+def _buffer(t, dtype, n, name, device):
     """_need and the device check of one buffer, for the frequent case."""
-    if (type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.numel() >= n
-            and t.is_contiguous()):
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == device.index
+            and t.numel() >= n and t.is_contiguous()):
         return
     _need(t, (dtype,), n, name)
     _cuda(t)
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the other buffers on {device}")
 
 
 class _AdamWJob(ctypes.Structure):
@@ -115,6 +148,7 @@ class GradList:
             raise TypeError(f"grads[0]: dtype {dtype}, expected float32 or bfloat16")
         _need_all(self.grads, (dtype,), 0, "grads")
         _cuda(self.grads)
+        self.device = _one_device(self.grads)  # None for an empty list
         n = len(self.grads)
         self.type = _TYPE[dtype]
         self._ptrs = (ctypes.c_void_p * max(n, 1))(*[g.data_ptr() for g in self.grads])
@@ -128,20 +162,24 @@ def grad_norm(grads, max_norm=math.inf, out=None, workspace=None, stream=None):
     device float32 tensor (norm, coefficient), the ``clip`` of adamw_step.
     workspace: of grad_norm_workspace_bytes(), zeroed when allocated
     (new_workspace); calls on different streams need their own."""
-    if stream is not None:  # what is allocated here belongs to that stream
-        with torch.cuda.stream(stream):
-            return grad_norm(grads, max_norm, out, workspace)
     G = grads if isinstance(grads, GradList) else GradList(grads)
+    if G.device is None and out is None:
+        raise ValueError("grad_norm: an empty list needs an out tensor")
+    device = G.device or out.device
+    if stream is not None:  # what is allocated here belongs to that stream
+        with torch.cuda.stream(_stream_of(stream, device)):
+            return grad_norm(G, max_norm, out, workspace)
+    if _away(device):
+        with torch.cuda.device(device):
+            return grad_norm(G, max_norm, out, workspace)
     if out is None:
-        if not G.grads:
-            raise ValueError("grad_norm: an empty list needs an out tensor")
-        out = torch.empty(2, dtype=torch.float32, device=G.grads[0].device)
+        out = torch.empty(2, dtype=torch.float32, device=device)
     if workspace is None:
-        workspace = new_workspace(grad_norm_workspace_bytes(), out.device)
-    _buffer(out, torch.float32, 2, "out")
-    _buffer(workspace, torch.uint8, 0, "workspace")
+        workspace = new_workspace(grad_norm_workspace_bytes(), device)
+    _buffer(out, torch.float32, 2, "out", device)
+    _buffer(workspace, torch.uint8, 0, "workspace", device)
     st = lib().dl_grad_norm(G._ptrs, G._numel, len(G.grads), G.type, max_norm, out.data_ptr(),
-                            workspace.data_ptr(), workspace.numel(), _on(None, out.device))
+                            workspace.data_ptr(), workspace.numel(), _on(None, device))
     if st:
         raise DLError("dl_grad_norm", st)
     return out
@@ -198,12 +236,14 @@ class AdamWJobs:
                 setattr(self._jobs[j], "d_decay" if name == "decay" else name,
                         None if t is None else t.data_ptr())
             self._jobs[j].frag = ctypes.pointer(F._c)
-        _cuda(*lists.values())
+        offsets = [F.d_offsets for F in self.frags]
+        _cuda(*lists.values(), offsets)
         self.buffers = lists
         self._cfg = _AdamWConfig()
         self._cfg_ref = ctypes.byref(self._cfg)
-        used = [t for x in lists.values() for t in x if t is not None]
-        self.device = used[0].device if used else torch.device("cuda", torch.cuda.current_device())
+        self.device = _one_device(*lists.values(), offsets) or torch.device(
+            "cuda", torch.cuda.current_device())
+        self._index = self.device.index
 
 
 def adamw_step(jobs: AdamWJobs, step, lr=4e-4, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1,
@@ -212,8 +252,13 @@ def adamw_step(jobs: AdamWJobs, step, lr=4e-4, betas=(0.9, 0.95), eps=1e-8, weig
     from 1. clip: device float32 (norm, coefficient) as grad_norm returns it;
     a coefficient that is not finite skips the step on the device. seed: of
     the 8-bit states' rounding; it may stay the same over a run."""
+    if jobs._index != _current():
+        with torch.cuda.device(jobs.device):
+            return adamw_step(jobs, step, lr, betas, eps, weight_decay, clip, seed, stream)
+    if stream is not None:
+        _stream_of(stream, jobs.device)
     if clip is not None:
-        _buffer(clip, torch.float32, 2, "clip")
+        _buffer(clip, torch.float32, 2, "clip", jobs.device)
     c = jobs._cfg
     c.lr, (c.beta1, c.beta2), c.eps, c.weight_decay = lr, betas, eps, weight_decay
     c.step, c.seed = step, seed & (2**64 - 1)
@@ -354,15 +399,18 @@ def layernorm_forward(x, weight, bias=None, eps=1e-5, rms=False, y=None, mean=No
     """Layer norm over the last dimension (dl_layernorm_forward). Returns
     (y, mean, rstd), mean None with rms=True. x: float32, bfloat16 or float16
     with a contiguous last dimension; weight, bias: float32 or bfloat16."""
-    if stream is not None:
-        with torch.cuda.stream(stream):
-            return layernorm_forward(x, weight, bias, eps, rms, y, mean, rstd)
     xp, xs = _rows(x, "x")
+    device = x.device
+    if stream is not None:
+        with torch.cuda.stream(_stream_of(stream, device)):
+            return layernorm_forward(x, weight, bias, eps, rms, y, mean, rstd)
+    if _away(device):
+        with torch.cuda.device(device):
+            return layernorm_forward(x, weight, bias, eps, rms, y, mean, rstd)
     shape = x.shape
     width = shape[-1]
     rows = x.numel() // width
     ptype = _params(weight, bias, width)
-    device = x.device
     if y is None:
         y = _empty_like(x)
         yp, ys = (y.data_ptr() if xp is not None else None), width
@@ -377,9 +425,13 @@ def layernorm_forward(x, weight, bias=None, eps=1e-5, rms=False, y=None, mean=No
         mean = torch.empty(shape[:-1], dtype=torch.float32, device=device)
     if given:
         mean = _stats(mean, rstd, rows, rms)
-    if xp is None or yp is None or not (weight.is_cuda and rstd.is_cuda and (
-            bias is None or bias.is_cuda) and (mean is None or mean.is_cuda)):
+    at = x.get_device()
+    if xp is None or not (
+            y.get_device() == at and weight.get_device() == at and rstd.get_device() == at
+            and (bias is None or bias.get_device() == at)
+            and (mean is None or mean.get_device() == at)):
         _cuda(x, weight, bias, y, mean, rstd)
+        _one_device(x, weight, bias, y, mean, rstd)
     st = lib().dl_layernorm_forward(xp, xs, _TYPE[x.dtype], rows, width, weight.data_ptr(),
                                     _at(bias), ptype, eps, DL_NORM_RMS if rms else 0, yp, ys,
                                     _at(mean), rstd.data_ptr(), _on(None, device))
@@ -397,16 +449,20 @@ def layernorm_backward(dy, x, weight, mean, rstd, dweight=None, dbias=None, rms=
     a call that passes dweight alone computes no dbias. A copy that timed out
     is reported by read_device_status(None), and by the workspace's status
     word when the caller passed one."""
+    xp, xs = _rows(x, "x")
+    device = x.device
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with torch.cuda.stream(_stream_of(stream, device)):
             return layernorm_backward(dy, x, weight, mean, rstd, dweight, dbias, rms, accumulate,
                                       dx, workspace, bias)
-    xp, xs = _rows(x, "x")
+    if _away(device):
+        with torch.cuda.device(device):
+            return layernorm_backward(dy, x, weight, mean, rstd, dweight, dbias, rms, accumulate,
+                                      dx, workspace, bias)
     dyp, ds = _rows(dy, "dy", x)
     width = x.shape[-1]
     rows = x.numel() // width
     ptype = _params(weight, None, width)
-    device = x.device
     if dweight is None:
         if accumulate:
             raise ValueError("accumulate: needs the dweight to add to")
@@ -425,10 +481,14 @@ def layernorm_backward(dy, x, weight, mean, rstd, dweight=None, dbias=None, rms=
     _need(dweight, (weight.dtype,), width, "dweight")
     _need(dbias, (weight.dtype,), width, "dbias")
     _need(workspace, _U8, 0, "workspace")
-    if xp is None or dyp is None or dxp is None or not (
-            weight.is_cuda and rstd.is_cuda and dweight.is_cuda and workspace.is_cuda
-            and (mean is None or mean.is_cuda) and (dbias is None or dbias.is_cuda)):
+    at = x.get_device()
+    if xp is None or not (
+            dy.get_device() == at and dx.get_device() == at and weight.get_device() == at
+            and rstd.get_device() == at and dweight.get_device() == at
+            and workspace.get_device() == at and (mean is None or mean.get_device() == at)
+            and (dbias is None or dbias.get_device() == at)):
         _cuda(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace)
+        _one_device(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace)
     flags = (DL_NORM_RMS if rms else 0) | (DL_NORM_ACCUMULATE if accumulate else 0)
     st = lib().dl_layernorm_backward(
         dyp, ds, xp, xs, _TYPE[x.dtype], rows, width, weight.data_ptr(), ptype, _at(mean),

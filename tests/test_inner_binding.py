@@ -114,3 +114,149 @@ def test_a_bias_of_another_length_has_no_gradient(formulas):
     for n in (1, 63, 65):
         with pytest.raises(ValueError, match=f"bias: {n} elements, expected 64"):
             dl.layer_norm(x, w, torch.zeros(n))
+
+
+# ----------------------------------------------------------------------------
+# devices: tensors that say that they live on a GPU, a library that notes where
+# it was called
+
+
+class _Placed(torch.Tensor):
+    """A host tensor that gives a GPU as its device."""
+    @staticmethod
+    def on(t, index):
+        t = t.as_subclass(_Placed)
+        t._index = index
+        return t
+
+    device = property(lambda self: torch.device("cuda", self._index))
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return self._index
+
+    @classmethod
+    def __torch_function__(cls, func, types, args=(), kwargs=None):
+        with torch._C.DisableTorchFunctionSubclass():
+            return func(*args, **(kwargs or {}))
+
+
+class _Stream:
+    def __init__(self, index):
+        self.device, self.cuda_stream = torch.device("cuda", index), 100 + index
+
+
+@pytest.fixture
+def machine(monkeypatch):
+    """Two GPUs, the first one current, as far as the binding can see."""
+    state = {"current": 0, "calls": []}
+
+    class Device:
+        def __init__(self, device):
+            self.index = torch.device(device).index
+
+        def __enter__(self):
+            self.before, state["current"] = state["current"], self.index
+
+        def __exit__(self, *a):
+            state["current"] = self.before
+
+    class On(Device):
+        def __init__(self, stream):
+            self.index = stream.device.index
+
+    class Library:
+        def __getattr__(self, name):
+            if name.endswith(("_bytes", "_slots")):
+                return getattr(real, name)
+
+            def call(*args):
+                state["calls"].append((name, state["current"], args[-1]))
+                return 0
+            return call
+    real = dl.lib()
+    monkeypatch.setattr(inner, "lib", lambda: Library())
+    monkeypatch.setattr(inner, "_current", lambda: state["current"])
+    monkeypatch.setattr(inner, "_raw_stream", lambda index: 10 + index)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    return state
+
+
+def _on(index, *sizes, dtype=torch.float32):
+    return [_Placed.on(torch.zeros(s, dtype=dtype), index) for s in sizes]
+
+
+def _fragment(numels, index):
+    F = dl.Fragment(numels, device="cpu")
+    F.d_offsets = _Placed.on(F.d_offsets, index)
+    return F
+
+
+def _calls(index):
+    """Every inner-step call, with all its buffers on one GPU."""
+    x, y, w, mean, rstd = _on(index, (4, 8), (4, 8), 8, 4, 4)
+    dw, db, out, grad, theta, m, v = _on(index, 8, 8, 2, 12, 12, 12, 12)
+    ws, = _on(index, max(inner.grad_norm_workspace_bytes(), inner.layernorm_workspace_bytes(4, 8)),
+              dtype=torch.uint8)
+    J = dl.AdamWJobs([_fragment([5, 7], index)], [theta], [grad], [m], [v])
+    return {
+        "dl_grad_norm": lambda **k: dl.grad_norm([grad], 1.0, **{"out": out, "workspace": ws, **k}),
+        "dl_adamw_step": lambda **k: dl.adamw_step(J, 1, **{"clip": out, **k}),
+        "dl_layernorm_forward": lambda **k: dl.layernorm_forward(
+            x, **{"weight": w, "bias": db, "y": y, "mean": mean, "rstd": rstd, **k}),
+        "dl_layernorm_backward": lambda **k: dl.layernorm_backward(
+            y, x, **{"weight": w, "mean": mean, "rstd": rstd, "dweight": dw, "dbias": db, "dx": y,
+                     "workspace": ws, **k}),
+    }
+
+
+CALLS = ["dl_grad_norm", "dl_adamw_step", "dl_layernorm_forward", "dl_layernorm_backward"]
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_a_call_runs_on_its_buffers_device(machine, name):
+    for index in (0, 1):
+        _calls(index)[name]()
+        assert machine["calls"].pop() == (name, index, 10 + index) and machine["current"] == 0
+        _calls(index)[name](stream=_Stream(index))
+        got, at, stream = machine["calls"].pop()
+        assert (got, at) == (name, index) and machine["current"] == 0 and not machine["calls"]
+        assert stream in (100 + index, 10 + index)  # given, or made current with its device
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_a_stream_of_another_device_is_refused(machine, name):
+    for index in (0, 1):
+        with pytest.raises(ValueError, match=f"stream of cuda:{1 - index}, buffers on cuda:{index}"):
+            _calls(index)[name](stream=_Stream(1 - index))
+    assert not machine["calls"]
+
+
+@pytest.mark.parametrize("name,arg,size", [
+    ("dl_grad_norm", "out", 2), ("dl_grad_norm", "workspace", 1 << 16), ("dl_adamw_step", "clip", 2),
+    ("dl_layernorm_forward", "weight", 8), ("dl_layernorm_forward", "bias", 8),
+    ("dl_layernorm_forward", "y", (4, 8)), ("dl_layernorm_forward", "mean", 4),
+    ("dl_layernorm_forward", "rstd", 4), ("dl_layernorm_backward", "weight", 8),
+    ("dl_layernorm_backward", "mean", 4), ("dl_layernorm_backward", "rstd", 4),
+    ("dl_layernorm_backward", "dweight", 8), ("dl_layernorm_backward", "dbias", 8),
+    ("dl_layernorm_backward", "dx", (4, 8)), ("dl_layernorm_backward", "workspace", 1 << 16)])
+def test_buffers_of_two_devices_are_refused(machine, name, arg, size):
+    for index in (0, 1):
+        other, = _on(1 - index, size, dtype=torch.uint8 if arg == "workspace" else torch.float32)
+        with pytest.raises(ValueError, match="cuda:0.*cuda:1|cuda:1.*cuda:0"):
+            _calls(index)[name](**{arg: other})
+    assert not machine["calls"]
+
+
+def test_lists_of_two_devices_are_refused(machine):
+    (a, b, c, d), (e,) = _on(0, 12, 12, 12, 12), _on(1, 12)
+    with pytest.raises(ValueError, match="one device"):
+        dl.GradList([a, e])
+    F = _fragment([5, 7], 0)
+    with pytest.raises(ValueError, match="one device"):
+        dl.AdamWJobs([F], [a], [b], [c], [e])
+    with pytest.raises(ValueError, match="one device"):  # the offsets, which the kernels read
+        dl.AdamWJobs([_fragment([5, 7], 1)], [a], [b], [c], [d])
+    with pytest.raises(ValueError, match="CUDA device"):
+        dl.AdamWJobs([dl.Fragment([5, 7], device="cpu")], [a], [b], [c], [d])
