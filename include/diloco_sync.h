@@ -473,7 +473,7 @@ typedef struct dl_adamw_job {
 typedef struct dl_adamw_config {
     double lr;           /* >= 0; lr * weight_decay and lr / (1 - beta1^step) at most FLT_MAX */
     double beta1, beta2; /* in [0, 1) */
-    double eps;          /* >= FLT_MIN */
+    double eps;          /* FLT_MIN to 2^125 */
     double weight_decay; /* >= 0 */
     int64_t step;        /* this step's number, from 1: the bias corrections' exponent */
     uint64_t seed;       /* of the 8-bit states' rounding */

@@ -206,6 +206,11 @@ struct AdamArgs {
     const float* clip;
 };
 
+// The approximate quotients below take a denominator beyond 2^126 for infinite
+// (the update would be lost). A finite root is below 2^64 and its scale below
+// 2^27, so eps alone could reach that far.
+constexpr double kMostEps = 0x1p125;
+
 // theta' from the new moments; root = sqrt(v')
 __device__ __forceinline__ float step_theta(const AdamArgs& a, float theta, float m, float root,
                                             float keep) {
@@ -848,7 +853,7 @@ extern "C" int dl_adamw_step(const dl_adamw_job* jobs, int32_t n_jobs, int32_t g
         (state_type != DL_F32 && state_type != DL_E4M3))
         return DL_ERR_ARG;
     if (!(cfg->lr >= 0.0 && cfg->lr <= FLT_MAX) || !(cfg->beta1 >= 0.0 && cfg->beta1 < 1.0) ||
-        !(cfg->beta2 >= 0.0 && cfg->beta2 < 1.0) || !(cfg->eps >= FLT_MIN && cfg->eps <= FLT_MAX) ||
+        !(cfg->beta2 >= 0.0 && cfg->beta2 < 1.0) || !(cfg->eps >= FLT_MIN && cfg->eps <= kMostEps) ||
         !(cfg->weight_decay >= 0.0 && cfg->weight_decay <= FLT_MAX) || cfg->step < 1)
         return DL_ERR_ARG;
     if (!aligned_to(d_clip, 4)) return DL_ERR_ALIGN;

@@ -1,6 +1,8 @@
 """The inner-step binding on the host (no GPU): sizes that do not fit the ABI's
 arguments, what it passes on, and the autograd operation with the two norm
 calls replaced by their formulas in torch."""
+import ctypes
+
 import pytest
 import torch
 
@@ -28,6 +30,22 @@ def test_widths_beyond_the_abi_are_refused():
     x, w = (torch.empty(s, dtype=torch.bfloat16, device="meta") for s in ((2, 2**31 - 1), (2**31 - 1,)))
     with pytest.raises(ValueError, match="CUDA device"):  # the widest that fits: the next check
         dl.layernorm_forward(x, w)
+
+
+def test_adamw_refuses_an_eps_whose_quotient_is_lost(library):
+    """Beyond 2^126 the approximate quotient is 0, whatever the moment: with
+    lr = eps = 2e38 the update would be m, and was nothing."""
+    off = torch.tensor([0, 4], dtype=torch.int64)
+    f = dl._Fragment(off.data_ptr(), 1 << 20, 1)
+    for state in (0, 3):
+        for eps, refused in ((2.0 ** 125, False), (2.0 ** 125 * 1.01, True), (2e38, True), (3.4e38, True)):
+            job = (inner._AdamWJob * 1)()
+            job[0].frag = ctypes.pointer(f)
+            for k in ("theta", "grad", "m", "v", "m_scale", "v_scale"):
+                setattr(job[0], k, (1 << 20) + (4 if k == "theta" else 0))  # theta off 16 bytes
+            c = inner._AdamWConfig(1e-3, 0.9, 0.95, eps, 0.1, 1, 0)
+            got = library.dl_adamw_step(job, 1, 0, state, ctypes.byref(c), None, None)
+            assert got == (-1 if refused else -2), eps  # -2: the next check, of theta's alignment
 
 
 # ----------------------------------------------------------------------------
