@@ -454,9 +454,11 @@ __device__ __forceinline__ void step_quad(const AdamArgs& a, float coef, float k
     float c[4], d[4];
     decode4(q.cm, c);
     decode4(q.cs, d);
-    // The scales are powers of two: folded into the betas they give the same
-    // bits as value = code * scale first (the code's square is exact too).
-    const float2 b1 = both(a.beta1 * q.msc), b2 = both(a.beta2 * (q.ssc * q.ssc));
+    // m's scale, a power of two, is folded into beta1: the same bits as value =
+    // code * scale first. s takes its own product: folded into a small beta2 the
+    // smallest scale's square would leave fp32's normal range, and a square that
+    // is Inf could come out finite (measured with the fold: 0.5% faster).
+    const float2 b1 = both(a.beta1 * q.msc), b2 = both(a.beta2), ssc = both(q.ssc);
     // The definition rounds the products before the sum. A packed product and
     // a packed sum come out fused (CUDA 13.0, their .rn notwithstanding: exact
     // cancellations then leave a residue), so the sums are x * one + y with a
@@ -465,10 +467,11 @@ __device__ __forceinline__ void step_quad(const AdamArgs& a, float coef, float k
     float2 m[2], v[2], r[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const float2 cd = make_float2(c[2 * h], c[2 * h + 1]), dd = make_float2(d[2 * h], d[2 * h + 1]);
+        const float2 cd = make_float2(c[2 * h], c[2 * h + 1]);
+        const float2 s = mul2(make_float2(d[2 * h], d[2 * h + 1]), ssc);
         const float2 g = mul2(q.gr[h], both(coef));
         m[h] = fma2(mul2(cd, b1), one, mul2(g, both(a.om_beta1)));
-        v[h] = fma2(mul2(mul2(dd, dd), b2), one, mul2(mul2(g, g), both(a.om_beta2)));
+        v[h] = fma2(mul2(mul2(s, s), b2), one, mul2(mul2(g, g), both(a.om_beta2)));
         r[h] = root2(v[h]);
     }
     // Zeros and tiny values take the exact function, as does Inf, whose

@@ -303,3 +303,53 @@ def test_dx_of_rows_on_an_offset(dl, width, offset):
     along = (wdy * abs(h)).mean(1, keepdims=True)
     tol = U * (2 * abs(want) + r * (5 * wdy + 95 * wdy.mean(1, keepdims=True) + 100 * abs(h) * along))
     assert np.all(abs(np64(dx) - want) <= tol), float((abs(np64(dx) - want) / tol).max())
+
+
+# ----------------------------------------------------------------------------
+# the ends of the ranges
+
+
+@pytest.mark.parametrize("b2", [1e-9, 0.003, 0.0, 0.95])
+def test_adamw8_smallest_scales_and_small_betas(dl, b2):
+    """The smallest scale's square times a small beta2 lies below fp32's normal
+    range; the moments are those of value = code * scale all the same, codes
+    and scales bit for bit."""
+    rng = np.random.default_rng(1)
+    n = [128 * 9 + 5, 128 * 4]
+    F = dl.Fragment(n)
+    g = to_cuda(rng.standard_normal(F.n) * 1e-22)
+    g[::3] = 0
+    th = torch.zeros(F.n, device="cuda")
+    e4 = torch.float8_e4m3fn
+    m, v = (torch.from_numpy(rng.integers(0, 0x78, F.n).astype(np.uint8)).cuda().view(e4)
+            for _ in range(2))
+    slots = dl.adamw_scale_slots(F)
+    msc, ssc = (torch.full((slots,), 2.0 ** -60, device="cuda") for _ in range(2))
+    old = (codes(m), codes(v), msc.cpu().numpy(), ssc.cpu().numpy())
+    dl.adamw_step(dl.AdamWJobs([F], [th], [g], [m], [v], [msc], [ssc]), 5, lr=1e-3, betas=(0.9, b2),
+                  seed=4)
+    want = ref.adamw8_codes(g.cpu().numpy(), *old, n, 5, 0.9, b2, 1.0, 4)
+    for got, w in zip((codes(m), msc.cpu().numpy(), codes(v), ssc.cpu().numpy()), want):
+        assert np.array_equal(got, w)
+
+
+def test_adamw8_a_root_beyond_fp32_squares(dl):
+    """code * scale = 2^64: its square is Inf, so the block's new scale is NaN;
+    its neighbours' are not."""
+    F = dl.Fragment([384])
+    th, g = torch.zeros(384, device="cuda"), torch.zeros(384, device="cuda")
+    e4 = torch.float8_e4m3fn
+    m = torch.zeros(384, dtype=torch.uint8, device="cuda").view(e4)
+    v = torch.zeros(384, dtype=torch.uint8, device="cuda")
+    v[130] = 0x78  # 256
+    v[5] = 0x70    # 128
+    v = v.view(e4)
+    slots = dl.adamw_scale_slots(F)
+    msc, ssc = (torch.full((slots,), 2.0 ** 56, device="cuda") for _ in range(2))
+    old = (codes(m), codes(v), msc.cpu().numpy(), ssc.cpu().numpy())
+    dl.adamw_step(dl.AdamWJobs([F], [th], [g], [m], [v], [msc], [ssc]), 2, seed=1, **HYPER)
+    want = ref.adamw8_codes(g.cpu().numpy(), *old, [384], 2, 0.9, 0.95, 1.0, 1)
+    assert np.isnan(want[3][1]) and np.isfinite(want[3][[0, 2]]).all()
+    assert np.array_equal(ssc.cpu().numpy(), want[3], equal_nan=True)
+    keep = np.r_[0:128, 256:384]
+    assert np.array_equal(codes(v)[keep], want[2][keep])
