@@ -19,7 +19,7 @@ constexpr int kNormVecs = 8;      // 16-byte loads of a thread in flight
 constexpr int kNormChunk = kThreads * kNormVecs;  // 16-byte vectors per chunk
 
 struct NormWorkspace {  // after the header; zeroed once, left as found
-    double total;       // sum over the launches of one call so far
+    double total;       // sum over the launches of one call so far; the first sets it
     uint32_t done;      // blocks of this launch that have finished
     double partial[kNormBlocks];
 };
@@ -29,7 +29,7 @@ struct NormArgs {
     int64_t numel[kNormBuffers];
     int64_t chunk_end[kNormBuffers];  // running number of chunks
     int n;
-    int last;  // the call's last launch
+    int first, last;  // whether this is the call's first, its last launch
     double max_norm;
     float* out;
     NormWorkspace* ws;
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ 
     if (lane == 0) red[warp] = s;
     __syncthreads();
     if (threadIdx.x == 0) {
-        double t = a.ws->total;
+        double t = a.first ? 0.0 : a.ws->total;  // a call that failed halfway leaves a total
         for (int w = 0; w < kWarps; ++w) t += red[w];
         a.ws->done = 0;
         a.ws->total = a.last ? 0.0 : t;
@@ -804,6 +804,7 @@ extern "C" int dl_grad_norm(const void* const* grads, const int64_t* numel, int3
     a.out = d_out;
     a.ws = reinterpret_cast<NormWorkspace*>(static_cast<char*>(d_workspace) + kWsHeader);
     int32_t i = 0;
+    int first = 1;
     do {
         a.n = 0;
         int64_t chunks = 0;
@@ -817,7 +818,9 @@ extern "C" int dl_grad_norm(const void* const* grads, const int64_t* numel, int3
             a.numel[a.n] = numel[i];
             a.chunk_end[a.n++] = chunks;
         }
+        a.first = first;
         a.last = i == n_grads;
+        first = 0;
         if (a.n == 0) {  // nothing left to read: one block writes the result
             a.g[0] = nullptr;
             a.numel[0] = 0;

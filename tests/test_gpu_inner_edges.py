@@ -353,3 +353,16 @@ def test_adamw8_a_root_beyond_fp32_squares(dl):
     assert np.array_equal(ssc.cpu().numpy(), want[3], equal_nan=True)
     keep = np.r_[0:128, 256:384]
     assert np.array_equal(codes(v)[keep], want[2][keep])
+
+
+def test_grad_norm_after_an_interrupted_call(dl):
+    """A call of several launches that stopped halfway (its error was reported)
+    leaves a running total behind; the next call does not add to it."""
+    rng = np.random.default_rng(9)
+    for count in (1, 200):
+        bufs = [to_cuda(rng.standard_normal(500)) for _ in range(count)]
+        ws = dl.new_workspace(dl.grad_norm_workspace_bytes())
+        want = dl.grad_norm(bufs, 1.0, workspace=ws).clone()
+        ws[256:264].view(torch.float64).fill_(1e6)  # the workspace's running total
+        assert torch.equal(dl.grad_norm(bufs, 1.0, workspace=ws), want)
+        assert torch.equal(dl.grad_norm(bufs, 1.0, workspace=ws), want)
