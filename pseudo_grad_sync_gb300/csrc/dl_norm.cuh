@@ -13,6 +13,8 @@
 // are loaded straight into registers.
 #pragma once
 
+#include <float.h>
+
 #include "dl_phase.h"
 #include "dl_types.cuh"
 
@@ -180,10 +182,12 @@ struct RowSum {
 };
 
 // s / n with its rounding corrected by the remainder (inv = 1 / n): a
-// constant row's mean is then the constant itself, whatever the width.
+// constant row's mean is then the constant itself, whatever the width. The
+// remainder of an infinite sum is NaN, for which the larger operand is the
+// other one: the mean stays infinite.
 __device__ __forceinline__ float divided(float s, float n, float inv) {
     const float q = s * inv;
-    return fmaf(fmaf(-q, n, s), inv, q);
+    return fmaf(fmaxf(fmaf(-q, n, s), -FLT_MAX), inv, q);
 }
 
 // Sum over the whole block, for rows that a block reads several times.

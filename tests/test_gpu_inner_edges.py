@@ -366,3 +366,18 @@ def test_grad_norm_after_an_interrupted_call(dl):
         ws[256:264].view(torch.float64).fill_(1e6)  # the workspace's running total
         assert torch.equal(dl.grad_norm(bufs, 1.0, workspace=ws), want)
         assert torch.equal(dl.grad_norm(bufs, 1.0, workspace=ws), want)
+
+
+@pytest.mark.parametrize("width", [5, 64, 300, 1000, 4096, 5632, 8192, 16_384, 20_000])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_the_mean_of_a_row_with_an_infinity(dl, width, kind):
+    """It is that infinity, NaN only where both signs meet; y is NaN."""
+    x = base._rows(np.random.default_rng(width), 6, width, kind, 0)
+    inf = float("inf")
+    x[0, 0], x[1, width - 1], x[2, 1], x[2, 2], x[3, 3] = inf, -inf, inf, -inf, float("nan")
+    w = to_cuda(np.ones(width))
+    y, mean, rstd = dl.layernorm_forward(x, w)
+    m = mean.tolist()
+    assert m[0] == inf and m[1] == -inf and np.isnan(m[2:4]).all() and np.isfinite(m[4:]).all()
+    assert bool(torch.isnan(y[:4]).all()) and bool(torch.isfinite(y[4:]).all())
+    assert np.isnan(rstd.tolist()[:4]).all()
