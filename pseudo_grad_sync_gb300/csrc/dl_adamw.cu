@@ -50,8 +50,8 @@ __device__ __forceinline__ void unpack(const uint4& q, float (&v)[8], __nv_bfloa
 
 // A group's sum of squares in this range lost nothing to fp32's range: none
 // of its squares overflowed, and a subnormal square is off by 2^-150 at most.
-// Any other group (zeros, tiny or huge values, Inf, NaN) is summed again in
-// fp64.
+// A group of zeros (told by the words' bits) adds nothing; any other group
+// (tiny or huge values, Inf, NaN) is summed again in fp64.
 constexpr float kSquareLo = 0x1p-100f, kSquareHi = 0x1p126f;
 
 // read once, not kept in L1
@@ -118,8 +118,10 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ 
         for (int u = 0; u < kNormVecs; ++u)
             q[u] = i0 + u * kThreads < vecs ? load_once(body + i0 + u * kThreads) : uint4{0, 0, 0, 0};
         float part[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t any = 0;
 #pragma unroll
         for (int u = 0; u < kNormVecs; ++u) {
+            any |= q[u].x | q[u].y | q[u].z | q[u].w;
             float v[W];
             unpack(q[u], v, T());
 #pragma unroll
@@ -128,7 +130,7 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ 
         const float group = (part[0] + part[1]) + (part[2] + part[3]);
         if (group >= kSquareLo && group <= kSquareHi)
             sum += static_cast<double>(group);
-        else
+        else if (any & (sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu))
             sum += squares64<T>(body, i0, vecs);
         if (first == 0) {
             const int64_t rest = n - vecs * W;  // the head's and the tail's elements

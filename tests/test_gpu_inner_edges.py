@@ -381,3 +381,46 @@ def test_the_mean_of_a_row_with_an_infinity(dl, width, kind):
     assert m[0] == inf and m[1] == -inf and np.isnan(m[2:4]).all() and np.isfinite(m[4:]).all()
     assert bool(torch.isnan(y[:4]).all()) and bool(torch.isfinite(y[4:]).all())
     assert np.isnan(rstd.tolist()[:4]).all()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_grad_norm_of_mostly_zeros(dl, kind):
+    """Rows that no token met (an embedding's gradient): zeros of both signs
+    beside values in fp32's range of squares, below and above it."""
+    rng = np.random.default_rng(5)
+    g = to_cuda(np.zeros((600, 4096)), kind)
+    g[::7] = -0.0
+    assert dl.grad_norm([g], 1.0).tolist() == [0.0, 1.0]
+    for scale in (1.0, 1e-30, 1e25):
+        g[3::50] = to_cuda(rng.standard_normal((12, 4096)) * scale, kind)
+        g[17, 5] = scale
+        want = base._norm64([g])
+        got = float(dl.grad_norm([g])[0])
+        assert abs(got - want) <= NORM_TOL * want
+    g[400, 4095] = float("nan")
+    assert np.isnan(dl.grad_norm([g], 1.0).tolist()).all()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_grad_norm_of_zeros_takes_no_longer(dl, kind):
+    """Half again as long as dense values at most (4 GB, beyond L2); read
+    twice, as groups outside the range are, zeros took two to seven times."""
+    n = 1 << (30 if kind == "f32" else 31)
+    G = dl.GradList([torch.ones(n, dtype=base.TYPES[kind], device="cuda")])
+    ws, out = dl.new_workspace(dl.grad_norm_workspace_bytes()), torch.zeros(2, device="cuda")
+    took = []
+    for fill in (1.0, 0.0):
+        G.grads[0].fill_(fill)
+        dl.grad_norm(G, 1.0, out, ws)
+        best = float("inf")
+        for _ in range(5):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            dl.grad_norm(G, 1.0, out, ws)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        took.append(best)
+        norm = n ** 0.5 * fill
+        assert abs(float(out[0]) - norm) <= NORM_TOL * norm
+    assert took[1] <= 1.5 * took[0], took
