@@ -45,9 +45,9 @@ _current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 # another one makes it current first (one comparison of indexes when not).
 
 
-def _away(device):
-    """Whether device is a GPU other than the current one."""
-    return device.type == "cuda" and device.index != _current()
+def _away(index):
+    """Whether a GPU (its index; -1 for the host) is not the current one."""
+    return index >= 0 and index != _current()
 
 
 def _stream_of(stream, device):
@@ -149,6 +149,7 @@ class GradList:
         _need_all(self.grads, (dtype,), 0, "grads")
         _cuda(self.grads)
         self.device = _one_device(self.grads)  # None for an empty list
+        self._index = -1 if self.device is None else self.device.index
         n = len(self.grads)
         self.type = _TYPE[dtype]
         self._ptrs = (ctypes.c_void_p * max(n, 1))(*[g.data_ptr() for g in self.grads])
@@ -169,7 +170,7 @@ def grad_norm(grads, max_norm=math.inf, out=None, workspace=None, stream=None):
     if stream is not None:  # what is allocated here belongs to that stream
         with torch.cuda.stream(_stream_of(stream, device)):
             return grad_norm(G, max_norm, out, workspace)
-    if _away(device):
+    if _away(G._index if G._index >= 0 else out.get_device()):
         with torch.cuda.device(device):
             return grad_norm(G, max_norm, out, workspace)
     if out is None:
@@ -252,7 +253,7 @@ def adamw_step(jobs: AdamWJobs, step, lr=4e-4, betas=(0.9, 0.95), eps=1e-8, weig
     from 1. clip: device float32 (norm, coefficient) as grad_norm returns it;
     a coefficient that is not finite skips the step on the device. seed: of
     the 8-bit states' rounding; it may stay the same over a run."""
-    if jobs._index != _current():
+    if _away(jobs._index):
         with torch.cuda.device(jobs.device):
             return adamw_step(jobs, step, lr, betas, eps, weight_decay, clip, seed, stream)
     if stream is not None:
@@ -404,7 +405,8 @@ def layernorm_forward(x, weight, bias=None, eps=1e-5, rms=False, y=None, mean=No
     if stream is not None:
         with torch.cuda.stream(_stream_of(stream, device)):
             return layernorm_forward(x, weight, bias, eps, rms, y, mean, rstd)
-    if _away(device):
+    at = x.get_device()
+    if _away(at):
         with torch.cuda.device(device):
             return layernorm_forward(x, weight, bias, eps, rms, y, mean, rstd)
     shape = x.shape
@@ -425,7 +427,6 @@ def layernorm_forward(x, weight, bias=None, eps=1e-5, rms=False, y=None, mean=No
         mean = torch.empty(shape[:-1], dtype=torch.float32, device=device)
     if given:
         mean = _stats(mean, rstd, rows, rms)
-    at = x.get_device()
     if xp is None or not (
             y.get_device() == at and weight.get_device() == at and rstd.get_device() == at
             and (bias is None or bias.get_device() == at)
@@ -455,7 +456,8 @@ def layernorm_backward(dy, x, weight, mean, rstd, dweight=None, dbias=None, rms=
         with torch.cuda.stream(_stream_of(stream, device)):
             return layernorm_backward(dy, x, weight, mean, rstd, dweight, dbias, rms, accumulate,
                                       dx, workspace, bias)
-    if _away(device):
+    at = x.get_device()
+    if _away(at):
         with torch.cuda.device(device):
             return layernorm_backward(dy, x, weight, mean, rstd, dweight, dbias, rms, accumulate,
                                       dx, workspace, bias)
@@ -481,7 +483,6 @@ def layernorm_backward(dy, x, weight, mean, rstd, dweight=None, dbias=None, rms=
     _need(dweight, (weight.dtype,), width, "dweight")
     _need(dbias, (weight.dtype,), width, "dbias")
     _need(workspace, _U8, 0, "workspace")
-    at = x.get_device()
     if xp is None or not (
             dy.get_device() == at and dx.get_device() == at and weight.get_device() == at
             and rstd.get_device() == at and dweight.get_device() == at
