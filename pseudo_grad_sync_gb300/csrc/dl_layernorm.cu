@@ -62,6 +62,7 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) k_norm_fwd(const __grid_co
         ring.init();
 #pragma unroll
         for (int i = 0; i < Geo::kStages - 1; ++i) ring.issue(i, begin + i * kGroups, a.x, a.xs, a.x, a.xs);
+        if (a.report.lost) ring.lose(begin);
     }
     float2 w[kPairs], b[kPairs];
     uint32_t valid = 0;  // a bit per element below the width
@@ -157,6 +158,7 @@ __global__ void __launch_bounds__(BLOCK, 512 / BLOCK) k_norm_fwd(const __grid_co
             }
         }
     }
+    if constexpr (BULK) ring.drain();
 }
 
 // Rows too wide for a block's registers: the row is read three times (from
@@ -205,7 +207,7 @@ bool launch(FwdArgs<T> a, cudaStream_t s, int* status) {
     if (grid == 0) return true;
     if (BULK && rounds <= grid) return false;
     if (BULK && library_status_word(&a.report.word) != DL_OK) return true;
-    if (BULK) a.report.polls = wait_polls(kRowPolls);
+    if (BULK) a.report.lost = waits_run_out();
     a.run = (rounds + grid - 1) / grid * Geo::kGroups;
     grid = (a.rows + a.run - 1) / a.run;
     k_norm_fwd<T, N, TPR, EPT, BLOCK, BULK, FULL><<<static_cast<int>(grid), BLOCK, Geo::kBytes, s>>>(a);

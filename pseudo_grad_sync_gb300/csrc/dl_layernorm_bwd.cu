@@ -80,6 +80,7 @@ __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdA
         ring.init();
 #pragma unroll
         for (int i = 0; i < Geo::kStages - 1; ++i) ring.issue(i, begin + i * kGroups, dy, a.ds, x, a.xs);
+        if (a.report.lost) ring.lose(begin);
     }
     float2 w[kPairs], dw[kPairs], db[kPairs];
 #pragma unroll
@@ -169,6 +170,7 @@ __global__ void __launch_bounds__(BLOCK) k_norm_bwd(const __grid_constant__ BwdA
             store_row<T, N, TPR, VPT, FULL>(a.dx + off + r * a.os, out, t, width, a.vec_out);
         }
     }
+    if constexpr (BULK) ring.drain();
     // the join's blocks may take the place of those that end from here on
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // the block's sums over its rows
@@ -303,7 +305,7 @@ int launch_form(BwdArgs<T> a, cudaStream_t s) {
     if (parts > kMostBlocks) parts = kMostBlocks;
     if (BULK && rounds <= parts) return 0;
     if (BULK && library_status_word(&a.report.second) != DL_OK) return DL_ERR_CUDA;
-    if (BULK) a.report.polls = wait_polls(kRowPolls);
+    if (BULK) a.report.lost = waits_run_out();
     a.run = (rounds + parts - 1) / parts * Geo::kGroups;
     parts = (a.rows + a.run - 1) / a.run;
     cudaLaunchConfig_t config = {};
@@ -405,7 +407,7 @@ extern "C" int dl_layernorm_backward(const void* dy, int64_t dy_stride, const vo
         using T = decltype(zero);
         return backward<T>(BwdArgs<T>{static_cast<const T*>(dy), static_cast<const T*>(x),
                                       static_cast<T*>(dx), weight, mean, rstd, part,
-                                      RingReport{static_cast<uint32_t*>(d_workspace), nullptr, 0},
+                                      RingReport{static_cast<uint32_t*>(d_workspace), nullptr, false},
                                       dy_stride, x_stride, dx_stride, rows, 0, width, param_type, rms,
                                       false},
                            s);

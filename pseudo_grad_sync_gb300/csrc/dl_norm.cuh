@@ -220,23 +220,30 @@ __device__ __forceinline__ void prefetch_rows(int64_t first, int groups, int64_t
 
 constexpr int kRowPolls = 1 << 17;  // of a wait for a round's rows: about a second
 
-// Where a ring reports a wait that ran out (either may be null), and after how
-// many polls one does.
+// Where a ring reports a wait that ran out (either may be null), and whether to
+// take the first one for such.
 struct RingReport {
     uint32_t* word;
     uint32_t* second;
-    int polls;
+    bool lost;
 };
 
-// After a wait that ran out, out of line: sets the status words; warp 0 waits
-// for the copies that it has in flight with `left` rounds to go.
+// The end of a block with a wait that ran out: sets the status words, and warp
+// 0, which issued the copies, waits (bounded too) until those in flight at its
+// own failed wait have landed. `record` is what RowRing::record left of it. Out
+// of line, and the record in shared memory: carried in registers, or with the
+// reports in the loop, rows of 5632 took up to 10% longer backward.
 template <int STAGES>
-__device__ __noinline__ void ring_failed(uint64_t* full, RingPhase<STAGES> phase, const RingReport& report,
-                                         int64_t left) {
+__device__ __noinline__ void ring_drain(uint64_t* full, const uint64_t* record, const RingReport& report) {
     if (report.word) atomicOr(report.word, kDevErrCopyTimeout);
     if (report.second) atomicOr(report.second, kDevErrCopyTimeout);
     if (threadIdx.x >= 32) return;
-    for (int i = 0; i < phase.in_flight(left); ++i)
+    __syncwarp();
+    const int at = static_cast<int>(*record);
+    RingPhase<STAGES> phase;
+    phase.stage = at % STAGES;
+    phase.parity = at / STAGES % 2;
+    for (int i = 0; i < at / (2 * STAGES); ++i)
         mbar_wait_bounded(full + phase.stage_of(i), phase.parity_of(i), kRowPolls);
 }
 
@@ -251,7 +258,7 @@ struct RowRing {
     static constexpr size_t kStage = kGroups * ARRAYS * kRow;
     static constexpr size_t kBytes = STAGES * kStage;
     unsigned char* base;
-    uint64_t* full;  // a barrier per stage
+    uint64_t* full;  // a barrier per stage, and a word
     const RingReport& report;  // of the kernel's arguments
     int64_t end;               // of the block's rows
     // bytes of a row that a bulk copy takes: a last, partial pack is loaded by its owner
@@ -291,16 +298,30 @@ struct RowRing {
     __device__ __forceinline__ int stage() const { return phase.stage; }
     __device__ __forceinline__ int before() const { return phase.before(); }
     __device__ __forceinline__ void advance() { phase.advance(); }
-    // Until the current stage holds the round from row `first` on. A wait that
-    // runs out sets the status words; the warp then neither waits nor copies any
-    // more and the block's outputs are undefined. Warp 0, which issued them,
-    // first waits (bounded too) until its copies in flight have landed: the
-    // block never ends with one, nor reuses its memory under one.
+    // Until the current stage holds the round from row `first` on. After a wait
+    // that ran out the warp neither waits nor copies any more, and the block's
+    // outputs are undefined.
     __device__ __forceinline__ void wait(int64_t first) {
         if (!ok) return;
-        ok = __all_sync(kFull, mbar_wait_bounded(full + phase.stage, phase.parity, report.polls));
-        if (ok) return;
-        ring_failed<STAGES>(full, phase, report, (end - first + kGroups - 1) / kGroups);
+        ok = __all_sync(kFull, mbar_wait_bounded(full + phase.stage, phase.parity, kRowPolls));
+        if (!ok) record(first);
+    }
+    // The wait for the first round as one that ran out.
+    __device__ __forceinline__ void lose(int64_t first) {
+        ok = false;
+        record(first);
+    }
+    // Before the block ends or uses the ring's memory for something else.
+    __device__ __forceinline__ void drain() {
+        if (!ok) ring_drain<STAGES>(full, full + STAGES, report);
+    }
+
+private:
+    // behind the barriers: what warp 0 has in flight
+    __device__ __forceinline__ void record(int64_t first) {
+        if (threadIdx.x == 0)
+            full[STAGES] = (phase.in_flight((end - first + kGroups - 1) / kGroups) * 2 + phase.parity) * STAGES +
+                           phase.stage;
     }
 };
 

@@ -127,13 +127,10 @@ private:
     std::atomic<int> kept_[kDevices] = {};
 };
 
-// Polls of the bounded waits for copies: `most`, or fewer by DL_WAIT_POLLS
-// (environment; tests use it to make waits run out)
-inline int wait_polls(int most) {
+// DL_WAIT_POLLS=0 (environment; tests use it): waits for copies run out at once
+inline bool waits_run_out() {
     const char* v = getenv("DL_WAIT_POLLS");
-    if (!v) return most;
-    const long n = strtol(v, nullptr, 10);
-    return n >= 0 && n < most ? static_cast<int>(n) : most;
+    return v && v[0] == '0' && v[1] == 0;
 }
 
 // p is a multiple of a (a power of two); null is
