@@ -96,7 +96,8 @@ __host__ __device__ inline int64_t head_of(const void* p, int64_t n) {
 // that finishes last joins the partial sums, lane by lane in a fixed order,
 // and leaves the ticket at zero: one launch and no memset per 64 buffers.
 // 1.1G bf16 gradients: 309 us, 7.1 TB/s (105% of the copy rate; it only
-// reads). Twelve small tensors (150001 fp32): 4.9 us on the device.
+// reads), zeros among them or not. Twelve small tensors (150001 fp32): 4.9 us
+// on the device.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ NormArgs a) {
     constexpr int W = 16 / sizeof(T);
@@ -266,8 +267,8 @@ constexpr int kTile32 = kThreads * 4 * kGroups32;
 // several tensors looks up each group's decay. Square root and quotient are
 // the approximate instructions (2 ulp; nothing is stored of them but theta,
 // whose update they scale).
-// 1.1B set (24 fragments, bf16 gradients and copy): 4317 us, 7.1 TB/s (105%
-// of the copy rate); 2000 ragged tensors (48M elements, fp32): 204 us, 6.6 TB/s.
+// 1.1B set (24 fragments, bf16 gradients and copy): 4333 us, 7.1 TB/s (105%
+// of the copy rate); 2000 ragged tensors (48M elements, fp32): 205 us, 6.6 TB/s.
 // Loads of single elements instead of fours: 5648 and 370 us.
 
 template <typename G>
@@ -712,24 +713,30 @@ __device__ __forceinline__ void any_block(const AdamArgs& a, const AdamJob& J, f
 
 // States in 8 bits. A warp takes runs of blocks, a lane four elements of each.
 // Traffic is 12 bytes per element plus the gradient and the copy, so the
-// arithmetic counts: 263 instructions per block of 128 elements against about
-// 350 issue slots that HBM leaves (issue active 64%). Hence the packed fp32 pairs, the hardware's
+// arithmetic counts: 265 instructions per block of 128 elements against about
+// 350 issue slots that HBM leaves (issue active 63%). Hence the packed fp32 pairs, the hardware's
 // stochastic conversion (one instruction for four codes), power-of-two scales
-// (no division, folded into the betas), one hash per four elements, and a
-// rounded root in six instructions. Copies run kStages - 1 blocks ahead in the
+// (no division), one hash per four elements, and a rounded root in six
+// instructions. Copies run kStages - 1 blocks ahead in the
 // warp's ring (loads into registers, two blocks at a time: 1441 us). Blocks
 // of a tensor that starts off a multiple of four elements go through the same
 // ring as shifted quads (element by element: 233 us for the ragged set).
 // Runs of 32 blocks, scheduled by the hardware; equal shares for a persistent
 // grid took 1211 us, runs of 16 about 1600. Three blocks of threads per SM (80
-// registers) with five stages against four (64) with four: the same 1115 us
+// registers) with five stages against four (64) with four: the same time
 // there, but the 1.1B set with fp32 gradients 3221 against 3293 and the ragged
 // set 170 against 177. The loop of unshifted blocks is unrolled twice; the
-// shifted ones' is not (194 us: the instruction cache holds three of them).
-// 415M-element fragment (bf16 gradients and copy): 1115 us, 6.0 TB/s (88% of
-// the copy rate); 2000 ragged tensors (48M elements, fp32 gradients): 170 us,
-// 4.6 TB/s (67%): 298 instructions per block with the shifts, against some 310
-// issue slots that HBM leaves there.
+// shifted ones' is not (ragged set 194 us when it is).
+// 415M-element fragment (bf16 gradients and copy): 1122 us, 6.0 TB/s (88% of
+// the copy rate); 200M elements that are mostly zero, whose roots take the
+// exact function: 537 against 476 us dense.
+// 2000 ragged tensors (48M elements, fp32 gradients): 171 us, 4.5 TB/s (66%).
+// Neither issue (63%) nor HBM (56%) is full there. The same set with its sizes
+// rounded to fours takes 152 us, to whole blocks 143, one tensor of that size
+// 136 (83%), and four times the elements run at 78%: what it pays is the
+// shifts and the first block of each run, which is loaded element by element
+// (15 us), blocks cut short and changes of tensor (17), and a call of 3.2 waves
+// whose warps fill and drain their rings once each (the rest).
 template <typename G>
 __global__ void __launch_bounds__(kThreads, 3) k_adamw8(const __grid_constant__ AdamArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];

@@ -537,7 +537,9 @@ class _LayerNorm(torch.autograd.Function):
 
 def layer_norm(x, weight, bias=None, eps=1e-5, rms=False):
     """layernorm_forward as a torch.autograd operation. First derivatives only:
-    differentiating its gradients again (create_graph=True) raises."""
+    differentiating its gradients again (create_graph=True) raises. It always
+    takes a weight; parameters are float32 or bfloat16; x's leading dimensions
+    must fold into rows that do not overlap (x.contiguous() where not)."""
     if bias is not None and bias.numel() != weight.numel():  # its gradient would not fit it
         raise ValueError(f"bias: {bias.numel()} elements, expected {weight.numel()}")
     return _LayerNorm.apply(x, weight, bias, eps, rms)
