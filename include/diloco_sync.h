@@ -572,6 +572,147 @@ int dl_layernorm_backward(const void* dy, int64_t dy_stride, const void* x, int6
                           void* dx, int64_t dx_stride, void* dweight, void* dbias,
                           void* d_workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The two ends of a learner's decoder, beside its norms: the rotary positions
+ * of queries and keys, and the log probabilities of the next tokens. The
+ * conventions of the inner step hold. Neither needs a workspace.
+ * ------------------------------------------------------------------------ */
+
+/* Integer types. */
+#define DL_I32 4
+#define DL_I64 5
+
+#define DL_ROTARY_MAX_DIM 8192 /* rotated elements of a head */
+#define DL_ROTARY_MAX_JOBS 4   /* tensors of one dl_rotary_apply call */
+
+/* How dl_rotary_frequencies scales the pairs for contexts longer than the trained one. */
+#define DL_ROTARY_PLAIN 0  /* not at all */
+#define DL_ROTARY_LINEAR 1 /* f / factor */
+#define DL_ROTARY_BASE 2   /* base * factor^(dim / (dim - 2)) in place of base; dim > 2 */
+#define DL_ROTARY_PARTS 3  /* by parts: a pair that makes r = context * f / 2 pi turns over
+                            * `context` tokens keeps g = min(1, max(0, (r - low) / (high - low)))
+                            * of f and takes (1 - g) of f / factor */
+
+/*
+ * Turns per token of the dim / 2 pairs of a head's rotated elements:
+ *   f_i = base^(-2 i / dim) radians per token, scaled as above
+ *   turns[i] = 2^64 * f_i / (2 pi), rounded to an integer
+ * so that position * turns[i] in 64 wrapping bits is the exact fraction of a
+ * turn, however far the position. Host only. A caller with frequencies of its
+ * own fills the table by the second formula (below 2 pi radians per token).
+ *   dim      even, 2 .. DL_ROTARY_MAX_DIM
+ *   base     >= 1, finite
+ *   factor   >= 1, finite; ignored with DL_ROTARY_PLAIN
+ *   context, low, high  DL_ROTARY_PARTS only: context > 0, 0 <= low < high
+ *   turns    host [dim / 2], out; copied to the device by the caller
+ */
+int dl_rotary_frequencies(int32_t dim, double base, int32_t scaling, double factor, double context,
+                          double low, double high, uint64_t* turns);
+
+/* One tensor of a dl_rotary_apply call: x and y are [batch][tokens][heads]
+ * [head_dim], the last dimension contiguous, the others at these strides (in
+ * elements, >= 0; heads before tokens is a matter of strides). */
+typedef struct dl_rotary_job {
+    const void* x;
+    void* y; /* may be x itself (same strides), else no part of any x or other y */
+    int64_t x_batch, x_token, x_head;
+    int64_t y_batch, y_token, y_head; /* no two elements of y at one place */
+    int32_t heads;
+} dl_rotary_job;
+
+#define DL_ROTARY_INTERLEAVED 1 /* pairs (2i, 2i + 1) in place of (i, i + rotary_dim / 2) */
+#define DL_ROTARY_INVERSE 2     /* by the negative angle: the gradient's rotation */
+
+/*
+ * Rotary positions of up to four tensors (queries and keys) in one launch.
+ * With p the token's position and phi = 2 pi * turns[i] * p, every pair
+ * (a, b) of a head's first rotary_dim elements becomes
+ *   a' = amplitude * (a cos phi - b sin phi)
+ *   b' = amplitude * (b cos phi + a sin phi)
+ * in fp32, rounded once; the elements behind are copied (left alone where y
+ * is x). phi is reduced exactly in 64-bit integers. The backward pass is the
+ * call on dy with DL_ROTARY_INVERSE and the same amplitude.
+ *   jobs, n_jobs    host, 1 .. DL_ROTARY_MAX_JOBS
+ *   type            DL_F32, DL_BF16 or DL_F16, of every x and y
+ *   rotary_dim      even, 2 .. min(head_dim, DL_ROTARY_MAX_DIM)
+ *   d_turns         device [rotary_dim / 2], 8-byte aligned
+ *   amplitude       finite in fp32
+ *   positions       device [batch][tokens] of position_type (DL_I32 or DL_I64),
+ *                   batch b starting at b * position_stride (0: one row for
+ *                   all); NULL: token s of every batch is at first + s
+ *   first           of the first token where positions is NULL, else ignored
+ * Pointers need the alignment of their elements only; 16-byte aligned heads
+ * are faster. batch, tokens or heads = 0 is a no-op.
+ */
+int dl_rotary_apply(const dl_rotary_job* jobs, int32_t n_jobs, int32_t type, int64_t batch,
+                    int64_t tokens, int32_t head_dim, int32_t rotary_dim, const uint64_t* d_turns,
+                    double amplitude, const void* positions, int32_t position_type,
+                    int64_t position_stride, int64_t first, int32_t flags, void* stream);
+
+#define DL_LOGPROBS_MAX_TOP 32 /* alternatives of a row */
+
+/*
+ * Log probabilities over rows of logits z, in one pass over them:
+ *   m = max z, S = sum e^(z - m)
+ *   logp    = (z[token] - m) - ln S
+ *   lse     = m + ln S
+ *   entropy = ln S - sum e^(z - m) (z - m) / S        (a term of z = -inf is 0)
+ *   top     the n_top most probable tokens, most probable first, the lower
+ *           token first where logits are equal, and their logp
+ * Sums in fp32, in a fixed order.
+ *   logits    device [rows][vocab] of type (DL_F32, DL_BF16 or DL_F16); row r
+ *             starts at r * stride elements, stride >= vocab
+ *   tokens    device [rows] of token_type (DL_I32 or DL_I64), or NULL for no logp
+ *   logp, entropy, lse   device [rows] fp32, out; logp is NULL exactly where
+ *             tokens is, the others may be
+ *   n_top     0 .. DL_LOGPROBS_MAX_TOP; top_tokens (int64) and top_logp (fp32)
+ *             device [rows][n_top], out, NULL for n_top = 0
+ *   row_max, log_sum     device [rows] fp32, out: m and ln S, for the backward
+ *             call; NULL both where none follows
+ * Rows:
+ *  - A negative token leaves its row out: the row is not read, every output
+ *    is 0 (top: tokens -1, logp -inf).
+ *  - A token >= vocab has logp NaN; the row's other outputs are as usual.
+ *  - A logit of -inf (a mask) has probability 0 and is no alternative; entries
+ *    of top past the other logits have token -1 and logp -inf.
+ *  - A row of nothing but -inf has lse = log_sum = logp = -inf, row_max = 0
+ *    and entropy 0.
+ *  - A row with NaN or +inf: NaN in every fp32 output, token -1 in top.
+ * Pointers need the alignment of their elements only. rows = 0 is a no-op;
+ * vocab >= 1.
+ */
+int dl_logprobs_forward(const void* logits, int64_t stride, int32_t type, int64_t rows,
+                        int32_t vocab, const void* tokens, int32_t token_type, float* logp,
+                        float* entropy, float* lse, int32_t n_top, int64_t* top_tokens,
+                        float* top_logp, float* row_max, float* log_sum, void* stream);
+
+/*
+ * The logits' gradient. With p = e^((z - m) - ln S) from the row's statistics,
+ * and the gradients g of logp, h of entropy, l of lse and q[i] of top_logp:
+ *   dlogits[j] = p_j (l - g - sum q - h (ln p_j + entropy))
+ *                + g [j = token] + sum of the q[i] with top_tokens[i] = j
+ * in fp32, rounded once to type. One pass: logits read once, dlogits written once.
+ *   tokens           as in the forward call
+ *   row_max, log_sum, entropy   as the forward call wrote them; entropy only
+ *                    with d_entropy
+ *   d_logp, d_entropy, d_lse    device [rows] fp32; NULL for none (d_logp needs
+ *                    tokens)
+ *   n_top, top_tokens, d_top    device [rows][n_top]; n_top = 0 and NULL for
+ *                    none. An entry with a negative token or one >= vocab has no
+ *                    gradient; tokens may repeat.
+ *   dlogits          device [rows][vocab] of type, its own stride; may be
+ *                    logits itself (same stride), else no part of it
+ * A row that is left out (a negative token), has nothing but -inf (log_sum =
+ * -inf), or whose gradients are all zero, is not read: its dlogits are zeros.
+ * A token >= vocab makes a row with g other than 0 NaN.
+ */
+int dl_logprobs_backward(const void* logits, int64_t stride, int32_t type, int64_t rows,
+                         int32_t vocab, const void* tokens, int32_t token_type,
+                         const float* row_max, const float* log_sum, const float* entropy,
+                         const float* d_logp, const float* d_entropy, const float* d_lse,
+                         int32_t n_top, const int64_t* top_tokens, const float* d_top,
+                         void* dlogits, int64_t dlogits_stride, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,10 +22,18 @@ A learner's inner step (``inner``, imported here):
     layernorm_forward    layer norm of rows
     layernorm_backward   its gradients
 
+The two ends of its decoder (``decoder``, imported here):
+
+    rotary_frequencies   turns per token of a head's pairs (host)
+    rotary_apply         queries and keys turned by their positions
+    logprobs_forward     log probabilities of tokens, entropy, alternatives
+    logprobs_backward    the logits' gradient
+
 ``OuterSync`` bundles the three device calls of one fragment with their
 workspaces; ``ModelSync`` holds the workspace of ``outer_sync`` for a fixed
 list of fragments. ``InnerAdamW`` bundles a learner's clip and AdamW step with their
-states; ``layer_norm`` is the norm as a torch.autograd operation.
+states; ``layer_norm`` is the norm as a torch.autograd operation, as ``rotary`` and
+``token_logprobs`` are the decoder's ends.
 """
 from __future__ import annotations
 
@@ -116,6 +124,7 @@ def lib():
         L.dl_read_device_status.restype = ctypes.c_int
         L.dl_read_device_status.argtypes = [vp, vp, vp]
         inner.declare(L)
+        decoder.declare(L)
         _lib = L
     return _lib
 
@@ -577,3 +586,8 @@ from .inner import (  # noqa: E402,F401
     DL_ADAMW_BLOCK, DL_BF16, DL_E4M3, DL_F16, DL_F32, DL_NORM_ACCUMULATE, DL_NORM_RMS, AdamWJobs,
     GradList, InnerAdamW, adamw_scale_slots, adamw_step, grad_norm, grad_norm_workspace_bytes,
     layer_norm, layernorm_backward, layernorm_forward, layernorm_workspace_bytes)
+from . import decoder  # noqa: E402
+from .decoder import (  # noqa: E402,F401
+    DL_I32, DL_I64, DL_LOGPROBS_MAX_TOP, DL_ROTARY_INTERLEAVED, DL_ROTARY_INVERSE,
+    DL_ROTARY_MAX_DIM, DL_ROTARY_MAX_JOBS, LogProbs, RotaryFrequencies, TokenLogProbs,
+    logprobs_backward, logprobs_forward, rotary, rotary_apply, rotary_frequencies, token_logprobs)

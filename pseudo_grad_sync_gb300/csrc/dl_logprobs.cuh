@@ -1,0 +1,82 @@
+// Token log probabilities: what the forward and the backward kernels share.
+//
+// A row of logits is cut at 16-byte boundaries into packs of N elements; pack 0
+// and the last one may lie partly outside the row. Column of element i of
+// pack p: p * N + i - skew, skew being the elements between the boundary and
+// the row's start.
+#pragma once
+
+#include <math.h>
+
+#include "dl_types.cuh"
+
+namespace dl {
+
+constexpr float kLog2E = 1.44269504f, kLn2 = 0.693147181f;
+constexpr float kLeast = -200.f;  // an exponent of 2 that is 0 in fp32, and no infinity
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// the larger, NaN if one is
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float2 as_floats(uint32_t w, __nv_bfloat16) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float2 as_floats(uint32_t w, __half) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+// elements 2i and 2i + 1 of a pack
+template <typename T, int N>
+__device__ __forceinline__ float2 pair_at(const Pack<T, N>& p, int i) {
+    if constexpr (sizeof(T) == 2) {
+        return as_floats(reinterpret_cast<const uint32_t*>(p.v)[i], T());
+    } else {
+        return make_float2(p.v[2 * i], p.v[2 * i + 1]);
+    }
+}
+
+// A row's packs. `base` is the boundary at or before its start.
+template <typename T>
+struct RowPacks {
+    static constexpr int N = 16 / sizeof(T);
+    const T* base;
+    int skew, packs;
+    int64_t end;  // skew + width: elements from base to the row's end
+
+    __device__ __forceinline__ RowPacks(const T* row, int64_t width) {
+        skew = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+        base = row - skew;
+        end = skew + width;
+        packs = static_cast<int>((end + N - 1) / N);
+    }
+    __device__ __forceinline__ bool whole(int p) const {
+        return (p > 0 || skew == 0) && (int64_t(p) + 1) * N <= end;
+    }
+    __device__ __forceinline__ bool inside(int64_t place) const { return place >= skew && place < end; }
+    // pack p, `fill` where it lies outside the row
+    __device__ __forceinline__ Pack<T, N> load(int p, T fill) const {
+        if (whole(p)) return reinterpret_cast<const Pack<T, N>*>(base)[p];
+        Pack<T, N> r;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int64_t at = int64_t(p) * N + i;
+            r.v[i] = inside(at) ? base[at] : fill;
+        }
+        return r;
+    }
+};
+
+__device__ __forceinline__ int64_t token_at(const void* tokens, int32_t type, int64_t row) {
+    return type == DL_I64 ? static_cast<const int64_t*>(tokens)[row] : static_cast<const int32_t*>(tokens)[row];
+}
+
+}  // namespace dl
