@@ -2,6 +2,8 @@
 #include <float.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "dl_logprobs.cuh"
 
 namespace dl {
@@ -25,8 +27,9 @@ struct ForwardArgs {
 // units of log 2, a = sum e^(z - m) (z - m). Nothing yet: m lowest and s zero,
 // so that -inf - m is -inf and adds nothing.
 struct Part {
-    float m = -FLT_MAX, s = 0.f, a = 0.f;
+    float m, s, a;
 
+    static __device__ __forceinline__ Part nothing() { return {-FLT_MAX, 0.f, 0.f}; }
     // to a larger maximum
     __device__ __forceinline__ void raise(float top) {
         const float t = max_nan((m - top) * kLog2E, kLeast), f = exp2_fast(t);
@@ -34,48 +37,71 @@ struct Part {
         s *= f;
         m = top;
     }
-    __device__ __forceinline__ void add(Part o) {
-        const float top = max_nan(m, o.m);
-        raise(top);
-        o.raise(top);
-        s += o.s;
-        a += o.a;
-    }
 };
 
-template <typename T, int N>
-__device__ __forceinline__ float largest(const Pack<T, N>& p) {
+template <typename T, int N, int U>
+__device__ __forceinline__ float largest(const Pack<T, N> (&p)[U]) {
     if constexpr (sizeof(T) == 2) {
         using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
-        const T2* q = reinterpret_cast<const T2*>(p.v);
-        T2 r = q[0];
+        T2 r = reinterpret_cast<const T2*>(p[0].v)[0];
 #pragma unroll
-        for (int i = 1; i < N / 2; ++i) r = __hmax2_nan(r, q[i]);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = u == 0; i < N / 2; ++i) r = __hmax2_nan(r, reinterpret_cast<const T2*>(p[u].v)[i]);
         const float2 f = as_floats(*reinterpret_cast<const uint32_t*>(&r), T());
         return max_nan(f.x, f.y);
     } else {
-        return max_nan(max_nan(p.v[0], p.v[1]), max_nan(p.v[2], p.v[3]));
+        float r = p[0].v[0];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = u == 0; i < N; ++i) r = max_nan(r, p[u].v[i]);
+        return r;
     }
 }
 
-// Adds U packs: the maximum first, then every term relative to it.
+// Adds U packs: the maximum first, then every term relative to it. A term
+// that is 0 because its logit is -inf makes the entropy's sum NaN; that sum is
+// then taken again with exponents kept finite, which costs the packs with
+// masked logits a second pass and the others nothing.
 template <bool ENTROPY, typename T, int N, int U>
-__device__ __forceinline__ void add_packs(Part& part, const Pack<T, N> (&p)[U], float top) {
-    part.raise(max_nan(part.m, top));
+__device__ __forceinline__ void add_packs(Part& part, const Pack<T, N> (&p)[U]) {
+    part.raise(max_nan(part.m, largest(p)));
     float2 s = make_float2(0.f, 0.f), a = s;
     const float2 minus = both(-part.m), unit = both(kLog2E);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
-            float2 t = mul2(add2(pair_at(p[u], i), minus), unit);
-            if (ENTROPY) t = make_float2(max_nan(t.x, kLeast), max_nan(t.y, kLeast));
+            const float2 t = mul2(add2(pair_at(p[u], i), minus), unit);
             const float2 e = make_float2(exp2_fast(t.x), exp2_fast(t.y));
             s = add2(s, e);
             if (ENTROPY) a = fma2(e, t, a);
         }
+    float sum = a.x + a.y;
+    if (ENTROPY && !(sum == sum)) {
+        sum = 0.f;
+        for (int u = 0; u < U; ++u)
+            for (int i = 0; i < N; ++i) {
+                const float t = max_nan((to_f32(p[u].v[i]) - part.m) * kLog2E, kLeast);
+                sum = fmaf(exp2_fast(t), t, sum);
+            }
+    }
     part.s += s.x + s.y;
-    part.a += a.x + a.y;
+    part.a += sum;
+}
+
+// the parts of a warp's lanes, joined in every lane
+__device__ __forceinline__ void join(Part& part) {
+    float top = part.m;
+#pragma unroll
+    for (int j = 16; j > 0; j /= 2) top = max_nan(top, __shfl_xor_sync(kAll, top, j));
+    part.raise(top);
+#pragma unroll
+    for (int j = 16; j > 0; j /= 2) {
+        part.s += __shfl_xor_sync(kAll, part.s, j);
+        part.a += __shfl_xor_sync(kAll, part.a, j);
+    }
 }
 
 // Logits as keys: a larger key is a larger logit, of equal ones the lower
@@ -92,198 +118,429 @@ __device__ __forceinline__ float logit_of(uint64_t key) {
 }
 __device__ __forceinline__ uint32_t column_of(uint64_t key) { return 0xffffffffu - static_cast<uint32_t>(key); }
 
-// A warp's 32 largest keys, one per lane, the largest in lane 0.
-struct WarpTop {
-    uint64_t key = 0;
+// Lists of 32 values, one per lane, the largest in lane 0.
+template <typename K>
+__device__ __forceinline__ K exchange(K key, int lane, int j, bool descending) {
+    const K o = __shfl_xor_sync(kAll, key, j);
+    return (((lane & j) == 0) == descending) == (key > o) ? key : o;
+}
+// L lists of values in any order, each sorted (bitonic)
+template <int L, typename K>
+__device__ __forceinline__ void sort_lists(K (&key)[L], int lane) {
+#pragma unroll
+    for (int k = 2; k <= 32; k *= 2)
+#pragma unroll
+        for (int j = k / 2; j > 0; j /= 2)
+#pragma unroll
+            for (int l = 0; l < L; ++l) key[l] = exchange(key[l], lane, j, (lane & k) == 0 || k == 32);
+}
+// the 32 largest of two lists, the second in reverse order
+template <typename K>
+__device__ __forceinline__ K merge_lists(K key, K reversed, int lane) {
+    key = key > reversed ? key : reversed;
+#pragma unroll
+    for (int j = 16; j > 0; j /= 2) key = exchange(key, lane, j, true);
+    return key;
+}
 
-    __device__ __forceinline__ void exchange(int lane, int j, bool descending) {
-        const uint64_t o = __shfl_xor_sync(kAll, key, j);
-        const bool first = (lane & j) == 0;
-        key = (first == descending) == (key > o) ? key : o;
-    }
-    // any keys in any order (bitonic)
-    __device__ __forceinline__ void sort(int lane) {
-        for (int k = 2; k <= 32; k *= 2)
-            for (int j = k / 2; j > 0; j /= 2) exchange(lane, j, (lane & k) == 0 || k == 32);
-    }
-    // the 32 largest of these and another list's, given in reverse order
-    __device__ __forceinline__ void merge(int lane, uint64_t reversed) {
-        key = key > reversed ? key : reversed;
-        for (int j = 16; j > 0; j /= 2) exchange(lane, j, true);
-    }
-    // one more key, the same in every lane
-    __device__ __forceinline__ void insert(int lane, uint64_t k) {
-        const int place = __popc(__ballot_sync(kAll, key > k));
-        const uint64_t before = __shfl_up_sync(kAll, key, 1);
-        key = lane < place ? key : lane == place ? k : before;
+// A row, or a block's share of one: packs [begin, end), in stages of U packs per thread.
+template <typename T, int TPR, int U>
+struct Share {
+    RowPacks<T> packs;
+    int begin, end, stages;
+
+    __device__ __forceinline__ Share(const T* row, int vocab, int rank, int ranks) : packs(row, vocab) {
+        const int each = (packs.packs + ranks - 1) / ranks;
+        begin = min(rank * each, packs.packs);
+        end = min(begin + each, packs.packs);
+        stages = max((end - begin + TPR * U - 1) / (TPR * U), 1);
     }
 };
 
+constexpr int kCandidates = 64;
+
+// What a block's warps hand over at a row's end, in turns: the last warp
+// works on one row's while the others fill in the next one's.
 template <int WARPS>
-struct Scratch {
+struct Handover {
     Part part[WARPS];
-    uint64_t list[WARPS][32];
-    uint64_t threshold;
-    int chosen, threads[WARPS * 32];
+    float most[WARPS][32];
+};
+// The finishing warp's own: the packs it reads again, the threads that had
+// them, candidates, and a cluster's exchange.
+template <int WARPS>
+struct Finish {
+    static constexpr int kRead = WARPS == 1 ? 4 : 16;
+    uint4 again[kRead][32];
+    uint64_t candidate[kCandidates + 32 * 8];
+    uint64_t key[32];
+    Part part;
+    int thread[WARPS * 32];
+    int waiting;
 };
 
-// One block per row at a time. Every thread keeps the running maximum and sums
-// of its packs; warps and then the block join them.
+template <typename T, int TPR>
+struct Geometry {
+    static constexpr int kWarps = TPR / 32;  // of a row
+    static constexpr bool kAlone = kWarps == 1;
+    static constexpr int kMain = kAlone ? 128 : TPR, kBlock = kAlone ? kMain : kMain + 32, kGroups = kMain / TPR;
+    static constexpr int U = kAlone ? 2 : 4, kStages = kAlone ? 6 : 3;
+    static constexpr size_t kRing = size_t(kStages) * U * kMain * 16;
+    static constexpr size_t kHand = kAlone ? 0 : 2 * sizeof(Handover<kWarps>);
+    static constexpr size_t kFinish = sizeof(Finish<kWarps>);
+    static constexpr size_t bytes(bool top) { return kRing + kHand + (top ? kFinish * kGroups : sizeof(Part)); }
+};
+
+// The n_top largest logits of a row (or a share) from the largest one of every
+// thread, by one warp; lane i gets the i-th key, 0 past the finite logits.
 //
-// Alternatives: each thread also remembers its best pack and that pack's
-// largest logit. The n_top-th largest of the threads' best is a bound that no
-// alternative lies below, and only n_top threads have an element that reaches
-// it: their packs alone are read again, a warp per thread, and what reaches
-// the bound goes into the warps' sorted lists, which are merged.
-template <typename T, int BLOCK, bool ENTROPY, bool TOP>
-__global__ void __launch_bounds__(BLOCK) k_logprobs(const __grid_constant__ ForwardArgs<T> a) {
-    constexpr int N = 16 / sizeof(T), U = 4, kWarps = BLOCK / 32;
-    __shared__ Scratch<TOP ? kWarps : 1> top;
-    __shared__ Part parts[kWarps];
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+// The n_top-th largest of the threads' maxima is a bound that no alternative
+// lies below, and (ties aside) only n_top threads have a logit that reaches
+// it. Their packs alone are read again, many at a time; what reaches the
+// bound is collected, and sorted in runs of 32.
+template <typename T, int TPR, int WARPS, typename S>
+__device__ __forceinline__ uint64_t alternatives(const S& mine, const float (&most)[WARPS], int n_top, int lane,
+                                                 Finish<WARPS>& own) {
+    constexpr int N = 16 / sizeof(T), kRead = Finish<WARPS>::kRead;
+    using P = Pack<T, N>;
+    float best[WARPS];
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) best[w] = most[w];
+    sort_lists(best, lane);
+#pragma unroll
+    for (int half = WARPS / 2; half > 0; half /= 2)
+#pragma unroll
+        for (int w = 0; w < half; ++w)
+            best[w] = merge_lists(best[w], __shfl_sync(kAll, best[w + half], 31 - lane), lane);
+    const float bound = __shfl_sync(kAll, best[0], n_top - 1);
+    int threads = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        const unsigned reach = __ballot_sync(kAll, most[w] >= bound);
+        if (most[w] >= bound) own.thread[threads + __popc(reach & ((1u << lane) - 1))] = w * 32 + lane;
+        threads += __popc(reach);
+    }
+    if (lane == 0) own.waiting = 0;
+    __syncwarp();
+    uint64_t found = 0, least = 0;  // the list so far, its n_top-th key
+    auto take = [&](int count) {
+        for (int c = 0; c < count; c += 32) {
+            uint64_t next[1] = {c + lane < count ? own.candidate[c + lane] : 0};
+            sort_lists(next, lane);
+            found = merge_lists(found, __shfl_sync(kAll, next[0], 31 - lane), lane);
+        }
+        least = __shfl_sync(kAll, found, n_top - 1);
+        __syncwarp();
+        if (lane == 0) own.waiting = 0;
+        __syncwarp();
+    };
+    // item i: pack i % packs of the (i / packs)-th thread; a lane takes every 32nd
+    const int packs = max((mine.end - mine.begin + TPR - 1) / TPR, 1), items = threads * packs;
+    const int more_threads = 32 / packs, more_packs = 32 % packs;
+    int who = lane / packs, at = lane % packs;
+    auto advance = [&](int& w, int& p) {
+        w += more_threads, p += more_packs;
+        if (p >= packs) p -= packs, ++w;
+    };
     const T none = from_f32<T>(-INFINITY);
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const int64_t token = a.tokens ? token_at(a.tokens, a.token_type, row) : 0;
-        if (token < 0) {
-            if (threadIdx.x == 0) {
-                a.logp[row] = 0.f;
-                if (a.lse) a.lse[row] = 0.f;
-                if (a.entropy) a.entropy[row] = 0.f;
-                if (a.row_max) a.row_max[row] = 0.f, a.log_sum[row] = 0.f;
+    for (int first = lane; first - lane < items; first += 32 * kRead) {
+        int w = who, p = at;
+#pragma unroll
+        for (int r = 0; r < kRead; ++r) {
+            if (first + 32 * r < items) {
+                const int pack = mine.begin + p * TPR + own.thread[w];
+                if (pack < mine.end && mine.packs.whole(pack))
+                    copy_async<16>(&own.again[r][lane], mine.packs.base + int64_t(pack) * N);
             }
-            if (TOP && threadIdx.x < a.n_top) {
-                a.top_tokens[row * a.n_top + threadIdx.x] = -1;
-                a.top_logp[row * a.n_top + threadIdx.x] = -INFINITY;
-            }
-            continue;
+            advance(w, p);
         }
-        const RowPacks<T> packs(a.logits + row * a.stride, a.vocab);
-        Part part;
-        float best = -INFINITY;
-        int best_pack = -1;
-        for (int64_t p = threadIdx.x; p < packs.packs; p += BLOCK * U) {
-            Pack<T, N> q[U];
-            float most = -INFINITY;
+        copy_commit();
+        copy_wait<0>();
+        for (int r = 0; r < kRead && first - lane + 32 * r < items; ++r) {
+            bool any = false;
+            if (first + 32 * r < items) {
+                const int pack = mine.begin + at * TPR + own.thread[who];
+                if (pack < mine.end) {
+                    const P q[1] = {mine.packs.whole(pack) ? *reinterpret_cast<const P*>(&own.again[r][lane])
+                                                           : mine.packs.load(pack, none)};
+                    any = largest(q) >= bound;
+                    if (any) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (p + u * BLOCK < packs.packs) {
-                    q[u] = packs.load(static_cast<int>(p + u * BLOCK), none);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < N; ++i) q[u].v[i] = none;
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const float m = largest(q[u]);
-                if (TOP && m > best) best = m, best_pack = static_cast<int>(p + u * BLOCK);
-                most = max_nan(most, m);
-            }
-            add_packs<ENTROPY>(part, q, most);
-        }
-#pragma unroll
-        for (int j = 16; j > 0; j /= 2) {
-            Part o;
-            o.m = __shfl_xor_sync(kAll, part.m, j);
-            o.s = __shfl_xor_sync(kAll, part.s, j);
-            o.a = __shfl_xor_sync(kAll, part.a, j);
-            part.add(o);
-        }
-        if (lane == 0) parts[warp] = part;
-        uint64_t low = 0, high = 0;  // between these keys lies the thread's best
-        if constexpr (TOP) {
-            if (best_pack >= 0) {
-                const int64_t first = int64_t(best_pack) * N - packs.skew;
-                high = key_of(best, static_cast<uint32_t>(first < 0 ? 0 : first));
-                low = key_of(best, static_cast<uint32_t>(min(first + N - 1, int64_t(a.vocab) - 1)));
-            }
-            WarpTop list{low};
-            list.sort(lane);
-            top.list[warp][lane] = list.key;
-            if (threadIdx.x == 0) top.chosen = 0;
-        }
-        __syncthreads();
-        part = parts[0];
-        for (int w = 1; w < kWarps; ++w) part.add(parts[w]);
-        WarpTop found;
-        if constexpr (TOP) {
-            if (warp == 0) {
-                WarpTop list{top.list[0][lane]};
-                for (int w = 1; w < kWarps; ++w) list.merge(lane, top.list[w][31 - lane]);
-                const uint64_t bound = __shfl_sync(kAll, list.key, a.n_top - 1);
-                if (lane == 0) top.threshold = bound;
-            }
-            __syncthreads();
-            const uint64_t bound = top.threshold;
-            if (high != 0 && high >= bound) top.threads[atomicAdd(&top.chosen, 1)] = threadIdx.x;
-            __syncthreads();
-            for (int c = warp; c < top.chosen; c += kWarps) {
-                for (int64_t p = top.threads[c]; p < packs.packs; p += 32 * BLOCK) {
-                    const int64_t mine = p + lane * BLOCK;
-                    Pack<T, N> q;
-#pragma unroll
-                    for (int i = 0; i < N; ++i) q.v[i] = none;
-                    if (mine < packs.packs) q = packs.load(static_cast<int>(mine), none);
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        const uint64_t k = key_of(to_f32(q.v[i]), static_cast<uint32_t>(mine * N + i - packs.skew));
-                        unsigned who = __ballot_sync(kAll, k != 0 && k >= bound);
-                        while (who) {
-                            found.insert(lane, __shfl_sync(kAll, k, __ffs(who) - 1));
-                            who &= who - 1;
+                        for (int i = 0; i < N; ++i) {
+                            const float v = to_f32(q[0].v[i]);
+                            const uint64_t k =
+                                key_of(v, static_cast<uint32_t>(int64_t(pack) * N + i - mine.packs.skew));
+                            if (v >= bound && k > least) own.candidate[atomicAdd(&own.waiting, 1)] = k;
                         }
                     }
                 }
             }
-            top.list[warp][lane] = found.key;  // the threshold's lists were read before the last barrier but one
-            __syncthreads();
-            if (warp == 0)
-                for (int w = 1; w < kWarps; ++w) found.merge(lane, top.list[w][31 - lane]);
-        }
-        if (warp == 0) {
-            // nothing but -inf: no sum; NaN or +inf: a sum of NaN
-            const bool empty = part.s == 0.f, bad = !(part.s >= 0.f);
-            const float m = bad ? NAN : empty ? 0.f : part.m, log_sum = logf(part.s);
-            if (lane == 0) {
-                if (a.tokens) {
-                    float z = NAN;
-                    if (token < a.vocab) z = to_f32(a.logits[row * a.stride + token]);
-                    a.logp[row] = empty && token < a.vocab ? -INFINITY : (z - m) - log_sum;
-                }
-                if (a.lse) a.lse[row] = m + log_sum;
-                if (a.entropy) a.entropy[row] = empty ? 0.f : log_sum - part.a / part.s * kLn2;
-                if (a.row_max) a.row_max[row] = m, a.log_sum[row] = log_sum;
+            if (__any_sync(kAll, any)) {
+                __syncwarp();
+                const int waiting = own.waiting;
+                __syncwarp();
+                if (waiting >= kCandidates) take(waiting);
             }
-            if (TOP && lane < a.n_top) {
-                const bool have = found.key != 0 && !bad;
-                a.top_tokens[row * a.n_top + lane] = have ? static_cast<int64_t>(column_of(found.key)) : -1;
-                a.top_logp[row * a.n_top + lane] =
-                    bad ? NAN : have ? (logit_of(found.key) - m) - log_sum : -INFINITY;
-            }
+            advance(who, at);
         }
-        __syncthreads();  // the next row writes the shared lists
     }
+    __syncwarp();
+    take(own.waiting);
+    return found;
 }
 
-template <typename T, int BLOCK, bool ENTROPY, bool TOP>
-int launch(const ForwardArgs<T>& a, cudaStream_t s) {
+// TPR threads per row: a warp (four rows to a block), or eight, or with CLUSTER
+// eight in each block of a cluster. Every thread keeps the running maximum and
+// sums of its packs and a warp joins its lanes'.
+//
+// Packs come in by asynchronous copies into a ring that each thread has to
+// itself, kStages - 1 stages ahead and on into the next rows. Where eight warps
+// share a row a ninth one joins their parts, finds the alternatives and
+// writes the outputs while they are at the next row; one barrier per row
+// hands over.
+template <typename T, int TPR, bool ENTROPY, bool TOP, bool CLUSTER>
+__global__ void __launch_bounds__(Geometry<T, TPR>::kBlock, TPR == 32 ? 6 : 3)
+    k_logprobs(const __grid_constant__ ForwardArgs<T> a) {
+    using Geo = Geometry<T, TPR>;
+    constexpr int N = 16 / sizeof(T), U = Geo::U, kWarps = Geo::kWarps, kAhead = Geo::kStages - 1;
+    constexpr bool kAlone = Geo::kAlone;
+    using P = Pack<T, N>;
+    using Mine = Share<T, TPR, U>;
+    extern __shared__ __align__(16) unsigned char smem[];
+    Handover<kWarps>* const hand = reinterpret_cast<Handover<kWarps>*>(smem + Geo::kRing);
+    const int group = kAlone ? threadIdx.x / 32 : 0, lane = threadIdx.x % 32;
+    Finish<kWarps>& own = reinterpret_cast<Finish<kWarps>*>(smem + Geo::kRing + Geo::kHand)[group];
+    const int rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
+    const int ranks = CLUSTER ? static_cast<int>(cluster_size()) : 1;
+    const int64_t step = int64_t(gridDim.x) / ranks * Geo::kGroups;
+    auto token_of = [&](int64_t row) { return a.tokens && row < a.rows ? token_at(a.tokens, a.token_type, row) : 0; };
+    auto share = [&](int64_t row) { return Mine(a.logits + row * a.stride, a.vocab, rank, ranks); };
+    int64_t row = (CLUSTER ? blockIdx.x / ranks : blockIdx.x) * int64_t(Geo::kGroups) + group;
+    int64_t token = token_of(row);
+
+    auto finish = [&](const Mine& mine, float z, Part part, const float (&most)[kWarps]) {
+        uint64_t found = 0;
+        if constexpr (TOP) found = alternatives<T, TPR, kWarps>(mine, most, a.n_top, lane, own);
+        if constexpr (CLUSTER) {
+            // without alternatives the exchange holds a part alone
+            Part* const shared = TOP ? &own.part : reinterpret_cast<Part*>(&own);
+            if (lane == 0) *shared = part;
+            if (TOP) own.key[lane] = found;
+            cluster_barrier();
+            if (rank == 0) {
+                part = Part::nothing();
+                if (lane < ranks) {
+                    part.m = load_cluster(&shared->m, lane);
+                    part.s = load_cluster(&shared->s, lane);
+                    part.a = load_cluster(&shared->a, lane);
+                }
+                join(part);
+                if (TOP)
+                    for (int r = 1; r < ranks; ++r)
+                        found = merge_lists(found, load_cluster(&own.key[31 - lane], r), lane);
+            }
+            cluster_barrier();
+            if (rank != 0) return;
+        }
+        // nothing but -inf: no sum; NaN or +inf: a sum of NaN
+        const bool empty = part.s == 0.f, bad = !(part.s >= 0.f);
+        const float m = bad ? NAN : empty ? 0.f : part.m, log_sum = logf(part.s);
+        if (lane == 0) {
+            if (a.tokens) a.logp[row] = empty && token < a.vocab ? -INFINITY : (z - m) - log_sum;
+            if (a.lse) a.lse[row] = m + log_sum;
+            if (a.entropy) a.entropy[row] = empty ? 0.f : log_sum - part.a / part.s * kLn2;
+            if (a.row_max) a.row_max[row] = m, a.log_sum[row] = log_sum;
+        }
+        if (TOP && lane < a.n_top) {
+            const bool have = found != 0 && !bad;
+            a.top_tokens[row * a.n_top + lane] = have ? static_cast<int64_t>(column_of(found)) : -1;
+            a.top_logp[row * a.n_top + lane] = bad ? NAN : have ? (logit_of(found) - m) - log_sum : -INFINITY;
+        }
+    };
+    auto leave_out = [&]() {
+        if (rank != 0) return;
+        if (lane == 0) {
+            a.logp[row] = 0.f;
+            if (a.lse) a.lse[row] = 0.f;
+            if (a.entropy) a.entropy[row] = 0.f;
+            if (a.row_max) a.row_max[row] = 0.f, a.log_sum[row] = 0.f;
+        }
+        if (TOP && lane < a.n_top) {
+            a.top_tokens[row * a.n_top + lane] = -1;
+            a.top_logp[row * a.n_top + lane] = -INFINITY;
+        }
+    };
+
+    if (!kAlone && threadIdx.x >= Geo::kMain) {  // the warp that finishes the others' rows
+        for (int set = 0; row < a.rows; row += step) {
+            const int64_t after = token_of(row + step);
+            if (token < 0) {
+                leave_out();
+            } else {
+                float z = NAN;
+                if (lane == 0 && a.tokens && token < a.vocab) z = to_f32(a.logits[row * a.stride + token]);
+                __syncthreads();
+                Part part = lane < kWarps ? hand[set].part[lane] : Part::nothing();
+                join(part);
+                float most[kWarps];
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) most[w] = TOP ? hand[set].most[w][lane] : 0.f;
+                finish(share(row), z, part, most);
+                set ^= 1;
+            }
+            token = after;
+        }
+        return;
+    }
+
+    const int t = threadIdx.x % TPR;
+    P* const ring = reinterpret_cast<P*>(smem) + threadIdx.x;
+    auto slot = [&](int stage, int u) { return ring + (stage * U + u) * Geo::kMain; };
+    const T none = from_f32<T>(-INFINITY);
+    // the first and last place of the logits: a pack that holds a row's edge is
+    // copied whole where it lies between them, and masked
+    const T* const from = a.logits;
+    const T* const to = a.logits + (a.rows - 1) * a.stride + a.vocab;
+    // what is copied next: stage `next_k` of row `next`
+    int64_t next = row, next_token = token, next_after = token_of(row + step);
+    auto skip = [&]() {  // to the first row that is not left out
+        while (next < a.rows && next_token < 0) next += step, next_token = next_after, next_after = token_of(next + step);
+    };
+    skip();
+    Mine then = share(next < a.rows ? next : 0);
+    int next_k = 0;
+    auto issue = [&](int stage) {
+        if (next < a.rows) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int p = then.begin + (next_k * U + u) * TPR + t;
+                const T* src = then.packs.base + int64_t(p) * N;
+                if (p < then.end && src >= from && src + N <= to) copy_async<16>(slot(stage, u), src);
+            }
+            if (++next_k >= then.stages) {
+                next += step, next_token = next_after, next_after = token_of(next + step);
+                skip();
+                if (next < a.rows) then = share(next);
+                next_k = 0;
+            }
+        }
+        copy_commit();
+    };
+    for (int k = 0; k < kAhead; ++k) issue(k);
+    int stage = 0, set = 0;
+    for (; row < a.rows; row += step) {
+        const int64_t after = token_of(row + step);
+        if (token < 0) {
+            if (kAlone) leave_out();
+            token = after;
+            continue;
+        }
+        const Mine mine = share(row);
+        // the token's logit; a row's only warp finds it in the ring
+        float z = NAN;
+        const int64_t place = token + mine.packs.skew;
+        const int place_pack = kAlone && a.tokens && token < a.vocab ? static_cast<int>(place / N) : -1;
+        Part part = Part::nothing();
+        for (int k = 0; k < mine.stages; ++k) {
+            copy_wait<kAhead - 1>();
+            const int first = mine.begin + k * U * TPR;
+            P q[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) q[u] = *slot(stage, u);
+            // the row's edges and the share's end
+            if ((k == 0 && rank == 0) || k == mine.stages - 1) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int p = first + u * TPR + t;
+                    if (p >= mine.end) {
+#pragma unroll
+                        for (int i = 0; i < N; ++i) q[u].v[i] = none;
+                    } else if (!mine.packs.whole(p)) {
+                        const T* src = mine.packs.base + int64_t(p) * N;
+                        if (src >= from && src + N <= to) {
+#pragma unroll
+                            for (int i = 0; i < N; ++i)
+                                if (!mine.packs.inside(int64_t(p) * N + i)) q[u].v[i] = none;
+                        } else {
+                            q[u] = mine.packs.load(p, none);
+                        }
+                    }
+                }
+            }
+            if (kAlone && place_pack >= first && place_pack < first + U * TPR && place_pack % TPR == t) {
+                const T* src = mine.packs.base + int64_t(place_pack) * N;
+                z = to_f32(src >= from && src + N <= to
+                               ? reinterpret_cast<const T*>(slot(stage, (place_pack - first) / TPR))[place % N]
+                               : mine.packs.base[place]);
+            }
+            issue(stage == 0 ? kAhead : stage - 1);  // where the stage before this one was
+            add_packs<ENTROPY>(part, q);
+            stage = stage == kAhead ? 0 : stage + 1;
+        }
+        const float most = part.m;
+        join(part);
+        if constexpr (kAlone) {
+            const float mosts[1] = {most};
+            finish(mine, __shfl_sync(kAll, z, place_pack & 31), part, mosts);
+        } else {
+            if (lane == 0) hand[set].part[t / 32] = part;
+            if (TOP) hand[set].most[t / 32][lane] = most;
+            __syncthreads();
+            if constexpr (CLUSTER) {
+                cluster_barrier();
+                cluster_barrier();
+            }
+        }
+        token = after, set ^= 1;
+    }
+    copy_wait<0>();
+}
+
+template <typename T, int TPR, bool ENTROPY, bool TOP, bool CLUSTER>
+int launch(const ForwardArgs<T>& a, int ranks, cudaStream_t s) {
+    using Geo = Geometry<T, TPR>;
+    auto* kernel = k_logprobs<T, TPR, ENTROPY, TOP, CLUSTER>;
     static Resident resident;
-    const int grid =
-        resident.grid(reinterpret_cast<const void*>(k_logprobs<T, BLOCK, ENTROPY, TOP>), BLOCK, 0, a.rows);
+    const int64_t work = (a.rows + Geo::kGroups - 1) / Geo::kGroups * ranks;
+    const int grid = resident.grid(reinterpret_cast<const void*>(kernel), Geo::kBlock, Geo::bytes(TOP), work);
     if (grid == 0) return DL_ERR_CUDA;
-    k_logprobs<T, BLOCK, ENTROPY, TOP><<<grid, BLOCK, 0, s>>>(a);
-    return launch_status();
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3(grid < ranks ? ranks : grid / ranks * ranks);
+    config.blockDim = dim3(Geo::kBlock);
+    config.dynamicSmemBytes = Geo::bytes(TOP);
+    config.stream = s;
+    cudaLaunchAttribute cluster;
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = ranks;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    config.attrs = &cluster;
+    config.numAttrs = CLUSTER ? 1 : 0;
+    if (cudaLaunchKernelEx(&config, kernel, a) != cudaSuccess) {
+        cudaGetLastError();
+        return DL_ERR_CUDA;
+    }
+    return DL_OK;
 }
 
-template <typename T, int BLOCK>
-int launch(const ForwardArgs<T>& a, cudaStream_t s) {
-    if (a.entropy) return a.n_top ? launch<T, BLOCK, true, true>(a, s) : launch<T, BLOCK, true, false>(a, s);
-    return a.n_top ? launch<T, BLOCK, false, true>(a, s) : launch<T, BLOCK, false, false>(a, s);
+template <typename T, int TPR, bool CLUSTER>
+int launch(const ForwardArgs<T>& a, int ranks, cudaStream_t s) {
+    if (a.entropy)
+        return a.n_top ? launch<T, TPR, true, true, CLUSTER>(a, ranks, s)
+                       : launch<T, TPR, true, false, CLUSTER>(a, ranks, s);
+    return a.n_top ? launch<T, TPR, false, true, CLUSTER>(a, ranks, s)
+                   : launch<T, TPR, false, false, CLUSTER>(a, ranks, s);
 }
 
 template <typename T>
 int forward(const ForwardArgs<T>& a, cudaStream_t s) {
-    return launch<T, 256>(a, s);
+    constexpr int N = 16 / sizeof(T);
+    const int64_t packs = a.vocab / N;
+    if (packs <= 256) return launch<T, 32, false>(a, 1, s);
+    // few rows: a cluster for each, while there are SMs for it and the shares fill a block
+    int ranks = 1;
+    while (ranks < 8 && a.rows * ranks * 2 <= 2 * sm_count() && packs / (ranks * 2) >= 256) ranks *= 2;
+    if (ranks > 1) return launch<T, 256, true>(a, ranks, s);
+    return launch<T, 256, false>(a, 1, s);
 }
 
 }  // namespace
