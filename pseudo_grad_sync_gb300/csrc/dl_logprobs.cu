@@ -65,8 +65,8 @@ __device__ __forceinline__ float largest(const Pack<T, N> (&p)[U]) {
 // then taken again with exponents kept finite, which costs the packs with
 // masked logits a second pass and the others nothing.
 template <bool ENTROPY, typename T, int N, int U>
-__device__ __forceinline__ void add_packs(Part& part, const Pack<T, N> (&p)[U]) {
-    part.raise(max_nan(part.m, largest(p)));
+__device__ __forceinline__ void add_packs(Part& part, const Pack<T, N> (&p)[U], float top) {
+    part.raise(max_nan(part.m, top));
     float2 s = make_float2(0.f, 0.f), a = s;
     const float2 minus = both(-part.m), unit = both(kLog2E);
 #pragma unroll
@@ -143,39 +143,49 @@ __device__ __forceinline__ K merge_lists(K key, K reversed, int lane) {
     return key;
 }
 
-// A row, or a block's share of one: packs [begin, end), in stages of U packs per thread.
+// A row, or a block's share of one: packs [begin, end), in stages of U packs
+// per thread. [low, high) of them lie between the logits' first and last place
+// and are copied whole; one that holds a row's edge is masked.
 template <typename T, int TPR, int U>
 struct Share {
     RowPacks<T> packs;
-    int begin, end, stages;
+    int begin, end, low, high, stages;
 
-    __device__ __forceinline__ Share(const T* row, int vocab, int rank, int ranks) : packs(row, vocab) {
+    __device__ __forceinline__ Share(const T* row, int vocab, int rank, int ranks, const T* from, const T* to)
+        : packs(row, vocab) {
         const int each = (packs.packs + ranks - 1) / ranks;
         begin = min(rank * each, packs.packs);
         end = min(begin + each, packs.packs);
+        low = max(begin, packs.base < from ? 1 : 0);
+        high = min(end, packs.packs - (packs.base + int64_t(packs.packs) * packs.N > to ? 1 : 0));
         stages = max((end - begin + TPR * U - 1) / (TPR * U), 1);
     }
 };
 
 constexpr int kCandidates = 64;
 
+// Slots of a thread's share: the largest logit of each stage, or of as many
+// consecutive ones as make the slots suffice.
+template <typename T, int WARPS>
+constexpr int kSlots = sizeof(T) == 4 && WARPS > 1 ? 8 : 16;
+
 // What a block's warps hand over at a row's end, in turns: the last warp
 // works on one row's while the others fill in the next one's.
-template <int WARPS>
-struct Handover {
+template <typename T, int WARPS>
+struct alignas(16) Handover {
     Part part[WARPS];
-    float most[WARPS][32];
+    T most[kSlots<T, WARPS>][WARPS * 32];
 };
-// The finishing warp's own: the packs it reads again, the threads that had
-// them, candidates, and a cluster's exchange.
+// The finishing warp's own: the packs it reads again, the threads and slots
+// that had them, candidates, and a cluster's exchange.
 template <int WARPS>
-struct Finish {
-    static constexpr int kRead = WARPS == 1 ? 4 : 16;
+struct alignas(16) Finish {
+    static constexpr int kRead = 4, kPlaces = 128;
     uint4 again[kRead][32];
     uint64_t candidate[kCandidates + 32 * 8];
     uint64_t key[32];
     Part part;
-    int thread[WARPS * 32];
+    int thread[WARPS * 32], place[kPlaces + 32];
     int waiting;
 };
 
@@ -184,24 +194,30 @@ struct Geometry {
     static constexpr int kWarps = TPR / 32;  // of a row
     static constexpr bool kAlone = kWarps == 1;
     static constexpr int kMain = kAlone ? 128 : TPR, kBlock = kAlone ? kMain : kMain + 32, kGroups = kMain / TPR;
-    static constexpr int U = kAlone ? 2 : 4, kStages = kAlone ? 6 : 3;
+    static constexpr int U = kAlone ? 2 : 4, kStages = kAlone ? 6 : 3, kHands = kAlone ? 1 : 2;
     static constexpr size_t kRing = size_t(kStages) * U * kMain * 16;
-    static constexpr size_t kHand = kAlone ? 0 : 2 * sizeof(Handover<kWarps>);
-    static constexpr size_t kFinish = sizeof(Finish<kWarps>);
-    static constexpr size_t bytes(bool top) { return kRing + kHand + (top ? kFinish * kGroups : sizeof(Part)); }
+    static constexpr size_t kHand = sizeof(Handover<T, kWarps>), kFinish = sizeof(Finish<kWarps>);
+    static_assert(kHand % 16 == 0 && kFinish % 16 == 0, "");
+    // a row's ring comes first, its handovers next
+    static constexpr size_t bytes(bool top) {
+        return kRing + (top ? kGroups * (kHands * kHand + kFinish) : kGroups * kHands * (kWarps + 1) * sizeof(Part));
+    }
 };
 
 // The n_top largest logits of a row (or a share) from the largest one of every
-// thread, by one warp; lane i gets the i-th key, 0 past the finite logits.
+// thread and slot, by one warp; lane i gets the i-th key, 0 past the finite logits.
 //
 // The n_top-th largest of the threads' maxima is a bound that no alternative
-// lies below, and (ties aside) only n_top threads have a logit that reaches
-// it. Their packs alone are read again, many at a time; what reaches the
-// bound is collected, and sorted in runs of 32.
-template <typename T, int TPR, int WARPS, typename S>
-__device__ __forceinline__ uint64_t alternatives(const S& mine, const float (&most)[WARPS], int n_top, int lane,
+// lies below, and (ties aside) n_top threads and hardly more slots have a
+// logit that reaches it. Their packs alone are read again; what reaches the
+// bound is collected, and sorted in runs of 32. One warp's instructions are
+// what this costs: every step leaves the next one little to look at.
+template <typename T, int TPR, int U, int WARPS, typename S>
+__device__ __forceinline__ uint64_t alternatives(const S& mine, const float (&most)[WARPS],
+                                                 const T (*slots)[WARPS * 32], int n_top, int lane,
                                                  Finish<WARPS>& own) {
-    constexpr int N = 16 / sizeof(T), kRead = Finish<WARPS>::kRead;
+    constexpr int N = 16 / sizeof(T), kRead = Finish<WARPS>::kRead, kPlaces = Finish<WARPS>::kPlaces;
+    constexpr int kOf = kSlots<T, WARPS>;
     using P = Pack<T, N>;
     float best[WARPS];
 #pragma unroll
@@ -223,68 +239,83 @@ __device__ __forceinline__ uint64_t alternatives(const S& mine, const float (&mo
     if (lane == 0) own.waiting = 0;
     __syncwarp();
     uint64_t found = 0, least = 0;  // the list so far, its n_top-th key
+    bool some = false;
     auto take = [&](int count) {
         for (int c = 0; c < count; c += 32) {
             uint64_t next[1] = {c + lane < count ? own.candidate[c + lane] : 0};
             sort_lists(next, lane);
-            found = merge_lists(found, __shfl_sync(kAll, next[0], 31 - lane), lane);
+            found = some ? merge_lists(found, __shfl_sync(kAll, next[0], 31 - lane), lane) : next[0];
+            some = true;
         }
         least = __shfl_sync(kAll, found, n_top - 1);
         __syncwarp();
         if (lane == 0) own.waiting = 0;
         __syncwarp();
     };
-    // item i: pack i % packs of the (i / packs)-th thread; a lane takes every 32nd
-    const int packs = max((mine.end - mine.begin + TPR - 1) / TPR, 1), items = threads * packs;
-    const int more_threads = 32 / packs, more_packs = 32 % packs;
-    int who = lane / packs, at = lane % packs;
-    auto advance = [&](int& w, int& p) {
-        w += more_threads, p += more_packs;
-        if (p >= packs) p -= packs, ++w;
-    };
     const T none = from_f32<T>(-INFINITY);
-    for (int first = lane; first - lane < items; first += 32 * kRead) {
-        int w = who, p = at;
+    const int per = (mine.stages + kOf - 1) / kOf, packs = per * U;  // stages and packs of a slot
+    const int more = 32 / packs, rest = 32 % packs;
+    // the packs of `places` slots: item i is pack i % packs of the (i / packs)-th
+    auto read = [&](int places) {
+        int which = lane / packs, at = lane % packs;
+        for (int first = 0; first < places * packs; first += 32 * kRead) {
+            int pack[kRead];
 #pragma unroll
-        for (int r = 0; r < kRead; ++r) {
-            if (first + 32 * r < items) {
-                const int pack = mine.begin + p * TPR + own.thread[w];
-                if (pack < mine.end && mine.packs.whole(pack))
-                    copy_async<16>(&own.again[r][lane], mine.packs.base + int64_t(pack) * N);
+            for (int r = 0; r < kRead; ++r) {
+                pack[r] = mine.end;
+                if (which < places) {
+                    const int place = own.place[which];
+                    pack[r] = mine.begin + ((place >> 16) * packs + at) * TPR + (place & 0xffff);
+                }
+                if (pack[r] < mine.end && mine.packs.whole(pack[r]))
+                    copy_async<16>(&own.again[r][lane], mine.packs.base + int64_t(pack[r]) * N);
+                which += more, at += rest;
+                if (at >= packs) at -= packs, ++which;
             }
-            advance(w, p);
-        }
-        copy_commit();
-        copy_wait<0>();
-        for (int r = 0; r < kRead && first - lane + 32 * r < items; ++r) {
-            bool any = false;
-            if (first + 32 * r < items) {
-                const int pack = mine.begin + at * TPR + own.thread[who];
-                if (pack < mine.end) {
-                    const P q[1] = {mine.packs.whole(pack) ? *reinterpret_cast<const P*>(&own.again[r][lane])
-                                                           : mine.packs.load(pack, none)};
+            copy_commit();
+            copy_wait<0>();
+#pragma unroll
+            for (int r = 0; r < kRead; ++r) {
+                bool any = false;
+                if (pack[r] < mine.end) {
+                    const P q[1] = {mine.packs.whole(pack[r]) ? *reinterpret_cast<const P*>(&own.again[r][lane])
+                                                              : mine.packs.load(pack[r], none)};
                     any = largest(q) >= bound;
                     if (any) {
-#pragma unroll
                         for (int i = 0; i < N; ++i) {
                             const float v = to_f32(q[0].v[i]);
+                            if (!(v >= bound)) continue;
                             const uint64_t k =
-                                key_of(v, static_cast<uint32_t>(int64_t(pack) * N + i - mine.packs.skew));
-                            if (v >= bound && k > least) own.candidate[atomicAdd(&own.waiting, 1)] = k;
+                                key_of(v, static_cast<uint32_t>(int64_t(pack[r]) * N + i - mine.packs.skew));
+                            if (k > least) own.candidate[atomicAdd(&own.waiting, 1)] = k;
                         }
                     }
                 }
+                if (__any_sync(kAll, any)) {
+                    __syncwarp();
+                    const int waiting = own.waiting;
+                    __syncwarp();
+                    if (waiting >= kCandidates) take(waiting);
+                }
             }
-            if (__any_sync(kAll, any)) {
-                __syncwarp();
-                const int waiting = own.waiting;
-                __syncwarp();
-                if (waiting >= kCandidates) take(waiting);
-            }
-            advance(who, at);
+        }
+        __syncwarp();
+    };
+    int places = 0;
+    for (int i = lane; i - lane < threads * kOf; i += 32) {
+        const int slot = i % kOf, who = i < threads * kOf ? own.thread[i / kOf] : 0;
+        const bool reaches = i < threads * kOf && slot * per < mine.stages && to_f32(slots[slot][who]) >= bound;
+        const unsigned lanes = __ballot_sync(kAll, reaches);
+        if (reaches) own.place[places + __popc(lanes & ((1u << lane) - 1))] = slot << 16 | who;
+        places += __popc(lanes);
+        if (places >= kPlaces) {
+            __syncwarp();
+            read(places);
+            places = 0;
         }
     }
     __syncwarp();
+    read(places);
     take(own.waiting);
     return found;
 }
@@ -307,23 +338,31 @@ __global__ void __launch_bounds__(Geometry<T, TPR>::kBlock, TPR == 32 ? 6 : 3)
     using P = Pack<T, N>;
     using Mine = Share<T, TPR, U>;
     extern __shared__ __align__(16) unsigned char smem[];
-    Handover<kWarps>* const hand = reinterpret_cast<Handover<kWarps>*>(smem + Geo::kRing);
     const int group = kAlone ? threadIdx.x / 32 : 0, lane = threadIdx.x % 32;
-    Finish<kWarps>& own = reinterpret_cast<Finish<kWarps>*>(smem + Geo::kRing + Geo::kHand)[group];
+    // without alternatives only parts are handed over, and a cluster exchanges one
+    using Hand = Handover<T, kWarps>;
+    Hand* const hand = reinterpret_cast<Hand*>(smem + Geo::kRing) + (TOP ? group * Geo::kHands : 0);
+    auto parts = [&](int set) {
+        return TOP ? hand[set].part : reinterpret_cast<Part*>(smem + Geo::kRing) + set * kWarps;
+    };
+    Finish<kWarps>& own =
+        reinterpret_cast<Finish<kWarps>*>(smem + Geo::kRing + Geo::kHand * Geo::kHands * Geo::kGroups)[group];
     const int rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
     const int ranks = CLUSTER ? static_cast<int>(cluster_size()) : 1;
     const int64_t step = int64_t(gridDim.x) / ranks * Geo::kGroups;
     auto token_of = [&](int64_t row) { return a.tokens && row < a.rows ? token_at(a.tokens, a.token_type, row) : 0; };
-    auto share = [&](int64_t row) { return Mine(a.logits + row * a.stride, a.vocab, rank, ranks); };
+    auto share = [&](int64_t row) {
+        return Mine(a.logits + row * a.stride, a.vocab, rank, ranks, a.logits,
+                    a.logits + (a.rows - 1) * a.stride + a.vocab);
+    };
     int64_t row = (CLUSTER ? blockIdx.x / ranks : blockIdx.x) * int64_t(Geo::kGroups) + group;
     int64_t token = token_of(row);
 
-    auto finish = [&](const Mine& mine, float z, Part part, const float (&most)[kWarps]) {
+    auto finish = [&](const Mine& mine, float z, Part part, const float (&most)[kWarps], int set) {
         uint64_t found = 0;
-        if constexpr (TOP) found = alternatives<T, TPR, kWarps>(mine, most, a.n_top, lane, own);
+        if constexpr (TOP) found = alternatives<T, TPR, U, kWarps>(mine, most, hand[set].most, a.n_top, lane, own);
         if constexpr (CLUSTER) {
-            // without alternatives the exchange holds a part alone
-            Part* const shared = TOP ? &own.part : reinterpret_cast<Part*>(&own);
+            Part* const shared = TOP ? &own.part : parts(Geo::kHands);
             if (lane == 0) *shared = part;
             if (TOP) own.key[lane] = found;
             cluster_barrier();
@@ -380,12 +419,21 @@ __global__ void __launch_bounds__(Geometry<T, TPR>::kBlock, TPR == 32 ? 6 : 3)
                 float z = NAN;
                 if (lane == 0 && a.tokens && token < a.vocab) z = to_f32(a.logits[row * a.stride + token]);
                 __syncthreads();
-                Part part = lane < kWarps ? hand[set].part[lane] : Part::nothing();
+                Part part = lane < kWarps ? parts(set)[lane] : Part::nothing();
                 join(part);
+                const Mine mine = share(row);
                 float most[kWarps];
+                if constexpr (TOP) {
+                    // the threads' maxima from their slots'
+                    const int used = min(mine.stages, kSlots<T, kWarps>);
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) most[w] = TOP ? hand[set].most[w][lane] : 0.f;
-                finish(share(row), z, part, most);
+                    for (int w = 0; w < kWarps; ++w) most[w] = -INFINITY;
+                    for (int i = 0; i < used; ++i)
+#pragma unroll
+                        for (int w = 0; w < kWarps; ++w)
+                            most[w] = fmaxf(most[w], to_f32(hand[set].most[i][w * 32 + lane]));
+                }
+                finish(mine, z, part, most, set);
                 set ^= 1;
             }
             token = after;
@@ -397,31 +445,32 @@ __global__ void __launch_bounds__(Geometry<T, TPR>::kBlock, TPR == 32 ? 6 : 3)
     P* const ring = reinterpret_cast<P*>(smem) + threadIdx.x;
     auto slot = [&](int stage, int u) { return ring + (stage * U + u) * Geo::kMain; };
     const T none = from_f32<T>(-INFINITY);
-    // the first and last place of the logits: a pack that holds a row's edge is
-    // copied whole where it lies between them, and masked
-    const T* const from = a.logits;
-    const T* const to = a.logits + (a.rows - 1) * a.stride + a.vocab;
     // what is copied next: stage `next_k` of row `next`
     int64_t next = row, next_token = token, next_after = token_of(row + step);
     auto skip = [&]() {  // to the first row that is not left out
         while (next < a.rows && next_token < 0) next += step, next_token = next_after, next_after = token_of(next + step);
     };
     skip();
-    Mine then = share(next < a.rows ? next : 0);
-    int next_k = 0;
+    const T* src;                    // this thread's first pack of the stage
+    int at, low, span, next_stages;  // its number; which ones are copied
+    auto begin = [&]() {
+        if (next >= a.rows) return;
+        const Mine m = share(next);
+        at = m.begin + t, src = m.packs.base + int64_t(at) * N;
+        low = m.low, span = m.high - m.low, next_stages = m.stages;
+    };
+    begin();
     auto issue = [&](int stage) {
         if (next < a.rows) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int p = then.begin + (next_k * U + u) * TPR + t;
-                const T* src = then.packs.base + int64_t(p) * N;
-                if (p < then.end && src >= from && src + N <= to) copy_async<16>(slot(stage, u), src);
-            }
-            if (++next_k >= then.stages) {
+            for (int u = 0; u < U; ++u)
+                if (static_cast<unsigned>(at + u * TPR - low) < static_cast<unsigned>(span))
+                    copy_async<16>(slot(stage, u), src + u * TPR * N);
+            at += U * TPR, src += U * TPR * N;
+            if (--next_stages == 0) {
                 next += step, next_token = next_after, next_after = token_of(next + step);
                 skip();
-                if (next < a.rows) then = share(next);
-                next_k = 0;
+                begin();
             }
         }
         copy_commit();
@@ -441,6 +490,11 @@ __global__ void __launch_bounds__(Geometry<T, TPR>::kBlock, TPR == 32 ? 6 : 3)
         const int64_t place = token + mine.packs.skew;
         const int place_pack = kAlone && a.tokens && token < a.vocab ? static_cast<int>(place / N) : -1;
         Part part = Part::nothing();
+        // alternatives: the largest logit of the slot, and of the slots before
+        constexpr int kOf = kSlots<T, kWarps>;
+        const int per = TOP ? (mine.stages + kOf - 1) / kOf : 1;
+        int in_slot = 0, slot_at = 0;
+        float slot_most = -INFINITY, most = -INFINITY;
         for (int k = 0; k < mine.stages; ++k) {
             copy_wait<kAhead - 1>();
             const int first = mine.begin + k * U * TPR;
@@ -456,8 +510,7 @@ __global__ void __launch_bounds__(Geometry<T, TPR>::kBlock, TPR == 32 ? 6 : 3)
 #pragma unroll
                         for (int i = 0; i < N; ++i) q[u].v[i] = none;
                     } else if (!mine.packs.whole(p)) {
-                        const T* src = mine.packs.base + int64_t(p) * N;
-                        if (src >= from && src + N <= to) {
+                        if (p >= mine.low && p < mine.high) {
 #pragma unroll
                             for (int i = 0; i < N; ++i)
                                 if (!mine.packs.inside(int64_t(p) * N + i)) q[u].v[i] = none;
@@ -468,30 +521,38 @@ __global__ void __launch_bounds__(Geometry<T, TPR>::kBlock, TPR == 32 ? 6 : 3)
                 }
             }
             if (kAlone && place_pack >= first && place_pack < first + U * TPR && place_pack % TPR == t) {
-                const T* src = mine.packs.base + int64_t(place_pack) * N;
-                z = to_f32(src >= from && src + N <= to
+                z = to_f32(place_pack >= mine.low && place_pack < mine.high
                                ? reinterpret_cast<const T*>(slot(stage, (place_pack - first) / TPR))[place % N]
                                : mine.packs.base[place]);
             }
             issue(stage == 0 ? kAhead : stage - 1);  // where the stage before this one was
-            add_packs<ENTROPY>(part, q);
+            const float here = largest(q);
+            add_packs<ENTROPY>(part, q, here);
+            if constexpr (TOP) {
+                slot_most = fmaxf(slot_most, here);
+                if (++in_slot == per || k == mine.stages - 1) {
+                    hand[set].most[slot_at][t] = from_f32<T>(slot_most);
+                    most = fmaxf(most, slot_most);
+                    ++slot_at, in_slot = 0, slot_most = -INFINITY;
+                }
+            }
             stage = stage == kAhead ? 0 : stage + 1;
         }
-        const float most = part.m;
         join(part);
         if constexpr (kAlone) {
             const float mosts[1] = {most};
-            finish(mine, __shfl_sync(kAll, z, place_pack & 31), part, mosts);
+            __syncwarp();  // the slots
+            finish(mine, __shfl_sync(kAll, z, place_pack & 31), part, mosts, 0);
         } else {
-            if (lane == 0) hand[set].part[t / 32] = part;
-            if (TOP) hand[set].most[t / 32][lane] = most;
+            if (lane == 0) parts(set)[t / 32] = part;
             __syncthreads();
             if constexpr (CLUSTER) {
                 cluster_barrier();
                 cluster_barrier();
             }
         }
-        token = after, set ^= 1;
+        token = after;
+        if (!kAlone) set ^= 1;
     }
     copy_wait<0>();
 }
@@ -535,7 +596,7 @@ template <typename T>
 int forward(const ForwardArgs<T>& a, cudaStream_t s) {
     constexpr int N = 16 / sizeof(T);
     const int64_t packs = a.vocab / N;
-    if (packs <= 256) return launch<T, 32, false>(a, 1, s);
+    if (packs <= 4096 && (packs <= 256 || a.rows >= 4096)) return launch<T, 32, false>(a, 1, s);
     // few rows: a cluster for each, while there are SMs for it and the shares fill a block
     int ranks = 1;
     while (ranks < 8 && a.rows * ranks * 2 <= 2 * sm_count() && packs / (ranks * 2) >= 256) ranks *= 2;
