@@ -174,6 +174,7 @@ constexpr int kSlots = sizeof(T) == 4 && WARPS > 1 ? 8 : 16;
 template <typename T, int WARPS>
 struct alignas(16) Handover {
     Part part[WARPS];
+    float best[WARPS][32];
     T most[kSlots<T, WARPS>][WARPS * 32];
 };
 // The finishing warp's own: the packs it reads again, the threads and slots
@@ -209,7 +210,8 @@ struct Geometry {
 //
 // The n_top-th largest of the threads' maxima is a bound that no alternative
 // lies below, and (ties aside) n_top threads and hardly more slots have a
-// logit that reaches it. Their packs alone are read again; what reaches the
+// logit that reaches it. (Of eight warps' maxima the two largest of every lane
+// are taken for all: a bound hardly lower, for a quarter of the sorting.) Their packs alone are read again; what reaches the
 // bound is collected, and sorted in runs of 32. One warp's instructions are
 // what this costs: every step leaves the next one little to look at.
 template <typename T, int TPR, int U, int WARPS, typename S>
@@ -219,16 +221,19 @@ __device__ __forceinline__ uint64_t alternatives(const S& mine, const float (&mo
     constexpr int N = 16 / sizeof(T), kRead = Finish<WARPS>::kRead, kPlaces = Finish<WARPS>::kPlaces;
     constexpr int kOf = kSlots<T, WARPS>;
     using P = Pack<T, N>;
-    float best[WARPS];
+    // a bound from the two largest of every lane's threads: n_top of these reach it
+    float first[1] = {most[0]}, second[1] = {-INFINITY};
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) best[w] = most[w];
-    sort_lists(best, lane);
-#pragma unroll
-    for (int half = WARPS / 2; half > 0; half /= 2)
-#pragma unroll
-        for (int w = 0; w < half; ++w)
-            best[w] = merge_lists(best[w], __shfl_sync(kAll, best[w + half], 31 - lane), lane);
-    const float bound = __shfl_sync(kAll, best[0], n_top - 1);
+    for (int w = 1; w < WARPS; ++w) {
+        second[0] = fmaxf(second[0], fminf(first[0], most[w]));
+        first[0] = fmaxf(first[0], most[w]);
+    }
+    sort_lists(first, lane);
+    if constexpr (WARPS > 1) {
+        sort_lists(second, lane);
+        first[0] = merge_lists(first[0], __shfl_sync(kAll, second[0], 31 - lane), lane);
+    }
+    const float bound = fmaxf(__shfl_sync(kAll, first[0], n_top - 1), -FLT_MAX);
     int threads = 0;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
@@ -254,10 +259,10 @@ __device__ __forceinline__ uint64_t alternatives(const S& mine, const float (&mo
     };
     const T none = from_f32<T>(-INFINITY);
     const int per = (mine.stages + kOf - 1) / kOf, packs = per * U;  // stages and packs of a slot
-    const int more = 32 / packs, rest = 32 % packs;
+    const int more = 32u / packs, rest = 32 - more * packs, lane_which = unsigned(lane) / packs;
     // the packs of `places` slots: item i is pack i % packs of the (i / packs)-th
     auto read = [&](int places) {
-        int which = lane / packs, at = lane % packs;
+        int which = lane_which, at = lane - lane_which * packs;
         for (int first = 0; first < places * packs; first += 32 * kRead) {
             int pack[kRead];
 #pragma unroll
@@ -302,9 +307,12 @@ __device__ __forceinline__ uint64_t alternatives(const S& mine, const float (&mo
         __syncwarp();
     };
     int places = 0;
-    for (int i = lane; i - lane < threads * kOf; i += 32) {
-        const int slot = i % kOf, who = i < threads * kOf ? own.thread[i / kOf] : 0;
-        const bool reaches = i < threads * kOf && slot * per < mine.stages && to_f32(slots[slot][who]) >= bound;
+    const int used = (mine.stages + per - 1) / per;
+    for (int i = 0; i < used * threads; i += 32) {
+        // item i + lane: thread by thread, slot by slot
+        const int item = i + lane, slot = unsigned(item) / threads;
+        const int who = own.thread[item - slot * threads];
+        const bool reaches = slot < used && to_f32(slots[min(slot, kOf - 1)][who]) >= bound;
         const unsigned lanes = __ballot_sync(kAll, reaches);
         if (reaches) own.place[places + __popc(lanes & ((1u << lane) - 1))] = slot << 16 | who;
         places += __popc(lanes);
@@ -374,9 +382,18 @@ __global__ void __launch_bounds__(Geometry<T, TPR>::kBlock, TPR == 32 ? 6 : 3)
                     part.a = load_cluster(&shared->a, lane);
                 }
                 join(part);
-                if (TOP)
-                    for (int r = 1; r < ranks; ++r)
-                        found = merge_lists(found, load_cluster(&own.key[31 - lane], r), lane);
+                if constexpr (TOP) {
+                    uint64_t of[8];
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) of[r] = r < ranks ? load_cluster(&own.key[lane], r) : 0;
+#pragma unroll
+                    for (int half = 4; half > 0; half /= 2)
+#pragma unroll
+                        for (int r = 0; r < half; ++r)
+                            if (half < ranks)
+                                of[r] = merge_lists(of[r], __shfl_sync(kAll, of[r + half], 31 - lane), lane);
+                    found = of[0];
+                }
             }
             cluster_barrier();
             if (rank != 0) return;
@@ -424,14 +441,8 @@ __global__ void __launch_bounds__(Geometry<T, TPR>::kBlock, TPR == 32 ? 6 : 3)
                 const Mine mine = share(row);
                 float most[kWarps];
                 if constexpr (TOP) {
-                    // the threads' maxima from their slots'
-                    const int used = min(mine.stages, kSlots<T, kWarps>);
 #pragma unroll
-                    for (int w = 0; w < kWarps; ++w) most[w] = -INFINITY;
-                    for (int i = 0; i < used; ++i)
-#pragma unroll
-                        for (int w = 0; w < kWarps; ++w)
-                            most[w] = fmaxf(most[w], to_f32(hand[set].most[i][w * 32 + lane]));
+                    for (int w = 0; w < kWarps; ++w) most[w] = hand[set].best[w][lane];
                 }
                 finish(mine, z, part, most, set);
                 set ^= 1;
@@ -490,11 +501,10 @@ __global__ void __launch_bounds__(Geometry<T, TPR>::kBlock, TPR == 32 ? 6 : 3)
         const int64_t place = token + mine.packs.skew;
         const int place_pack = kAlone && a.tokens && token < a.vocab ? static_cast<int>(place / N) : -1;
         Part part = Part::nothing();
-        // alternatives: the largest logit of the slot, and of the slots before
         constexpr int kOf = kSlots<T, kWarps>;
         const int per = TOP ? (mine.stages + kOf - 1) / kOf : 1;
         int in_slot = 0, slot_at = 0;
-        float slot_most = -INFINITY, most = -INFINITY;
+        float slot_most = -INFINITY, most = -INFINITY;  // of the slot, of the row
         for (int k = 0; k < mine.stages; ++k) {
             copy_wait<kAhead - 1>();
             const int first = mine.begin + k * U * TPR;
@@ -545,6 +555,7 @@ __global__ void __launch_bounds__(Geometry<T, TPR>::kBlock, TPR == 32 ? 6 : 3)
             finish(mine, __shfl_sync(kAll, z, place_pack & 31), part, mosts, 0);
         } else {
             if (lane == 0) parts(set)[t / 32] = part;
+            if (TOP) hand[set].best[t / 32][lane] = most;
             __syncthreads();
             if constexpr (CLUSTER) {
                 cluster_barrier();
