@@ -48,7 +48,7 @@ __device__ __forceinline__ float largest(const Pack<T, N> (&p)[U]) {
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = u == 0; i < N / 2; ++i) r = __hmax2_nan(r, reinterpret_cast<const T2*>(p[u].v)[i]);
-        const float2 f = as_floats(*reinterpret_cast<const uint32_t*>(&r), T());
+        const float2 f = unpack2(*reinterpret_cast<const uint32_t*>(&r), T());
         return max_nan(f.x, f.y);
     } else {
         float r = p[0].v[0];
@@ -73,7 +73,7 @@ __device__ __forceinline__ void add_packs(Part& part, const Pack<T, N> (&p)[U], 
     for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
-            const float2 t = mul2(add2(pair_at(p[u], i), minus), unit);
+            const float2 t = mul2(add2(pair_of(&p[u], i), minus), unit);
             const float2 e = make_float2(exp2_fast(t.x), exp2_fast(t.y));
             s = add2(s, e);
             if (ENTROPY) a = fma2(e, t, a);

@@ -8,7 +8,7 @@
 
 #include <math.h>
 
-#include "dl_types.cuh"
+#include "dl_norm.cuh"
 
 namespace dl {
 
@@ -26,22 +26,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
-}
-
-__device__ __forceinline__ float2 as_floats(uint32_t w, __nv_bfloat16) {
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-__device__ __forceinline__ float2 as_floats(uint32_t w, __half) {
-    return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-// elements 2i and 2i + 1 of a pack
-template <typename T, int N>
-__device__ __forceinline__ float2 pair_at(const Pack<T, N>& p, int i) {
-    if constexpr (sizeof(T) == 2) {
-        return as_floats(reinterpret_cast<const uint32_t*>(p.v)[i], T());
-    } else {
-        return make_float2(p.v[2 * i], p.v[2 * i + 1]);
-    }
 }
 
 // A row's packs. `base` is the boundary at or before its start.

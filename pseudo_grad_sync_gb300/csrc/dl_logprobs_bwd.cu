@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(BLOCK) k_logprobs_bwd(const __grid_constant__ 
                 } else {
 #pragma unroll
                     for (int i = 0; i < N / 2; ++i) {
-                        const float2 v = r.at(pair_at(q[u], i));
+                        const float2 v = r.at(pair_of(&q[u], i));
                         q[u].v[2 * i] = from_f32<T>(v.x), q[u].v[2 * i + 1] = from_f32<T>(v.y);
                     }
                 }

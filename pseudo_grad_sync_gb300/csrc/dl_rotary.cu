@@ -3,7 +3,7 @@
 #include <math.h>
 #include <stdint.h>
 
-#include "dl_types.cuh"
+#include "dl_norm.cuh"
 
 namespace dl {
 namespace {
@@ -14,10 +14,13 @@ struct RotaryArgs {
     dl_rotary_job job[DL_ROTARY_MAX_JOBS];
     const uint64_t* turns;
     const void* positions;
-    int64_t tokens, total;  // tokens of a batch and of all
-    int64_t position_stride, first, tiles;
+    int64_t batch, tokens;
+    int64_t position_batch, position_token;  // strides
+    int64_t first, first_step;               // of the tokens where positions is NULL
+    int64_t tiles_per_batch, tiles;
     float amplitude, direction;  // direction: -1 for the inverse
-    int32_t n_jobs, head_dim, pairs, position_type, tile;
+    int32_t n_jobs, head_dim, pairs, position_type;
+    int32_t tile, lanes;  // tokens of a tile, heads of a token side by side
 };
 
 // cos and sin of position * turns / 2^64 turns. The product wraps to the exact
@@ -37,113 +40,193 @@ __device__ __forceinline__ float2 cos_sin(uint64_t position, uint64_t turns) {
 }
 
 __device__ __forceinline__ uint64_t position_of(const RotaryArgs& a, int64_t batch, int64_t token) {
-    if (!a.positions) return static_cast<uint64_t>(a.first) + static_cast<uint64_t>(token);
-    const int64_t at = batch * a.position_stride + token;
+    if (!a.positions) return static_cast<uint64_t>(a.first) + static_cast<uint64_t>(token * a.first_step);
+    const int64_t at = batch * a.position_batch + token * a.position_token;
     return static_cast<uint64_t>(a.position_type == DL_I64 ? static_cast<const int64_t*>(a.positions)[at]
                                                            : static_cast<const int32_t*>(a.positions)[at]);
 }
 
-// (a, b) turned: a product and a fused product each, so that every form of the
-// kernel gives the same bits.
-__device__ __forceinline__ void turn(float& a, float& b, float2 cs) {
-    const float first = fmaf(a, cs.x, -__fmul_rn(b, cs.y));
-    b = fmaf(b, cs.x, __fmul_rn(a, cs.y));
+// A unit of a head: what one thread turns or copies at once.
+template <int N, bool INTERLEAVED>
+struct Form {
+    static constexpr bool kTwo = !INTERLEAVED || N == 1;  // two packs, else one
+    static constexpr int kSize = kTwo ? 2 * N : N, kPairs = kSize / 2;
+    static constexpr int kStep = INTERLEAVED ? kSize : N;  // from a turned unit's first pack to the next one's
+    static __host__ __device__ int units(int head_dim, int pairs) {
+        return pairs / kPairs + ((head_dim - 2 * pairs) / N * N + kSize - 1) / kSize;
+    }
+};
+
+// Two pairs turned: a product and a fused product each, in this order in every
+// form of the kernel, so that they all give the same bits.
+__device__ __forceinline__ void turn(float2& a, float2& b, float2 c, float2 s) {
+    const float2 bs = mul2(b, s), as = mul2(a, s);
+    a = fma2(a, c, make_float2(-bs.x, -bs.y));
+    b = fma2(b, c, as);
+}
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+    const float first = fmaf(a, c, -__fmul_rn(b, s));
+    b = fmaf(b, c, __fmul_rn(a, s));
     a = first;
+}
+
+// elements 2i and 2i + 1 of a pack
+template <typename T, int N>
+__device__ __forceinline__ void set_pair(Pack<T, N>& p, int i, float2 v) {
+    if constexpr (sizeof(T) == 2) {
+        reinterpret_cast<uint32_t*>(p.v)[i] = pack2(v, T());
+    } else {
+        p.v[2 * i] = v.x, p.v[2 * i + 1] = v.y;
+    }
+}
+
+// A unit's pairs turned in place. Half layout: the pairs' first elements in v,
+// the second ones in w; interleaved: neighbours in v (packs of one: in v and w).
+template <typename T, int N, bool INTERLEAVED, int PAIRS>
+__device__ __forceinline__ void turn_unit(Pack<T, N>& v, Pack<T, N>& w, const float2 (&cs)[PAIRS]) {
+    if constexpr (N == 1) {
+        float a = to_f32(v.v[0]), b = to_f32(w.v[0]);
+        turn(a, b, cs[0].x, cs[0].y);
+        v.v[0] = from_f32<T>(a), w.v[0] = from_f32<T>(b);
+    } else if constexpr (INTERLEAVED) {
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) {
+            float2 e = pair_of(&v, i);
+            turn(e.x, e.y, cs[i].x, cs[i].y);
+            set_pair(v, i, e);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < PAIRS / 2; ++i) {
+            float2 a = pair_of(&v, i), b = pair_of(&w, i);
+            turn(a, b, make_float2(cs[2 * i].x, cs[2 * i + 1].x), make_float2(cs[2 * i].y, cs[2 * i + 1].y));
+            set_pair(v, i, a);
+            set_pair(w, i, b);
+        }
+    }
 }
 
 // A block takes a tile of consecutive tokens, all heads of all tensors. First
 // its threads compute the tile's cosines and sines into shared memory, one per
-// (token, pair), so that a token's heads share them; then they walk over the
-// (token, head) rows, each thread on a fixed unit of the row: a pack of N
-// elements (half layout: the pack of its pairs' partners beside it), or a pack
-// behind the rotated part that is only copied.
+// (token, pair), so that a token's heads share them. Then each thread keeps
+// those of one unit of one token in registers and walks over the heads: a unit
+// is a pack of N elements (half layout: with the pack of its pairs' partners),
+// or packs behind the rotated part that are only copied.
 template <typename T, int N, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) k_rotary(const __grid_constant__ RotaryArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) k_rotary(const __grid_constant__ RotaryArgs a) {
     extern __shared__ __align__(16) float2 table[];
     using P = Pack<T, N>;
-    constexpr int kPairs = INTERLEAVED && N > 1 ? N / 2 : N;  // of a unit
-    const int turned = a.pairs / kPairs, rotated = 2 * a.pairs;
-    const int units = turned + (a.head_dim - rotated + N - 1) / N;
-    const int wide = min(units, kThreads), slots = kThreads / wide, slot = threadIdx.x / wide;
+    using F = Form<N, INTERLEAVED>;
+    constexpr int kPairs = F::kPairs, kRows = 4;  // heads at a time
+    constexpr bool kTwo = F::kTwo;
+    const int turned = a.pairs / kPairs, rotated = 2 * a.pairs, units = F::units(a.head_dim, a.pairs);
+    const int wide = min(units, kThreads);
+    const int slot = threadIdx.x / wide, local = slot / a.lanes, head = slot - local * a.lanes;
     for (int64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
-        const int64_t begin = tile * a.tile;
-        const int count = static_cast<int>(min(static_cast<int64_t>(a.tile), a.total - begin));
+        const int64_t batch = a.tiles_per_batch == 1 ? tile : a.batch == 1 ? 0 : tile / a.tiles_per_batch;
+        const int64_t begin = (tile - batch * a.tiles_per_batch) * a.tile;
+        const int count = static_cast<int>(min(static_cast<int64_t>(a.tile), a.tokens - begin));
         for (int i = threadIdx.x; i < count * a.pairs; i += kThreads) {
-            const int64_t at = begin + i / a.pairs, batch = at / a.tokens;
-            float2 cs = cos_sin(position_of(a, batch, at - batch * a.tokens), a.turns[i % a.pairs]);
+            const int token = i / a.pairs, pair = i - token * a.pairs;
+            const float2 cs = cos_sin(position_of(a, batch, begin + token), a.turns[pair]);
             table[i] = make_float2(cs.x * a.amplitude, cs.y * a.amplitude * a.direction);
         }
         __syncthreads();
-        for (int j = 0; j < a.n_jobs; ++j) {
-            const dl_rotary_job& job = a.job[j];
-            const bool in_place = job.x == job.y;
-            if (slot >= slots) continue;
-            for (int64_t row = slot; row < int64_t(count) * job.heads; row += slots) {
-                const int64_t local = row / job.heads, head = row - local * job.heads;
-                const int64_t at = begin + local, batch = at / a.tokens, token = at - batch * a.tokens;
-                const T* x = static_cast<const T*>(job.x) + batch * job.x_batch + token * job.x_token + head * job.x_head;
-                T* y = static_cast<T*>(job.y) + batch * job.y_batch + token * job.y_token + head * job.y_head;
-                for (int u = threadIdx.x % wide; u < units; u += wide) {
-                    if (u >= turned) {
-                        if (in_place) continue;
-                        const int c = rotated + (u - turned) * N;
-                        if (c + N <= a.head_dim) {
-                            *reinterpret_cast<P*>(y + c) = *reinterpret_cast<const P*>(x + c);
-                        } else {
-                            for (int i = c; i < a.head_dim; ++i) y[i] = x[i];
-                        }
-                        continue;
-                    }
-                    const float2* cs = table + local * a.pairs + u * kPairs;
-                    if constexpr (INTERLEAVED && N > 1) {
-                        P v = *reinterpret_cast<const P*>(x + u * N);
+        for (int u = threadIdx.x % wide; local < count && u < units; u += wide) {
+            const bool turns = u < turned;
+            float2 cs[kPairs];
 #pragma unroll
-                        for (int i = 0; i < kPairs; ++i) {
-                            float p = to_f32(v.v[2 * i]), q = to_f32(v.v[2 * i + 1]);
-                            turn(p, q, cs[i]);
-                            v.v[2 * i] = from_f32<T>(p), v.v[2 * i + 1] = from_f32<T>(q);
-                        }
-                        *reinterpret_cast<P*>(y + u * N) = v;
-                    } else {
-                        const int low = INTERLEAVED ? 2 * u : u * N, high = INTERLEAVED ? 2 * u + 1 : a.pairs + u * N;
-                        P v = *reinterpret_cast<const P*>(x + low), w = *reinterpret_cast<const P*>(x + high);
+            for (int i = 0; i < kPairs; ++i) cs[i] = turns ? table[local * a.pairs + u * kPairs + i] : make_float2(0.f, 0.f);
+            const int low = turns ? u * F::kStep : rotated + (u - turned) * F::kSize;
+            const int apart = turns && !INTERLEAVED ? a.pairs : N;  // between a unit's two packs
+            const bool two = kTwo && (turns || low + 2 * N <= a.head_dim);
+            for (int j = 0; j < a.n_jobs; ++j) {
+                const dl_rotary_job& job = a.job[j];
+                if (!turns && job.x == job.y) continue;  // in place: nothing to copy
+                const T* x = static_cast<const T*>(job.x) + batch * job.x_batch + (begin + local) * job.x_token + low;
+                T* y = static_cast<T*>(job.y) + batch * job.y_batch + (begin + local) * job.y_token + low;
+                for (int h = head; h < job.heads; h += kRows * a.lanes) {
+                    P v[kRows], w[kRows];
 #pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            float p = to_f32(v.v[i]), q = to_f32(w.v[i]);
-                            turn(p, q, cs[i]);
-                            v.v[i] = from_f32<T>(p), w.v[i] = from_f32<T>(q);
+                    for (int r = 0; r < kRows; ++r)
+                        if (h + r * a.lanes < job.heads) {
+                            const T* from = x + (h + r * a.lanes) * job.x_head;
+                            v[r] = *reinterpret_cast<const P*>(from);
+                            if (two) w[r] = *reinterpret_cast<const P*>(from + apart);
                         }
-                        *reinterpret_cast<P*>(y + low) = v;
-                        *reinterpret_cast<P*>(y + high) = w;
-                    }
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r)
+                        if (h + r * a.lanes < job.heads) {
+                            T* to = y + (h + r * a.lanes) * job.y_head;
+                            if (turns) turn_unit<T, N, INTERLEAVED>(v[r], w[r], cs);
+                            *reinterpret_cast<P*>(to) = v[r];
+                            if (two) *reinterpret_cast<P*>(to + apart) = w[r];
+                        }
                 }
             }
         }
+        // elements behind the last whole pack
+        const int tail = (a.head_dim - rotated) % N;
+        if (N > 1 && tail > 0)
+            for (int j = 0; j < a.n_jobs; ++j) {
+                const dl_rotary_job& job = a.job[j];
+                if (job.x == job.y) continue;
+                for (int64_t i = threadIdx.x; i < int64_t(count) * job.heads * tail; i += kThreads) {
+                    const int64_t row = i / tail, token = begin + row / job.heads, h = row % job.heads;
+                    const int64_t c = a.head_dim - tail + i % tail;
+                    static_cast<T*>(job.y)[batch * job.y_batch + token * job.y_token + h * job.y_head + c] =
+                        static_cast<const T*>(job.x)[batch * job.x_batch + token * job.x_token + h * job.x_head + c];
+                }
+            }
         __syncthreads();
     }
 }
 
+// How a block's threads are shared out: `wide` units of a head side by side,
+// `lanes` heads, and as many tokens as that leaves room for. Tokens share the
+// latency of a tile's cosines, heads need no more of them; where there are few
+// tokens the heads spread over the threads instead.
 template <typename T, int N, bool INTERLEAVED>
 int launch(RotaryArgs a, cudaStream_t s) {
+    const int units = Form<N, INTERLEAVED>::units(a.head_dim, a.pairs);
+    const int slots = kThreads / (units < kThreads ? units : kThreads);
+    int least = INT32_MAX, most = 1;
+    for (int j = 0; j < a.n_jobs; ++j) {
+        least = a.job[j].heads < least ? a.job[j].heads : least;
+        most = a.job[j].heads > most ? a.job[j].heads : most;
+    }
+    int lanes = 1;
+    while (lanes < 8 && 2 * lanes <= slots && 2 * lanes <= least) lanes *= 2;
+    auto blocks = [&](int l) {
+        const int tile = slots / l;
+        return a.batch * ((a.tokens + tile - 1) / tile);
+    };
+    while (2 * lanes <= slots && lanes < most && blocks(lanes) < 4 * sm_count()) lanes *= 2;
+    a.lanes = lanes, a.tile = slots / lanes;
+    if (a.tile > 4096 / a.pairs) a.tile = 4096 / a.pairs;  // 32 KB of cosines and sines
+    if (a.tile > a.tokens) a.tile = static_cast<int>(a.tokens);
+    a.tiles_per_batch = (a.tokens + a.tile - 1) / a.tile;
+    a.tiles = a.tiles_per_batch * a.batch;
     const size_t bytes = size_t(a.tile) * a.pairs * sizeof(float2);
-    const int64_t most = INT32_MAX;
-    k_rotary<T, N, INTERLEAVED><<<static_cast<unsigned>(a.tiles < most ? a.tiles : most), kThreads, bytes, s>>>(a);
+    k_rotary<T, N, INTERLEAVED>
+        <<<static_cast<unsigned>(a.tiles < INT32_MAX ? a.tiles : INT32_MAX), kThreads, bytes, s>>>(a);
     return launch_status();
 }
 
-template <typename T>
-int apply(const RotaryArgs& a, bool interleaved, cudaStream_t s) {
-    constexpr int N = 16 / sizeof(T);
-    // whole packs: of pairs' first elements beside packs of their second ones
-    // (half layout), or of neighbouring pairs
-    bool packs = (interleaved ? 2 * a.pairs : a.pairs) % N == 0;
-    for (int j = 0; j < a.n_jobs && packs; ++j) {
+// Packs as wide as every address, stride and the pairs allow: 16 bytes, or
+// half of that, down to single elements.
+template <typename T, int N>
+int by_pack(const RotaryArgs& a, bool interleaved, cudaStream_t s) {
+    bool fits = (interleaved ? 2 * a.pairs : a.pairs) % N == 0;
+    for (int j = 0; j < a.n_jobs && fits; ++j) {
         const dl_rotary_job& q = a.job[j];
-        packs = aligned16(q.x) && aligned16(q.y) &&
-                (q.x_batch | q.x_token | q.x_head | q.y_batch | q.y_token | q.y_head) % N == 0;
+        fits = aligned_to(q.x, N * sizeof(T)) && aligned_to(q.y, N * sizeof(T)) &&
+               (q.x_batch | q.x_token | q.x_head | q.y_batch | q.y_token | q.y_head) % N == 0;
     }
-    if (interleaved) return packs ? launch<T, N, true>(a, s) : launch<T, 1, true>(a, s);
-    return packs ? launch<T, N, false>(a, s) : launch<T, 1, false>(a, s);
+    if constexpr (N > 1) {
+        if (!fits) return by_pack<T, N / 2>(a, interleaved, s);
+    }
+    return interleaved ? launch<T, N, true>(a, s) : launch<T, N, false>(a, s);
 }
 
 // Whether [n0][n1][n2][width] at these strides has every element at a place of
@@ -229,17 +312,24 @@ extern "C" int dl_rotary_apply(const dl_rotary_job* jobs, int32_t n_jobs, int32_
     if (!d_turns) return DL_ERR_ARG;
     if (!aligned) return DL_ERR_ALIGN;
     a.turns = d_turns, a.positions = positions;
-    a.tokens = tokens, a.total = batch * tokens;
-    a.position_stride = position_stride, a.first = first;
+    a.batch = batch, a.tokens = tokens;
+    a.position_batch = position_stride, a.position_token = 1;
+    a.first = first, a.first_step = 1;
     a.amplitude = static_cast<float>(amplitude), a.direction = flags & DL_ROTARY_INVERSE ? -1.f : 1.f;
     a.head_dim = head_dim, a.pairs = rotary_dim / 2, a.position_type = position_type;
-    a.tile = 1;
-    a.tiles = (a.total + a.tile - 1) / a.tile;
+    if (tokens == 1) {  // single tokens of many sequences: one sequence of them
+        a.tokens = batch, a.batch = 1;
+        a.position_token = position_stride, a.first_step = 0;
+        for (int32_t j = 0; j < a.n_jobs; ++j) {
+            a.job[j].x_token = a.job[j].x_batch, a.job[j].y_token = a.job[j].y_batch;
+            a.job[j].x_batch = a.job[j].y_batch = 0;
+        }
+    }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool interleaved = flags & DL_ROTARY_INTERLEAVED;
     switch (type) {
-        case DL_F32: return apply<float>(a, interleaved, s);
-        case DL_BF16: return apply<__nv_bfloat16>(a, interleaved, s);
-        default: return apply<__half>(a, interleaved, s);
+        case DL_F32: return by_pack<float, 4>(a, interleaved, s);
+        case DL_BF16: return by_pack<__nv_bfloat16, 8>(a, interleaved, s);
+        default: return by_pack<__half, 8>(a, interleaved, s);
     }
 }
