@@ -20,7 +20,7 @@ struct RotaryArgs {
     int64_t tiles_per_batch, tiles;
     float amplitude, direction;  // direction: -1 for the inverse
     int32_t n_jobs, head_dim, pairs, position_type;
-    int32_t tile, lanes;  // tokens of a tile, heads of a token side by side
+    int32_t tile, side, lanes;  // tokens of a tile, tokens and heads of a token side by side
 };
 
 // cos and sin of position * turns / 2^64 turns. The product wraps to the exact
@@ -122,29 +122,35 @@ __global__ void __launch_bounds__(kThreads, 3) k_rotary(const __grid_constant__ 
     const int turned = a.pairs / kPairs, rotated = 2 * a.pairs, units = F::units(a.head_dim, a.pairs);
     const int wide = min(units, kThreads);
     const int slot = threadIdx.x / wide, local = slot / a.lanes, head = slot - local * a.lanes;
+    const int token0 = threadIdx.x / a.pairs, pair0 = threadIdx.x - token0 * a.pairs;
+    const int more_tokens = kThreads / a.pairs, more_pairs = kThreads - more_tokens * a.pairs;
+    const int first_unit = threadIdx.x % wide;
     for (int64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
         const int64_t batch = a.tiles_per_batch == 1 ? tile : a.batch == 1 ? 0 : tile / a.tiles_per_batch;
         const int64_t begin = (tile - batch * a.tiles_per_batch) * a.tile;
         const int count = static_cast<int>(min(static_cast<int64_t>(a.tile), a.tokens - begin));
-        for (int i = threadIdx.x; i < count * a.pairs; i += kThreads) {
-            const int token = i / a.pairs, pair = i - token * a.pairs;
+        for (int i = threadIdx.x, token = token0, pair = pair0; i < count * a.pairs; i += kThreads) {
             const float2 cs = cos_sin(position_of(a, batch, begin + token), a.turns[pair]);
             table[i] = make_float2(cs.x * a.amplitude, cs.y * a.amplitude * a.direction);
+            token += more_tokens, pair += more_pairs;
+            if (pair >= a.pairs) pair -= a.pairs, ++token;
         }
         __syncthreads();
-        for (int u = threadIdx.x % wide; local < count && u < units; u += wide) {
+        // a token's units (one each but for the widest heads), then the next token
+        for (int l = slot < a.side * a.lanes ? local : count, u = first_unit; l < count;
+             u + wide < units ? u += wide : (u = first_unit, l += a.side)) {
             const bool turns = u < turned;
             float2 cs[kPairs];
 #pragma unroll
-            for (int i = 0; i < kPairs; ++i) cs[i] = turns ? table[local * a.pairs + u * kPairs + i] : make_float2(0.f, 0.f);
+            for (int i = 0; i < kPairs; ++i) cs[i] = turns ? table[l * a.pairs + u * kPairs + i] : make_float2(0.f, 0.f);
             const int low = turns ? u * F::kStep : rotated + (u - turned) * F::kSize;
             const int apart = turns && !INTERLEAVED ? a.pairs : N;  // between a unit's two packs
             const bool two = kTwo && (turns || low + 2 * N <= a.head_dim);
             for (int j = 0; j < a.n_jobs; ++j) {
                 const dl_rotary_job& job = a.job[j];
                 if (!turns && job.x == job.y) continue;  // in place: nothing to copy
-                const T* x = static_cast<const T*>(job.x) + batch * job.x_batch + (begin + local) * job.x_token + low;
-                T* y = static_cast<T*>(job.y) + batch * job.y_batch + (begin + local) * job.y_token + low;
+                const T* x = static_cast<const T*>(job.x) + batch * job.x_batch + (begin + l) * job.x_token + low;
+                T* y = static_cast<T*>(job.y) + batch * job.y_batch + (begin + l) * job.y_token + low;
                 for (int h = head; h < job.heads; h += kRows * a.lanes) {
                     P v[kRows], w[kRows];
 #pragma unroll
@@ -196,14 +202,14 @@ int launch(RotaryArgs a, cudaStream_t s) {
         most = a.job[j].heads > most ? a.job[j].heads : most;
     }
     int lanes = 1;
-    while (lanes < 8 && 2 * lanes <= slots && 2 * lanes <= least) lanes *= 2;
-    auto blocks = [&](int l) {
-        const int tile = slots / l;
-        return a.batch * ((a.tokens + tile - 1) / tile);
-    };
-    while (2 * lanes <= slots && lanes < most && blocks(lanes) < 4 * sm_count()) lanes *= 2;
-    a.lanes = lanes, a.tile = slots / lanes;
-    if (a.tile > 4096 / a.pairs) a.tile = 4096 / a.pairs;  // 32 KB of cosines and sines
+    auto blocks = [&](int tile) { return a.batch * ((a.tokens + tile - 1) / tile); };
+    while (2 * lanes <= slots && (lanes * 8 <= least || (lanes * 2 <= least && blocks(slots / lanes) < 16 * sm_count())))
+        lanes *= 2;
+    while (2 * lanes <= slots && lanes < most && blocks(slots / lanes) < 4 * sm_count()) lanes *= 2;
+    a.lanes = lanes, a.side = slots / lanes, a.tile = a.side;
+    while (a.tile * a.pairs < 512 && blocks(2 * a.tile) >= 8 * sm_count()) a.tile *= 2;
+    const int most_tokens = 4096 / a.pairs;  // 32 KB of cosines and sines
+    if (a.tile > most_tokens) a.tile = most_tokens;
     if (a.tile > a.tokens) a.tile = static_cast<int>(a.tokens);
     a.tiles_per_batch = (a.tokens + a.tile - 1) / a.tile;
     a.tiles = a.tiles_per_batch * a.batch;
