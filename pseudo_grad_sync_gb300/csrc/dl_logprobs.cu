@@ -257,7 +257,6 @@ __device__ __forceinline__ uint64_t alternatives(const S& mine, const float (&mo
         if (lane == 0) own.waiting = 0;
         __syncwarp();
     };
-    const T none = from_f32<T>(-INFINITY);
     const int per = (mine.stages + kOf - 1) / kOf, packs = per * U;  // stages and packs of a slot
     const int more = 32u / packs, rest = 32 - more * packs, lane_which = unsigned(lane) / packs;
     // the packs of `places` slots: item i is pack i % packs of the (i / packs)-th
@@ -284,7 +283,7 @@ __device__ __forceinline__ uint64_t alternatives(const S& mine, const float (&mo
                 bool any = false;
                 if (pack[r] < mine.end) {
                     const P q[1] = {mine.packs.whole(pack[r]) ? *reinterpret_cast<const P*>(&own.again[r][lane])
-                                                              : mine.packs.load(pack[r], none)};
+                                                              : mine.packs.edge(pack[r], kNone<T>)};
                     any = largest(q) >= bound;
                     if (any) {
                         for (int i = 0; i < N; ++i) {
@@ -517,15 +516,14 @@ __global__ void __launch_bounds__(Geometry<T, TPR>::kBlock, TPR == 32 ? 6 : 3)
                 for (int u = 0; u < U; ++u) {
                     const int p = first + u * TPR + t;
                     if (p >= mine.end) {
-#pragma unroll
-                        for (int i = 0; i < N; ++i) q[u].v[i] = none;
+                        q[u] = filled<T, N>(kNone<T>);
                     } else if (!mine.packs.whole(p)) {
                         if (p >= mine.low && p < mine.high) {
 #pragma unroll
                             for (int i = 0; i < N; ++i)
                                 if (!mine.packs.inside(int64_t(p) * N + i)) q[u].v[i] = none;
                         } else {
-                            q[u] = mine.packs.load(p, none);
+                            q[u] = mine.packs.edge(p, kNone<T>);
                         }
                     }
                 }

@@ -8,6 +8,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 #include "dl_norm.cuh"
 
 namespace dl {
@@ -46,18 +48,42 @@ struct RowPacks {
         return (p > 0 || skew == 0) && (int64_t(p) + 1) * N <= end;
     }
     __device__ __forceinline__ bool inside(int64_t place) const { return place >= skew && place < end; }
-    // pack p, `fill` where it lies outside the row
-    __device__ __forceinline__ Pack<T, N> load(int p, T fill) const {
-        if (whole(p)) return reinterpret_cast<const Pack<T, N>*>(base)[p];
+    // pack p of `base`, `fill` where it lies outside the row; element by element
+    // into whole words, as a pack in registers is words
+    __device__ __forceinline__ Pack<T, N> edge(int64_t p, uint32_t fill) const {
         Pack<T, N> r;
+        uint32_t* const w = reinterpret_cast<uint32_t*>(r.v);
+        if constexpr (sizeof(T) == 2) {
+            const uint16_t* from = reinterpret_cast<const uint16_t*>(base);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int64_t at = int64_t(p) * N + i;
-            r.v[i] = inside(at) ? base[at] : fill;
+            for (int i = 0; i < 4; ++i) {
+                const int64_t at = p * N + 2 * i;
+                const uint32_t low = inside(at) ? from[at] : fill, high = inside(at + 1) ? from[at + 1] : fill;
+                w[i] = low | high << 16;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = inside(p * N + i) ? reinterpret_cast<const uint32_t*>(base)[p * N + i] : fill;
         }
         return r;
     }
+    __device__ __forceinline__ Pack<T, N> load(int p, uint32_t fill) const {
+        return whole(p) ? reinterpret_cast<const Pack<T, N>*>(base)[p] : edge(p, fill);
+    }
 };
+
+// the bits of -inf
+template <typename T>
+constexpr uint32_t kNone = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00u : 0xff80u;
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> filled(uint32_t fill) {
+    Pack<T, N> r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        reinterpret_cast<uint32_t*>(r.v)[i] = sizeof(T) == 4 ? fill : fill | fill << 16;
+    return r;
+}
 
 // A cluster's blocks.
 __device__ __forceinline__ uint32_t cluster_rank() {

@@ -6,6 +6,9 @@
 namespace dl {
 namespace {
 
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kThreads = 128;
+
 template <typename T>
 struct BackwardArgs {
     const T* logits;
@@ -32,123 +35,200 @@ struct Row {
     }
 };
 
-// A block takes a chunk of a row: U packs per thread. Every logit's value is
-// p_j times a polynomial of the row; the few columns named by the token and
-// the alternatives get their own gradients on top, before the one rounding:
-// the thread whose chunk has such a column computes it aside and stores it
-// after its packs.
-template <typename T, int N, int BLOCK, int U>
-__global__ void __launch_bounds__(BLOCK) k_logprobs_bwd(const __grid_constant__ BackwardArgs<T> a) {
-    __shared__ float aside[DL_LOGPROBS_MAX_TOP + 1];
+// 16 bytes from `shift` elements on in two neighbouring packs
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> shifted(const Pack<T, N>& p, const Pack<T, N>& q, int shift) {
+    const uint32_t* a = reinterpret_cast<const uint32_t*>(p.v);
+    const uint32_t* b = reinterpret_cast<const uint32_t*>(q.v);
+    uint32_t w[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    const int bytes = shift * static_cast<int>(sizeof(T));
+    if (bytes & 8) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (bytes & 4) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    if (bytes & 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    }
+    Pack<T, N> r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(r.v)[i] = w[i];
+    return r;
+}
+
+// A warp takes a chunk of a row: U packs per lane, cut where dlogits has its
+// 16-byte boundaries. Logits that lie otherwise on theirs (SHIFT) are read as
+// two packs each and shifted. Every logit's value is a factor of the row times
+// its probability; the few columns named by the token and the alternatives
+// get their own gradients on top, before the one rounding: a lane for each
+// computes that value aside and stores it after the chunk's packs.
+//
+// Bound by HBM: each logit is read once and written once.
+template <typename T, bool TOP, bool SHIFT>
+__global__ void __launch_bounds__(kThreads, TOP && !SHIFT ? 8 : 7) k_logprobs_bwd(const __grid_constant__ BackwardArgs<T> a) {
+    constexpr int N = 16 / sizeof(T), U = 8;
     using P = Pack<T, N>;
-    for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
-        const int64_t row = item / a.chunks;
+    const int lane = threadIdx.x % 32;
+    for (int64_t item = int64_t(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; item < a.items;
+         item += int64_t(gridDim.x) * (kThreads / 32)) {
+        const int64_t row = a.chunks == 1       ? item
+                            : a.items >> 32 == 0 ? static_cast<uint32_t>(item) / static_cast<uint32_t>(a.chunks)
+                                                 : item / a.chunks;
         const int chunk = static_cast<int>(item - row * a.chunks);
         const T* x = a.logits + row * a.stride;
         T* y = a.out + row * a.out_stride;
         const int64_t token = a.tokens ? token_at(a.tokens, a.token_type, row) : 0;
         const float g = a.d_logp ? a.d_logp[row] : 0.f, h = a.d_entropy ? a.d_entropy[row] : 0.f,
                     l = a.d_lse ? a.d_lse[row] : 0.f, log_sum = a.log_sum[row];
-        float named = 0.f;
-        bool any = g != 0.f || h != 0.f || l != 0.f;
-        for (int i = 0; i < a.n_top; ++i) {
-            const int64_t k = a.top_tokens[row * a.n_top + i];
-            const float q = a.d_top[row * a.n_top + i];
-            if (k >= 0 && k < a.vocab) {
-                named += q;
-                any = any || q != 0.f;
-            }
-        }
-        const bool zero = token < 0 || log_sum == -INFINITY || !any;
         Row r;
         r.m = a.row_max[row];
+        // this lane's alternative
+        int64_t mine = -1;
+        float q = 0.f, named = 0.f;
+        if constexpr (TOP) {
+            if (lane < a.n_top) {
+                mine = a.top_tokens[row * a.n_top + lane];
+                if (mine >= 0 && mine < a.vocab)
+                    q = a.d_top[row * a.n_top + lane];
+                else
+                    mine = -1;
+            }
+            named = q;
+#pragma unroll
+            for (int j = 16; j > 0; j /= 2) named += __shfl_xor_sync(kAll, named, j);
+        }
+        const bool any = g != 0.f || h != 0.f || l != 0.f || (TOP && __any_sync(kAll, q != 0.f));
+        const bool zero = token < 0 || log_sum == -INFINITY || !any;
         const float inverse = expf(-log_sum);
         r.c1 = -h * inverse;
         r.c0 = (l - g - named - (h != 0.f ? h * (a.entropy[row] - log_sum) : 0.f)) * inverse;
         if (g != 0.f && token >= a.vocab) r.c0 = NAN;
 
-        const int64_t skew = N == 1 ? 0 : static_cast<int64_t>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
-        const int64_t end = skew + a.vocab, first = (int64_t(chunk) * U * BLOCK + threadIdx.x) * N;
-        const T* xb = x - skew;
-        T* yb = y - skew;
-        // this thread's columns among the named ones (place: element from the boundary)
-        auto mine = [&](int64_t column) {
-            const int64_t pack = (column + skew) / N - int64_t(chunk) * U * BLOCK;
-            return pack >= 0 && pack < U * BLOCK && pack % BLOCK == threadIdx.x;
-        };
-        auto name = [&](int i) { return i == 0 ? (a.d_logp ? token : -1) : a.top_tokens[row * a.n_top + i - 1]; };
-        if (!zero)
-            for (int i = 0; i <= a.n_top; ++i) {
-                const int64_t k = name(i);
-                if (k < 0 || k >= a.vocab || !mine(k)) continue;
-                float more = 0.f;
-                for (int j = 0; j <= a.n_top; ++j)
-                    if (name(j) == k) more += j == 0 ? g : a.d_top[row * a.n_top + j - 1];
-                aside[i] = r.at(both(to_f32(x[k]))).x + more;
+        const RowPacks<T> out(y, a.vocab);
+        const int first = chunk * U * 32;
+        // [low, high): packs read and written whole. What is before and behind them, up to
+        // 2 N columns, is done element by element, a lane for each, by the row's first and last chunk.
+        P v[U];
+        const RowPacks<T> in(x, a.vocab);
+        int low = out.skew > 0, high = static_cast<int>(out.end / N);
+        if constexpr (SHIFT) {
+            // column p * N - out.skew is element p * N + in.skew - out.skew from x's boundary: the
+            // packs from there on, of which each lane reads one and takes the next from its neighbour
+            const int shift = in.skew - out.skew, back = shift < 0;
+            // packs that lie between the logits' first and last place
+            const int begin = in.base < a.logits;
+            const int end = in.packs - (in.base + int64_t(in.packs) * N > a.logits + (a.rows - 1) * a.stride + a.vocab);
+            low = max(low, begin + back), high = min(high, end - 1 + back);
+            P w[U + 1];
+#pragma unroll
+            for (int u = 0; u <= U; ++u) {
+                w[u] = filled<T, N>(0);
+                const int p = first - back + lane + u * 32;
+                if (p >= begin && p < (zero ? 0 : end) && (u < U || lane == 0))
+                    w[u] = reinterpret_cast<const P*>(in.base)[p];
             }
-        P q[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t at = first + int64_t(u) * BLOCK * N;
-            if (zero) {
+            for (int u = 0; u < U; ++u) {
+                P next;
 #pragma unroll
-                for (int i = 0; i < N; ++i) q[u].v[i] = from_f32<T>(0.f);
-            } else if (at >= skew && at + N <= end) {
-                q[u] = *reinterpret_cast<const P*>(xb + at);
-            } else {
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    q[u].v[i] = at + i >= skew && at + i < end ? xb[at + i] : from_f32<T>(0.f);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t at = first + int64_t(u) * BLOCK * N;
-            if (!zero) {
-                if constexpr (N == 1) {
-                    q[u].v[0] = from_f32<T>(r.at(both(to_f32(q[u].v[0]))).x);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < N / 2; ++i) {
-                        const float2 v = r.at(pair_of(&q[u], i));
-                        q[u].v[2 * i] = from_f32<T>(v.x), q[u].v[2 * i + 1] = from_f32<T>(v.y);
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t give = lane == 0 ? reinterpret_cast<const uint32_t*>(w[u + 1].v)[i]
+                                                    : reinterpret_cast<const uint32_t*>(w[u].v)[i];
+                    reinterpret_cast<uint32_t*>(next.v)[i] = __shfl_sync(kAll, give, (lane + 1) % 32);
                 }
+                v[u] = shifted(w[u], next, shift + back * N);
             }
-            if (at >= skew && at + N <= end) {
-                *reinterpret_cast<P*>(yb + at) = q[u];
-            } else {
+        } else {
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if (at + i >= skew && at + i < end) yb[at + i] = q[u].v[i];
+            for (int u = 0; u < U; ++u) {
+                v[u] = filled<T, N>(0);
+                const int p = first + u * 32 + lane;
+                if (p >= low && p < (zero ? 0 : high)) v[u] = reinterpret_cast<const P*>(in.base)[p];
             }
         }
-        if (!zero)
-            for (int i = 0; i <= a.n_top; ++i) {
-                const int64_t k = name(i);
-                if (k >= 0 && k < a.vocab && mine(k)) y[k] = from_f32<T>(aside[i]);
+        int64_t edge = -1;  // this lane's column of those
+        if (lane < 16) {
+            if (chunk == 0 && lane < low * N - out.skew) edge = lane;
+        } else if (chunk == a.chunks - 1) {
+            edge = int64_t(max(low, high)) * N - out.skew + lane - 16;
+        }
+        if (edge >= a.vocab) edge = -1;
+        const float at_edge = edge >= 0 && !zero ? to_f32(x[edge]) : 0.f;
+        // a named column of this chunk, and its value
+        auto within = [&](int64_t column) {
+            const int64_t pack = (column + out.skew) / N - first;
+            return column >= 0 && column < a.vocab && pack >= 0 && pack < U * 32;
+        };
+        const bool has_token = !zero && a.d_logp && within(token), has_top = TOP && !zero && within(mine);
+        float at_token = 0.f, at_top = 0.f;
+        if (has_token) {  // in every lane alike
+            float more = g;
+            if constexpr (TOP) {
+                float same = mine == token ? q : 0.f;
+#pragma unroll
+                for (int j = 16; j > 0; j /= 2) same += __shfl_xor_sync(kAll, same, j);
+                more += same;
             }
-        __syncthreads();  // the next item's threads write aside
+            at_token = r.at(both(to_f32(x[token]))).x + more;
+        }
+        if (TOP && __any_sync(kAll, has_top)) {
+            float more = a.d_logp && mine == token ? g : 0.f;
+            for (int i = 0; i < a.n_top; ++i) {
+                const int64_t other = __shfl_sync(kAll, mine, i);
+                const float its = __shfl_sync(kAll, q, i);
+                if (other == mine) more += its;
+            }
+            if (has_top) at_top = r.at(both(to_f32(x[mine]))).x + more;
+        }
+        if (a.logits == a.out) __syncwarp();  // named logits are read before their packs are written
+
+        if (!zero) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (first + u * 32 >= high) break;  // a short row
+                float2 f[N / 2];
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) f[i] = r.at(pair_of(&v[u], i));
+                v[u] = pack_of<T, N>(f);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int p = first + u * 32 + lane;
+            if (p >= low && p < high) reinterpret_cast<P*>(y - out.skew)[p] = v[u];
+        }
+        if (edge >= 0) y[edge] = from_f32<T>(zero ? 0.f : r.at(both(at_edge)).x);
+        if (has_token || (TOP && __any_sync(kAll, has_top))) {
+            __syncwarp();
+            if (has_top) y[mine] = from_f32<T>(at_top);
+            if (has_token && lane == 0) y[token] = from_f32<T>(at_token);
+        }
     }
 }
 
-template <typename T, int N, int BLOCK, int U>
+template <typename T, bool TOP, bool SHIFT>
 int launch(BackwardArgs<T> a, cudaStream_t s) {
-    const int64_t per = int64_t(BLOCK) * U * N;
-    a.chunks = static_cast<int32_t>((int64_t(a.vocab) + (N - 1) + per - 1) / per);
+    constexpr int N = 16 / sizeof(T), kPer = 32 * 8;
+    a.chunks = static_cast<int32_t>(((int64_t(a.vocab) + 2 * N - 2) / N + kPer - 1) / kPer);
     if (a.rows > INT64_MAX / a.chunks) return DL_ERR_ARG;
     a.items = a.rows * a.chunks;
-    k_logprobs_bwd<T, N, BLOCK, U><<<static_cast<unsigned>(a.items < INT32_MAX ? a.items : INT32_MAX), BLOCK, 0, s>>>(a);
+    const int64_t blocks = (a.items + kThreads / 32 - 1) / (kThreads / 32);
+    k_logprobs_bwd<T, TOP, SHIFT><<<static_cast<unsigned>(blocks < INT32_MAX ? blocks : INT32_MAX), kThreads, 0, s>>>(a);
     return launch_status();
 }
 
 template <typename T>
 int backward(const BackwardArgs<T>& a, cudaStream_t s) {
     constexpr int N = 16 / sizeof(T);
-    // packs need every row of dlogits to lie on its 16-byte boundary as its logits do
+    // every row of dlogits lies on its 16-byte boundary as its logits do
     const bool alike = (reinterpret_cast<uintptr_t>(a.logits) - reinterpret_cast<uintptr_t>(a.out)) % 16 == 0 &&
                        (a.rows == 1 || (a.stride - a.out_stride) % N == 0);
-    return alike ? launch<T, N, 256, 8>(a, s) : launch<T, 1, 256, 8>(a, s);
+    if (a.n_top) return alike ? launch<T, true, false>(a, s) : launch<T, true, true>(a, s);
+    return alike ? launch<T, false, false>(a, s) : launch<T, false, true>(a, s);
 }
 
 }  // namespace
