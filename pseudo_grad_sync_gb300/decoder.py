@@ -113,23 +113,32 @@ class RotaryFrequencies:
         self.device = self.turns.device
 
 
-def _heads(t, name, like=None):
-    """(dimensions, strides) of [batch][tokens][heads][head_dim]; a tensor of
-    three dimensions has a batch of one."""
+def _refuse_heads(t, name, like):
+    """The error of a tensor that _heads does not take."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dtype not in _TYPE or (like is not None and t.dtype is not like.dtype):
-        want = like.dtype if like is not None else "float32, bfloat16 or float16"
+    if t.dtype not in _TYPE or t.dtype is not like.dtype:
+        want = like.dtype if like is not t else "float32, bfloat16 or float16"
         raise TypeError(f"{name}: dtype {t.dtype}, expected {want}")
-    shape, stride = t.shape, t.stride()
-    if len(shape) == 3:
-        shape, stride = (1, *shape), (0, *stride)
-    elif len(shape) != 4:
-        raise ValueError(f"{name}: {len(shape)} dimensions, expected [batch, tokens, heads, "
+    if t.dim() not in (3, 4):
+        raise ValueError(f"{name}: {t.dim()} dimensions, expected [batch, tokens, heads, "
                          "head_dim] or [tokens, heads, head_dim]")
-    if stride[3] != 1 and shape[3] > 1:
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return shape, stride
+    raise ValueError(f"{name}: shape {tuple(t.shape)} does not go with {tuple(like.shape)}")
+
+
+def _heads(t, name, i, like, shape):
+    """Strides (batch, token, head) of [batch][tokens][heads][head_dim], which
+    must go with `like` of that shape; a tensor of three dimensions has a batch
+    of one. name and i name it where it does not."""
+    if isinstance(t, torch.Tensor) and t.dtype is like.dtype and t.dtype in _TYPE:
+        d, s = t.shape, t.stride()
+        n = len(d)
+        if (n == len(shape) and 3 <= n <= 4 and (s[-1] == 1 or d[-1] == 1) and d[-1] == shape[-1]
+                and d[-3] == shape[-3] and (n == 3 or d[0] == shape[0])):
+            return s if n == 4 else (0, *s)
+    _refuse_heads(t, f"{name}[{i}]", like)
 
 
 def _positions(positions, batch, tokens):
@@ -165,44 +174,52 @@ def rotary_apply(xs, frequencies, positions=None, first=0, interleaved=False, in
     xs = (xs,) if single else tuple(xs)
     if not 1 <= len(xs) <= DL_ROTARY_MAX_JOBS:
         raise ValueError(f"xs: {len(xs)} tensors, expected 1 to {DL_ROTARY_MAX_JOBS}")
-    shape, _ = _heads(xs[0], "xs[0]")
-    device = xs[0].device
+    x0 = xs[0]
+    if not isinstance(x0, torch.Tensor):
+        _refuse_heads(x0, "xs[0]", x0)
+    device = x0.device
     if stream is not None:
         with torch.cuda.stream(_stream_of(stream, device)):
-            return rotary_apply(xs[0] if single else xs, frequencies, positions, first, interleaved,
+            return rotary_apply(x0 if single else xs, frequencies, positions, first, interleaved,
                                 inverse, out)
-    at = xs[0].get_device()
+    at = x0.get_device()
     if _away(at):
         with torch.cuda.device(device):
-            return rotary_apply(xs[0] if single else xs, frequencies, positions, first, interleaved,
+            return rotary_apply(x0 if single else xs, frequencies, positions, first, interleaved,
                                 inverse, out)
     if not isinstance(frequencies, RotaryFrequencies):
         raise TypeError(f"frequencies: expected RotaryFrequencies, got {type(frequencies).__name__}")
-    batch, tokens, _, width = shape
-    if width < frequencies.dim:
-        raise ValueError(f"xs[0]: heads of {width} elements, frequencies rotate {frequencies.dim}")
-    _int32(width, "head_dim")
+    shape = x0.shape
+    n = len(xs)
     if out is None:
-        ys = tuple([torch.empty_like(x) for x in xs])
+        ys = None
     else:
         ys = (out,) if isinstance(out, torch.Tensor) else tuple(out)
-        if len(ys) != len(xs):
-            raise ValueError(f"out: {len(ys)} tensors for {len(xs)}")
-    jobs = (_RotaryJob * len(xs))()
-    here = frequencies.turns.get_device() == at
-    for i, (x, y) in enumerate(zip(xs, ys)):
-        xd, xt = _heads(x, f"xs[{i}]", xs[0])
-        yd, yt = _heads(y, f"out[{i}]", x)
-        if y.shape != x.shape:
-            raise ValueError(f"out[{i}]: shape {tuple(y.shape)}, expected {tuple(x.shape)}")
-        if xd[0] != batch or xd[1] != tokens or xd[3] != width or x.dim() != xs[0].dim():
-            raise ValueError(f"xs[{i}]: shape {tuple(x.shape)} does not go with "
-                             f"{tuple(xs[0].shape)}")
+        if len(ys) != n:
+            raise ValueError(f"out: {len(ys)} tensors for {n}")
+    jobs = (_RotaryJob * n)()
+    turns = frequencies.turns
+    here = turns.get_device() == at >= 0
+    given = []
+    for i, x in enumerate(xs):
         j = jobs[i]
-        j.x, j.y, j.heads = x.data_ptr(), y.data_ptr(), _int32(xd[2], "heads")
-        j.x_batch, j.x_token, j.x_head = xt[0], xt[1], xt[2]
-        j.y_batch, j.y_token, j.y_head = yt[0], yt[1], yt[2]
+        j.x_batch, j.x_token, j.x_head = _heads(x, "xs", i, x0, shape)[:3]
+        j.x, j.heads = x.data_ptr(), _int32(x.shape[-2], "heads")
+        if ys is None:
+            y = torch.empty_like(x)
+            j.y_batch, j.y_token, j.y_head = y.stride()[:3] if len(shape) == 4 else (0, *y.stride()[:2])
+        else:
+            y = ys[i]
+            if isinstance(y, torch.Tensor) and y.shape != x.shape:
+                raise ValueError(f"out[{i}]: shape {tuple(y.shape)}, expected {tuple(x.shape)}")
+            j.y_batch, j.y_token, j.y_head = _heads(y, "out", i, x0, shape)[:3]
+        j.y = y.data_ptr()
+        given.append(y)
         here = here and x.get_device() == at and y.get_device() == at
+    ys = tuple(given)
+    batch, tokens, width = shape[0] if len(shape) == 4 else 1, shape[-3], _int32(shape[-1], "head_dim")
+    if width < frequencies.dim:
+        raise ValueError(f"xs[0]: heads of {width} elements, frequencies rotate {frequencies.dim}")
     pp, ptype, pstride = None, DL_I64, 0
     if positions is not None:
         positions, ptype, pstride = _positions(positions, batch, tokens)
@@ -210,14 +227,13 @@ def rotary_apply(xs, frequencies, positions=None, first=0, interleaved=False, in
         here = here and positions.get_device() == at
     elif not -2**63 <= first < 2**63:
         raise ValueError(f"first: {first} does not fit 64 bits")
-    if at < 0 or not here:
-        _cuda(*xs, *ys, frequencies.turns, positions)
-        _one_device(*xs, *ys, frequencies.turns, positions)
+    if not here:
+        _cuda(*xs, *ys, turns, positions)
+        _one_device(*xs, *ys, turns, positions)
     flags = (DL_ROTARY_INTERLEAVED if interleaved else 0) | (DL_ROTARY_INVERSE if inverse else 0)
-    st = lib().dl_rotary_apply(jobs, len(xs), _TYPE[xs[0].dtype], batch, tokens, width,
-                               frequencies.dim, frequencies.turns.data_ptr(),
-                               frequencies.amplitude, pp, ptype, pstride, first, flags,
-                               _on(None, device))
+    st = lib().dl_rotary_apply(jobs, n, _TYPE[x0.dtype], batch, tokens, width, frequencies.dim,
+                               turns.data_ptr(), frequencies.amplitude, pp, ptype, pstride, first,
+                               flags, _on(None, device))
     if st:
         raise DLError("dl_rotary_apply", st)
     return ys[0] if single else ys
@@ -343,11 +359,10 @@ def logprobs_forward(logits, tokens=None, top=0, entropy=False, stream=None):
             tokens = tokens.contiguous()
     _all_on(at, logits, tokens)
     # tensors of their own: a caller may change one in place
-    values = [torch.empty(lead, dtype=torch.float32, device=device)
-              for _ in range(3 + (tokens is not None) + bool(entropy))]
-    lse, row_max, log_sum = values[:3]
-    logp = values[3] if tokens is not None else None
-    h = values[-1] if entropy else None
+    lse = torch.empty(lead, dtype=torch.float32, device=device)
+    row_max, log_sum = torch.empty_like(lse), torch.empty_like(lse)
+    logp = torch.empty_like(lse) if tokens is not None else None
+    h = torch.empty_like(lse) if entropy else None
     top_tokens = top_logp = None
     if top:
         top_tokens = torch.empty((*lead, top), dtype=torch.int64, device=device)
