@@ -210,8 +210,8 @@ struct Geometry {
 //
 // The n_top-th largest of the threads' maxima is a bound that no alternative
 // lies below, and (ties aside) n_top threads and hardly more slots have a
-// logit that reaches it. (Of eight warps' maxima the two largest of every lane
-// are taken for all: a bound hardly lower, for a quarter of the sorting.) Their packs alone are read again; what reaches the
+// logit that reaches it. (Of several warps' maxima the two largest of every
+// lane are taken for all: a bound hardly lower, for a part of the sorting.) Their packs alone are read again; what reaches the
 // bound is collected, and sorted in runs of 32. One warp's instructions are
 // what this costs: every step leaves the next one little to look at.
 template <typename T, int TPR, int U, int WARPS, typename S>
@@ -280,6 +280,7 @@ __device__ __forceinline__ uint64_t alternatives(const S& mine, const float (&mo
             copy_wait<0>();
 #pragma unroll
             for (int r = 0; r < kRead; ++r) {
+                if (first + 32 * r >= places * packs) break;
                 bool any = false;
                 if (pack[r] < mine.end) {
                     const P q[1] = {mine.packs.whole(pack[r]) ? *reinterpret_cast<const P*>(&own.again[r][lane])
@@ -327,17 +328,17 @@ __device__ __forceinline__ uint64_t alternatives(const S& mine, const float (&mo
     return found;
 }
 
-// TPR threads per row: a warp (four rows to a block), or eight, or with CLUSTER
-// eight in each block of a cluster. Every thread keeps the running maximum and
+// TPR threads per row: a warp (four rows to a block), or a block's, or with
+// CLUSTER those of a cluster's blocks. Every thread keeps the running maximum and
 // sums of its packs and a warp joins its lanes'.
 //
 // Packs come in by asynchronous copies into a ring that each thread has to
-// itself, kStages - 1 stages ahead and on into the next rows. Where eight warps
-// share a row a ninth one joins their parts, finds the alternatives and
+// itself, kStages - 1 stages ahead and on into the next rows. Where a block's
+// warps share a row one more joins their parts, finds the alternatives and
 // writes the outputs while they are at the next row; one barrier per row
 // hands over.
 template <typename T, int TPR, bool ENTROPY, bool TOP, bool CLUSTER>
-__global__ void __launch_bounds__(Geometry<T, TPR>::kBlock, TPR == 32 ? 6 : 3)
+__global__ void __launch_bounds__(Geometry<T, TPR>::kBlock, TPR == 32 ? 6 : TPR == 128 ? 5 : 3)
     k_logprobs(const __grid_constant__ ForwardArgs<T> a) {
     using Geo = Geometry<T, TPR>;
     constexpr int N = 16 / sizeof(T), U = Geo::U, kWarps = Geo::kWarps, kAhead = Geo::kStages - 1;
@@ -601,16 +602,22 @@ int launch(const ForwardArgs<T>& a, int ranks, cudaStream_t s) {
                    : launch<T, TPR, false, false, CLUSTER>(a, ranks, s);
 }
 
+// A warp per row while that leaves it less than 64 packs per lane and there
+// are rows for every warp (65536 x 4096 bf16 109 us, 331 with a block of eight
+// warps; 16384 x 32000 168, with a block of four 161); few rows by clusters of
+// up to eight blocks of eight warps, while there are SMs for them and the
+// shares fill a block (64 x 128256: 8.0 us, with one block each 19); else a
+// block of four warps (eight: 16384 x 32000 185 us, 8192 x 128256 291 for 297,
+// with entropy and 20 alternatives 388 for 376).
 template <typename T>
 int forward(const ForwardArgs<T>& a, cudaStream_t s) {
     constexpr int N = 16 / sizeof(T);
     const int64_t packs = a.vocab / N;
-    if (packs <= 4096 && (packs <= 256 || a.rows >= 4096)) return launch<T, 32, false>(a, 1, s);
-    // few rows: a cluster for each, while there are SMs for it and the shares fill a block
+    if (packs <= 2048 && (packs <= 256 || a.rows >= 4096)) return launch<T, 32, false>(a, 1, s);
     int ranks = 1;
     while (ranks < 8 && a.rows * ranks * 2 <= 2 * sm_count() && packs / (ranks * 2) >= 256) ranks *= 2;
     if (ranks > 1) return launch<T, 256, true>(a, ranks, s);
-    return launch<T, 256, false>(a, 1, s);
+    return launch<T, 128, false>(a, 1, s);
 }
 
 }  // namespace

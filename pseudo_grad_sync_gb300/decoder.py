@@ -274,15 +274,22 @@ def rotary(xs, frequencies, positions=None, first=0, interleaved=False):
 
 
 class LogProbs(NamedTuple):
-    """What logprobs_forward computed; None for what was not asked for. row_max
-    and log_sum are the statistics that logprobs_backward takes."""
+    """What logprobs_forward computed; None for what was not asked for.
+    statistics: [2, ...], the rows' row_max and log_sum for logprobs_backward."""
     logp: Optional[torch.Tensor]
     lse: torch.Tensor
     entropy: Optional[torch.Tensor]
     top_tokens: Optional[torch.Tensor]
     top_logp: Optional[torch.Tensor]
-    row_max: torch.Tensor
-    log_sum: torch.Tensor
+    statistics: torch.Tensor
+
+    @property
+    def row_max(self):
+        return self.statistics[0]
+
+    @property
+    def log_sum(self):
+        return self.statistics[1]
 
 
 class TokenLogProbs(NamedTuple):
@@ -358,9 +365,10 @@ def logprobs_forward(logits, tokens=None, top=0, entropy=False, stream=None):
         if not tokens.is_contiguous():
             tokens = tokens.contiguous()
     _all_on(at, logits, tokens)
-    # tensors of their own: a caller may change one in place
     lse = torch.empty(lead, dtype=torch.float32, device=device)
-    row_max, log_sum = torch.empty_like(lse), torch.empty_like(lse)
+    # both statistics in one allocation; what a caller may change in place has its own
+    statistics = torch.empty((2, *lead), dtype=torch.float32, device=device)
+    sp = statistics.data_ptr()
     logp = torch.empty_like(lse) if tokens is not None else None
     h = torch.empty_like(lse) if entropy else None
     top_tokens = top_logp = None
@@ -369,11 +377,10 @@ def logprobs_forward(logits, tokens=None, top=0, entropy=False, stream=None):
         top_logp = torch.empty((*lead, top), dtype=torch.float32, device=device)
     st = lib().dl_logprobs_forward(zp, zs, _TYPE[logits.dtype], rows, vocab, _at(tokens), ttype,
                                    _at(logp), _at(h), lse.data_ptr(), top, _at(top_tokens),
-                                   _at(top_logp), row_max.data_ptr(), log_sum.data_ptr(),
-                                   _on(None, device))
+                                   _at(top_logp), sp, sp + 4 * rows, _on(None, device))
     if st:
         raise DLError("dl_logprobs_forward", st)
-    return LogProbs(logp, lse, h, top_tokens, top_logp, row_max, log_sum)
+    return LogProbs(logp, lse, h, top_tokens, top_logp, statistics)
 
 
 def logprobs_backward(logits, tokens, row_max, log_sum, d_logp=None, d_entropy=None, d_lse=None,
@@ -453,19 +460,19 @@ class _TokenLogProbs(torch.autograd.Function):
     def forward(ctx, logits, tokens, top, entropy):
         r = logprobs_forward(logits, tokens, top, entropy)
         ctx.set_materialize_grads(False)
-        ctx.save_for_backward(logits, tokens, r.row_max, r.log_sum, r.entropy, r.top_tokens)
+        ctx.save_for_backward(logits, tokens, r.statistics, r.entropy, r.top_tokens)
         if top:
             ctx.mark_non_differentiable(r.top_tokens)
         return r.logp, r.lse, r.entropy, r.top_tokens, r.top_logp
 
     @staticmethod
     def backward(ctx, d_logp, d_lse, d_entropy, _, d_top):
-        logits, tokens, row_max, log_sum, entropy, top_tokens = ctx.saved_tensors
+        logits, tokens, statistics, entropy, top_tokens = ctx.saved_tensors
         # broadcast gradients (as of a mean) have one value for every row
         d_logp, d_lse, d_entropy, d_top = (
             None if d is None else d.contiguous() for d in (d_logp, d_lse, d_entropy, d_top))
-        args = (logits, tokens, row_max, log_sum, d_logp, d_entropy, d_lse, entropy, top_tokens,
-                d_top)
+        args = (logits, tokens, *statistics.unbind(0), d_logp, d_entropy, d_lse, entropy,
+                top_tokens, d_top)
         if torch.is_grad_enabled():
             dz = _TokenLogProbsGradient.apply(*args)
         else:

@@ -263,7 +263,7 @@ def formulas(monkeypatch):
         with torch.no_grad():
             w = ref.logprobs(logits, tokens, top)
             return dl.LogProbs(w.get("logp"), w["lse"], w["entropy"] if entropy else None, w.get("top_tokens"),
-                               w.get("top_logp"), w["row_max"], w["log_sum"])
+                               w.get("top_logp"), torch.stack([w["row_max"], w["log_sum"]]))
 
     def backward(logits, tokens, row_max, log_sum, d_logp=None, d_entropy=None, d_lse=None, entropy=None,
                  top_tokens=None, d_top=None, **kw):
