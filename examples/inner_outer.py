@@ -1,14 +1,17 @@
 """DiLoCo on one GPU: K learners take inner steps, then one outer step merges them.
 
 Every learner trains its own copy of a small residual model (embedding, blocks of
-layer norm and MLP, final norm, output layer) on its own synthetic data. The inner
-step is the library's: layer norms forward and backward, clipping by the global
-gradient norm, AdamW over the learner's flat fragments with 8- or 32-bit states.
+layer norm and MLP, with --attention also of causal attention on rotary queries and
+keys, final norm, output layer) on its own synthetic data. The inner step is the
+library's: layer norms, rotary positions and the tokens' log probabilities forward and
+backward, clipping by the global gradient norm, AdamW over the learner's flat fragments
+with 8- or 32-bit states.
 After H of them the outer step quantises the learners' pseudo-gradients, merges them
 and applies the outer Nesterov update to the global parameters, from which the
 learners go on.
 
     python examples/inner_outer.py [--learners 3] [--rounds 5] [--inner 20] [--bits 8]
+                                   [--attention]
 
 The memory layout is what makes the two halves meet without a copy: a learner's fp32
 parameters are one flat buffer per fragment; the model's bf16 weights are views into
@@ -25,32 +28,54 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import pseudo_grad_sync_gb300 as dl  # noqa: E402
 
 VOCAB, WIDTH, HIDDEN, BLOCKS = 512, 192, 512, 3
+TOKENS, SEQ = 512, 64                 # of an inner step; of a sequence
+HEADS, KV_HEADS, HEAD = 4, 2, 48      # of the attention: query heads, key and value heads
 
 
-def shapes():
+def shapes(attention=False):
     """name -> shape of every tensor of the model, in order."""
     out = {"embed": (VOCAB, WIDTH)}
     for i in range(BLOCKS):
+        if attention:
+            out |= {f"{i}.att_norm.w": (WIDTH,), f"{i}.qkv": ((HEADS + 2 * KV_HEADS) * HEAD, WIDTH),
+                    f"{i}.att_out": (WIDTH, HEADS * HEAD)}
         out |= {f"{i}.norm.w": (WIDTH,), f"{i}.norm.b": (WIDTH,), f"{i}.up": (HIDDEN, WIDTH),
                 f"{i}.down": (WIDTH, HIDDEN)}
     return out | {"norm.w": (WIDTH,), "out": (VOCAB, WIDTH)}
 
 
-def loss_of(p, tokens, targets):
+def attend(x, p, i, rotary):
+    """Causal attention of sequences of SEQ tokens, on rotary queries and keys."""
+    h = dl.layer_norm(x, p[f"{i}.att_norm.w"], rms=True)
+    qkv = (h @ p[f"{i}.qkv"].t()).view(-1, SEQ, HEADS + 2 * KV_HEADS, HEAD)
+    q, k, v = qkv.split([HEADS, KV_HEADS, KV_HEADS], 2)
+    q, k = dl.rotary((q, k), rotary)
+    k, v = (t.repeat_interleave(HEADS // KV_HEADS, 2) for t in (k, v))
+    a = torch.einsum("bshd,bthd->bhst", q, k).float() * HEAD ** -0.5
+    later = torch.ones(SEQ, SEQ, dtype=torch.bool, device=x.device).triu(1)
+    a = a.masked_fill(later, float("-inf")).softmax(-1).to(v.dtype)
+    y = torch.einsum("bhst,bthd->bshd", a, v).reshape(len(x), -1)
+    return y @ p[f"{i}.att_out"].t()
+
+
+def loss_of(p, tokens, targets, rotary=None):
     x = p["embed"][tokens]
     for i in range(BLOCKS):
+        if rotary is not None:
+            x = x + attend(x, p, i, rotary)
         h = dl.layer_norm(x, p[f"{i}.norm.w"], p[f"{i}.norm.b"])
         x = x + torch.nn.functional.gelu(h @ p[f"{i}.up"].t()) @ p[f"{i}.down"].t()
     h = dl.layer_norm(x, p["norm.w"], rms=True)
-    return torch.nn.functional.cross_entropy((h @ p["out"].t()).float(), targets)
+    return -dl.token_logprobs(h @ p["out"].t(), targets).logp.mean()
 
 
 class Learner:
     """A replica: flat buffers per fragment, the model's views into them, and
     its inner optimiser."""
 
-    def __init__(self, frags, names, theta_g, bits, seed):
-        sh = shapes()
+    def __init__(self, frags, names, theta_g, bits, seed, attention=False):
+        sh = shapes(attention)
+        self.rotary = dl.RotaryFrequencies(HEAD) if attention else None
         self.theta = [t.clone() for t in theta_g]
         self.copy = [t.to(torch.bfloat16) for t in self.theta]
         self.grad = [torch.zeros_like(c) for c in self.copy]
@@ -68,7 +93,7 @@ class Learner:
     def inner_step(self, tokens, targets):
         for g in self.grad:
             g.zero_()
-        loss = loss_of(self.p, tokens, targets)
+        loss = loss_of(self.p, tokens, targets, self.rotary)
         loss.backward()
         self.opt.step()
         return loss.detach()
@@ -87,9 +112,10 @@ def main(argv=None):
     ap.add_argument("--inner", type=int, default=20, help="inner steps per outer step")
     ap.add_argument("--bits", type=int, default=8, choices=(8, 32), help="AdamW state width")
     ap.add_argument("--fragments", type=int, default=2)
+    ap.add_argument("--attention", action="store_true", help="blocks with rotary attention")
     a = ap.parse_args(argv)
     torch.manual_seed(0)
-    sh = shapes()
+    sh = shapes(a.attention)
     order = list(sh)
     numel = [torch.Size(sh[n]).numel() for n in order]
     of, _ = dl.plan_fragments(numel, a.fragments)
@@ -102,7 +128,7 @@ def main(argv=None):
                  if n.endswith("norm.b") else torch.randn(sh[n]) * 0.05 for n in f]
         theta_g.append(torch.cat([t.reshape(-1) for t in parts]).cuda())
     momentum = [torch.zeros_like(t) for t in theta_g]
-    learners = [Learner(frags, names, theta_g, a.bits, seed=k) for k in range(a.learners)]
+    learners = [Learner(frags, names, theta_g, a.bits, k, a.attention) for k in range(a.learners)]
     sync = dl.ModelSync(frags, a.learners)
 
     table = torch.randperm(VOCAB).cuda()      # the task: token -> its partner
@@ -112,7 +138,7 @@ def main(argv=None):
         total = torch.zeros((), device="cuda")
         for L in learners:
             for _ in range(a.inner):
-                tokens = torch.randint(0, VOCAB, (512,), generator=data, device="cuda")
+                tokens = torch.randint(0, VOCAB, (TOKENS,), generator=data, device="cuda")
                 total += L.inner_step(tokens, table[tokens])
         sync.step(theta_g, momentum, [[L.theta[j] for L in learners] for j in range(len(frags))])
         for L in learners:

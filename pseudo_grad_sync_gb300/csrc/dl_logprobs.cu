@@ -267,6 +267,7 @@ __device__ __forceinline__ uint64_t alternatives(const S& mine, const float (&mo
 #pragma unroll
             for (int r = 0; r < kRead; ++r) {
                 pack[r] = mine.end;
+                if (first + 32 * r >= places * packs) continue;
                 if (which < places) {
                     const int place = own.place[which];
                     pack[r] = mine.begin + ((place >> 16) * packs + at) * TPR + (place & 0xffff);
@@ -615,7 +616,7 @@ int forward(const ForwardArgs<T>& a, cudaStream_t s) {
     const int64_t packs = a.vocab / N;
     if (packs <= 2048 && (packs <= 256 || a.rows >= 4096)) return launch<T, 32, false>(a, 1, s);
     int ranks = 1;
-    while (ranks < 8 && a.rows * ranks * 2 <= 2 * sm_count() && packs / (ranks * 2) >= 256) ranks *= 2;
+    while (ranks < 8 && a.rows * ranks * 2 <= 3 * sm_count() && packs / (ranks * 2) >= 256) ranks *= 2;
     if (ranks > 1) return launch<T, 256, true>(a, ranks, s);
     return launch<T, 128, false>(a, 1, s);
 }

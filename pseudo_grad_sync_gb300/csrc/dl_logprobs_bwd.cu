@@ -154,14 +154,17 @@ __global__ void __launch_bounds__(kThreads, TOP && !SHIFT ? 8 : 7) k_logprobs_bw
         if (lane < 16) {
             if (chunk == 0 && lane < low * N - out.skew) edge = lane;
         } else if (chunk == a.chunks - 1) {
-            edge = int64_t(max(low, high)) * N - out.skew + lane - 16;
+            edge = int64_t(max(low, high)) * N - out.skew + lane - 16;  // behind the last of them
         }
         if (edge >= a.vocab) edge = -1;
         const float at_edge = edge >= 0 && !zero ? to_f32(x[edge]) : 0.f;
-        // a named column of this chunk, and its value
+        // a named column is its pack's chunk's; behind the last whole pack the last chunk's, as its edge is
+        const int64_t behind = int64_t(max(low, high)) * N - out.skew;
         auto within = [&](int64_t column) {
+            if (column < 0 || column >= a.vocab) return false;
+            if (column >= behind) return chunk == a.chunks - 1;
             const int64_t pack = (column + out.skew) / N - first;
-            return column >= 0 && column < a.vocab && pack >= 0 && pack < U * 32;
+            return pack >= 0 && pack < U * 32;
         };
         const bool has_token = !zero && a.d_logp && within(token), has_top = TOP && !zero && within(mine);
         float at_token = 0.f, at_top = 0.f;

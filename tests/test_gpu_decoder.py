@@ -2,11 +2,14 @@
 
 Tolerances are worst-case bounds of the operators' fp32 arithmetic (u = 2^-24
 is half a unit in the last place), per element; tokens are compared exactly."""
+import importlib.util
 import math
+import os
 
 import pytest
 
 import decoder_ref as ref
+from conftest import ROOT
 
 pytestmark = pytest.mark.gpu
 
@@ -400,6 +403,28 @@ def test_logprobs_named_twice(dl):
     near(got, want, 16 * U * size + U * want.abs() + TINY["f32"])
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab", list(range(1018, 1031)) + [1, 2, 3, 6, 9, 15, 2047, 2048, 2049, 2056, 4099])
+def test_logprobs_named_at_the_edges(dl, kind, vocab):
+    """Tokens and alternatives at both ends of rows of every alignment, where a
+    row's chunks and its 16-byte packs end; dlogits aligned as the logits and
+    otherwise."""
+    rows = 34
+    for pad, opad in ((0, 0), (1, 0), (0, 3), (8, 8)):
+        z = logits_of(rows, vocab, kind, vocab, pad=pad)
+        near_ends = torch.arange(rows, device="cuda") // 2 % vocab
+        tokens = torch.where(torch.arange(rows, device="cuda") % 2 == 0, near_ends, vocab - 1 - near_ends)
+        r = dl.logprobs_forward(z, tokens, top=1)
+        named = torch.stack([vocab - 1 - near_ends, near_ends, tokens, near_ends * 0, near_ends * 0 + vocab - 1], 1)
+        g, q = randn((rows,), 3), randn((rows, 5), 4)
+        for d_top in (None, q):
+            out = torch.empty((rows, vocab + opad), device="cuda", dtype=TYPES[kind])[:, :vocab]
+            args = dict(top_tokens=named if d_top is not None else None, d_top=d_top)
+            want, size = ref.dlogits(z, tokens, r.row_max, r.log_sum, g, **args)
+            dl.logprobs_backward(z, tokens, r.row_max, r.log_sum, g, out=out, **args)
+            near(out, want, 16 * U * size + UT[kind] * want.abs() + 64 * TINY[kind], (pad, opad))
+
+
 def test_logprobs_shapes(dl):
     z = logits_of(12, 100, "bf16", 1).view(3, 4, 100)
     t = tokens_of(12, 100, 2).view(3, 4)
@@ -574,6 +599,24 @@ def test_decoder_step(dl):
     assert abs(float(loss) - float(want_loss)) <= 2000 * U * abs(float(want_loss))
     for n, a, b in zip(p, got, want):
         assert float((a.double() - b).norm()) <= 2000 * U * float(b.norm()), n
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_example_with_attention(dl, bits):
+    """examples/inner_outer.py with rotary attention: it runs, its losses are
+    numbers, and every parameter has a gradient."""
+    spec = importlib.util.spec_from_file_location(
+        "inner_outer", os.path.join(ROOT, "examples", "inner_outer.py"))
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    losses = example.main(["--learners", "2", "--rounds", "1", "--inner", "2", "--bits", str(bits),
+                           "--attention"])
+    assert all(math.isfinite(v) for v in losses)
+    p = {n: (torch.randn(s, generator=gen(i), device="cuda") * 0.05 + ("norm.w" in n)).requires_grad_()
+         for i, (n, s) in enumerate(example.shapes(True).items())}
+    tokens = tokens_of(2 * example.SEQ, example.VOCAB, 1)
+    example.loss_of(p, tokens, tokens.flip(0), dl.RotaryFrequencies(example.HEAD)).backward()
+    assert all(float(v.grad.abs().sum()) > 0 for v in p.values())
 
 
 # ----------------------------------------------------------------------------
