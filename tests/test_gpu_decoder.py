@@ -285,14 +285,15 @@ def test_logprobs(dl, kind, rows, vocab):
 @pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("vocab", [5, 63, 1000, 32003])
 def test_logprobs_strides_and_alignment(dl, kind, vocab):
-    """Rows inside wider ones, at every offset; what lies between stays as it was."""
+    """Rows inside wider ones, at every offset, NaN between them; what lies
+    between stays as it was."""
     rows = 6
     tokens = tokens_of(rows, vocab, 2)
     whole = logits_of(rows, vocab, kind, 3)
     want = dl.logprobs_forward(whole, tokens, top=4, entropy=True)
     grad = check_backward(dl, whole, tokens, want, kind, 4, 4, True)
     for pad, off in ((1, 0), (3, 1), (8, 3), (8, 8), (16, 5)):
-        room = torch.full((rows, vocab + pad), 9.0, device="cuda", dtype=TYPES[kind])
+        room = torch.full((rows, vocab + pad), math.nan, device="cuda", dtype=TYPES[kind])
         z = room[:, min(off, pad):min(off, pad) + vocab]
         z.copy_(whole)
         r = dl.logprobs_forward(z, tokens, top=4, entropy=True)
@@ -317,7 +318,7 @@ def test_logprobs_strides_and_alignment(dl, kind, vocab):
         if here is z:
             rest = torch.ones(vocab + pad, dtype=torch.bool)
             rest[min(off, pad):min(off, pad) + vocab] = False
-            assert bool((room[:, rest.cuda()] == 9).all())
+            assert bool(torch.isnan(room[:, rest.cuda()]).all())
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
@@ -389,6 +390,8 @@ def test_logprobs_alternatives(dl, kind, order):
     for top in (1, 20, 32):
         r = dl.logprobs_forward(z, None, top=top)
         check_logprobs(r, z, None, top, False)
+        again = dl.logprobs_forward(z, None, top=top)
+        assert torch.equal(r.top_tokens, again.top_tokens) and torch.equal(r.lse, again.lse)
 
 
 def test_logprobs_named_twice(dl):
@@ -458,6 +461,30 @@ def test_logprobs_long(dl):
     near(got[few], want, 16 * U * size + UT["bf16"] * want.abs() + 64 * TINY["bf16"])
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_logprobs_widest(dl, kind):
+    """A row of 2^31 - 1 columns, all masked but seven."""
+    vocab = 2**31 - 1
+    z = torch.full((1, vocab), -INF, device="cuda", dtype=TYPES[kind])
+    at = torch.tensor([0, 1, 7, 2**30 + 3, 2**31 - 9, 2**31 - 3, vocab - 1], device="cuda")
+    v = torch.tensor([1.0, -2.0, 3.0, 0.5, 3.0, 2.0, -1.0], device="cuda")
+    z[0, at] = v.to(z.dtype)
+    tokens = at[-1:]
+    r = dl.logprobs_forward(z, tokens, top=9, entropy=True)
+    lp = torch.log_softmax(v.double(), 0)
+    order = torch.sort(v, descending=True, stable=True).indices
+    assert r.top_tokens[0].tolist() == at[order].tolist() + [-1, -1]
+    near(r.top_logp[0, :7], lp[order], sum_tol(4.0) + 16 * U)
+    near(r.logp[0], lp[-1], sum_tol(4.0) + 16 * U)
+    near(r.entropy[0], -(lp.exp() * lp).sum(), 9 * sum_tol(4.0) + 16 * U)
+    g = torch.ones(1, device="cuda")
+    dz = dl.logprobs_backward(z, tokens, r.row_max, r.log_sum, g, out=z)
+    want = -lp.exp()
+    want[-1] += 1
+    near(dz[0, at], want, 64 * U + UT[kind] * want.abs())
+    assert int(torch.count_nonzero(dz)) == 7
+
+
 def test_token_logprobs_gradient(dl):
     """Every output's gradient together, against 64-bit autograd and differences."""
     z = logits_of(6, 301, "f32", 1).requires_grad_()
@@ -480,7 +507,7 @@ def test_token_logprobs_gradient(dl):
     assert float((got.double() - want).abs().max()) <= 1e-5 * float(want.abs().max())
     step = torch.randn(z.shape, generator=gen(9), device="cuda", dtype=torch.float64)
     eps = 1e-4
-    slope = float(plain(zd + eps * step) - plain(zd - eps * step)) / (2 * eps)
+    slope = float((plain(zd + eps * step) - plain(zd - eps * step)).detach()) / (2 * eps)
     assert abs(slope - float((got.double() * step).sum())) <= 1e-4 * float((got.double() * step).abs().sum())
     # a mean's gradient is one value for all rows
     z2 = z.detach().to(torch.bfloat16).requires_grad_()
@@ -545,6 +572,28 @@ def test_streams_and_graphs(dl):
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
     assert all(torch.equal(a, b) for a, b in zip(got[1], want[1]))
+
+
+def test_calls_at_once(dl):
+    """Calls of two streams at the same time, many of them, share nothing."""
+    F = dl.RotaryFrequencies(64)
+    work = []
+    for i in range(2):
+        z, t = logits_of(300, 32003 + 17 * i, "bf16", i), tokens_of(300, 32003, i)
+        x = randn((2, 400, 9, 64), 5 + i, "bf16")
+        r = dl.logprobs_forward(z, t, top=6, entropy=True)
+        work.append((z, t, x, r, dl.logprobs_backward(z, t, r.row_max, r.log_sum, r.logp), dl.rotary_apply(x, F)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in work]
+    for _ in range(10):
+        got = []
+        for s, (z, t, x, *_) in zip(streams, work):
+            with torch.cuda.stream(s):
+                r = dl.logprobs_forward(z, t, top=6, entropy=True)
+                got.append((r, dl.logprobs_backward(z, t, r.row_max, r.log_sum, r.logp), dl.rotary_apply(x, F)))
+        torch.cuda.synchronize()
+        for (r, d, y), (_, _, _, want, wd, wy) in zip(got, work):
+            assert all(torch.equal(a, b) for a, b in zip(r, want)) and torch.equal(d, wd) and torch.equal(y, wy)
 
 
 def _attend(x, w, F, apply):
