@@ -129,15 +129,17 @@ def _refuse_heads(t, name, like):
 
 
 def _heads(t, name, i, like, shape):
-    """Strides (batch, token, head) of [batch][tokens][heads][head_dim], which
-    must go with `like` of that shape; a tensor of three dimensions has a batch
-    of one. name and i name it where it does not."""
+    """Strides (batch, token, head, ...) of [batch][tokens][heads][head_dim],
+    which must go with `like` of that shape; a tensor of three dimensions has a
+    batch of one. name and i name it where it does not."""
     if isinstance(t, torch.Tensor) and t.dtype is like.dtype and t.dtype in _TYPE:
         d, s = t.shape, t.stride()
-        n = len(d)
-        if (n == len(shape) and 3 <= n <= 4 and (s[-1] == 1 or d[-1] == 1) and d[-1] == shape[-1]
-                and d[-3] == shape[-3] and (n == 3 or d[0] == shape[0])):
-            return s if n == 4 else (0, *s)
+        if len(d) == len(shape) and d[-1] == shape[-1] and (s[-1] == 1 or d[-1] == 1):
+            if len(d) == 4:
+                if d[1] == shape[1] and d[0] == shape[0]:
+                    return s
+            elif len(d) == 3 and d[0] == shape[0]:
+                return (0, *s)
     _refuse_heads(t, f"{name}[{i}]", like)
 
 
@@ -189,34 +191,29 @@ def rotary_apply(xs, frequencies, positions=None, first=0, interleaved=False, in
                                 inverse, out)
     if not isinstance(frequencies, RotaryFrequencies):
         raise TypeError(f"frequencies: expected RotaryFrequencies, got {type(frequencies).__name__}")
-    shape = x0.shape
-    n = len(xs)
+    shape, n = x0.shape, len(xs)
     if out is None:
-        ys = None
+        ys = [torch.empty_like(x) for x in xs]
     else:
-        ys = (out,) if isinstance(out, torch.Tensor) else tuple(out)
+        ys = [out] if isinstance(out, torch.Tensor) else list(out)
         if len(ys) != n:
             raise ValueError(f"out: {len(ys)} tensors for {n}")
     jobs = (_RotaryJob * n)()
     turns = frequencies.turns
     here = turns.get_device() == at >= 0
-    given = []
     for i, x in enumerate(xs):
-        j = jobs[i]
-        j.x_batch, j.x_token, j.x_head = _heads(x, "xs", i, x0, shape)[:3]
-        j.x, j.heads = x.data_ptr(), _int32(x.shape[-2], "heads")
-        if ys is None:
-            y = torch.empty_like(x)
-            j.y_batch, j.y_token, j.y_head = y.stride()[:3] if len(shape) == 4 else (0, *y.stride()[:2])
-        else:
-            y = ys[i]
-            if isinstance(y, torch.Tensor) and y.shape != x.shape:
-                raise ValueError(f"out[{i}]: shape {tuple(y.shape)}, expected {tuple(x.shape)}")
-            j.y_batch, j.y_token, j.y_head = _heads(y, "out", i, x0, shape)[:3]
-        j.y = y.data_ptr()
-        given.append(y)
-        here = here and x.get_device() == at and y.get_device() == at
-    ys = tuple(given)
+        y = ys[i]
+        xb, xt, xh, *_ = _heads(x, "xs", i, x0, shape)
+        yb, yt, yh, *_ = _heads(y, "out", i, x0, shape)
+        heads = x.shape[-2]
+        if y.shape[-2] != heads:
+            raise ValueError(f"out[{i}]: shape {tuple(y.shape)}, expected {tuple(x.shape)}")
+        if heads >= 2**31:
+            _int32(heads, "heads")
+        jobs[i] = (x.data_ptr(), y.data_ptr(), xb, xt, xh, yb, yt, yh, heads)
+        if here:
+            here = x.get_device() == at and y.get_device() == at
+    ys = tuple(ys)
     batch, tokens, width = shape[0] if len(shape) == 4 else 1, shape[-3], _int32(shape[-1], "head_dim")
     if width < frequencies.dim:
         raise ValueError(f"xs[0]: heads of {width} elements, frequencies rotate {frequencies.dim}")
