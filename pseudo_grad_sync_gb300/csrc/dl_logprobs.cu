@@ -64,20 +64,42 @@ __device__ __forceinline__ float largest(const Pack<T, N> (&p)[U]) {
 // that is 0 because its logit is -inf makes the entropy's sum NaN; that sum is
 // then taken again with exponents kept finite, which costs the packs with
 // masked logits a second pass and the others nothing.
+//
+// Where there are enough of them the exponents are one fused product each,
+// x * log2(e) + c with c = -m * log2(e) as rounded: all are off by the same
+// `off`, which the fused m * log2(e) + c gives exactly and the sums are
+// corrected by (16384 x 32000 bf16 with entropy and 5 alternatives 213 us,
+// 224 without). Not for maxima so large that it is no small number.
 template <bool ENTROPY, typename T, int N, int U>
 __device__ __forceinline__ void add_packs(Part& part, const Pack<T, N> (&p)[U], float top) {
     part.raise(max_nan(part.m, top));
     float2 s = make_float2(0.f, 0.f), a = s;
-    const float2 minus = both(-part.m), unit = both(kLog2E);
+    const float2 unit = both(kLog2E);
+    if (N * U >= 32 && fabsf(part.m) < 0x1p20f) {
+        const float c = -(part.m * kLog2E), off = fmaf(part.m, kLog2E, c), back = exp2_fast(-off);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-            const float2 t = mul2(add2(pair_of(&p[u], i), minus), unit);
-            const float2 e = make_float2(exp2_fast(t.x), exp2_fast(t.y));
-            s = add2(s, e);
-            if (ENTROPY) a = fma2(e, t, a);
-        }
+            for (int i = 0; i < N / 2; ++i) {
+                const float2 t = fma2(pair_of(&p[u], i), unit, both(c));
+                const float2 e = make_float2(exp2_fast(t.x), exp2_fast(t.y));
+                s = add2(s, e);
+                if (ENTROPY) a = fma2(e, t, a);
+            }
+        s.x = (s.x + s.y) * back, s.y = 0.f;
+        a.x = fmaf(a.x + a.y, back, -off * s.x), a.y = 0.f;
+    } else {
+        const float2 minus = both(-part.m);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                const float2 t = mul2(add2(pair_of(&p[u], i), minus), unit);
+                const float2 e = make_float2(exp2_fast(t.x), exp2_fast(t.y));
+                s = add2(s, e);
+                if (ENTROPY) a = fma2(e, t, a);
+            }
+    }
     float sum = a.x + a.y;
     if (ENTROPY && !(sum == sum)) {
         sum = 0.f;
@@ -344,16 +366,14 @@ __device__ __forceinline__ uint64_t alternatives(const S& mine, const float (&mo
 // straight into registers: 428 us). Where a block's warps share a row one more
 // joins their parts, finds the alternatives and writes the outputs while they
 // are at the next row; one barrier per row hands over (without that warp, the
-// alternatives found by all: 535 us where this takes 376).
+// alternatives found by all: 535 us where this takes 359).
 //
-// Bound by HBM without alternatives: 8192 x 128256 bf16 297 us (105% of the copy
-// rate, which also writes), with entropy 325 (96%); 16384 x 32000 161 (96%);
+// Bound by HBM without alternatives: 8192 x 128256 bf16 294 us (106% of the copy
+// rate, which also writes), with entropy 315 (98%); 16384 x 32000 157 (99%);
 // 8192 x 32000 fp32 with entropy and 5 alternatives 157 (99%). With alternatives
-// in 16 bits by instruction issue, 63% of the slots with HBM at 64%: 8192 x 128256
-// with entropy and 20 of them 376 us (83%), 16384 x 32000 with 5 224 (69%). 7.0
-// instructions per logit and lane, 8.0 with entropy; 1100 per row for one
-// alternative, 2000 for twenty. Few rows: 3 x 128256 with 8 alternatives 9.2 us,
-// without 4.9; 512 x 512 2.8 us.
+// in 16 bits by instruction issue beside HBM: 8192 x 128256 with entropy and 20
+// of them 359 us (87%), 16384 x 32000 with 5 213 (73%). Few rows: 3 x 128256
+// with 8 alternatives 9.2 us, without 4.9; 512 x 512 2.8 us.
 template <typename T, int TPR, bool ENTROPY, bool TOP, bool CLUSTER>
 __global__ void __launch_bounds__(Geometry<T, TPR>::kBlock, TPR == 32 ? 6 : TPR == 128 ? 5 : 3)
     k_logprobs(const __grid_constant__ ForwardArgs<T> a) {
@@ -520,8 +540,9 @@ __global__ void __launch_bounds__(Geometry<T, TPR>::kBlock, TPR == 32 ? 6 : TPR 
         Part part = Part::nothing();
         constexpr int kOf = kSlots<T, kWarps>;
         const int per = TOP ? (mine.stages + kOf - 1) / kOf : 1;
-        int in_slot = 0, slot_at = 0;
-        float slot_most = -INFINITY, most = -INFINITY;  // of the slot, of the row
+        T* slot_to = TOP ? &hand[set].most[0][t] : nullptr;
+        int in_slot = 0;
+        float slot_most = -INFINITY;
         for (int k = 0; k < mine.stages; ++k) {
             copy_wait<kAhead - 1>();
             const int first = mine.begin + k * U * TPR;
@@ -556,14 +577,15 @@ __global__ void __launch_bounds__(Geometry<T, TPR>::kBlock, TPR == 32 ? 6 : TPR 
             add_packs<ENTROPY>(part, q, here);
             if constexpr (TOP) {
                 slot_most = fmaxf(slot_most, here);
-                if (++in_slot == per || k == mine.stages - 1) {
-                    hand[set].most[slot_at][t] = from_f32<T>(slot_most);
-                    most = fmaxf(most, slot_most);
-                    ++slot_at, in_slot = 0, slot_most = -INFINITY;
+                if (++in_slot == per) {
+                    *slot_to = from_f32<T>(slot_most);
+                    slot_to += TPR, in_slot = 0, slot_most = -INFINITY;
                 }
             }
             stage = stage == kAhead ? 0 : stage + 1;
         }
+        if (TOP && in_slot > 0) *slot_to = from_f32<T>(slot_most);
+        const float most = part.m;
         join(part);
         if constexpr (kAlone) {
             const float mosts[1] = {most};
@@ -621,11 +643,11 @@ int launch(const ForwardArgs<T>& a, int ranks, cudaStream_t s) {
 
 // A warp per row while that leaves it less than 64 packs per lane and there
 // are rows for every warp (65536 x 4096 bf16 109 us, 331 with a block of eight
-// warps; 16384 x 32000 168, with a block of four 161); few rows by clusters of
+// warps; 16384 x 32000 166, with a block of four 157); few rows by clusters of
 // up to eight blocks of eight warps, while there are SMs for them and the
 // shares fill a block (64 x 128256: 8.0 us, with one block each 19); else a
-// block of four warps (eight: 16384 x 32000 185 us, 8192 x 128256 291 for 297,
-// with entropy and 20 alternatives 388 for 376).
+// block of four warps (eight: 16384 x 32000 185 us for 161 then, 8192 x 128256 291
+// for 297, with entropy and 20 alternatives 388 for 376).
 template <typename T>
 int forward(const ForwardArgs<T>& a, cudaStream_t s) {
     constexpr int N = 16 / sizeof(T);
