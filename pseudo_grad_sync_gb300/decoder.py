@@ -50,7 +50,7 @@ def declare(L):
     L.dl_rotary_frequencies.restype = ctypes.c_int
     L.dl_rotary_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64, vp]
     L.dl_rotary_apply.restype = ctypes.c_int
-    L.dl_rotary_apply.argtypes = [ctypes.POINTER(_RotaryJob), i32, i32, i64, i64, i32, i32, vp, f64,
+    L.dl_rotary_apply.argtypes = [vp, i32, i32, i64, i64, i32, i32, vp, f64,
                                   vp, i32, i64, i64, i32, vp]
     L.dl_logprobs_forward.restype = ctypes.c_int
     L.dl_logprobs_forward.argtypes = [vp, i64, i32, i64, i32, vp, i32, vp, vp, vp, i32, vp, vp, vp,
@@ -192,28 +192,35 @@ def rotary_apply(xs, frequencies, positions=None, first=0, interleaved=False, in
     if not isinstance(frequencies, RotaryFrequencies):
         raise TypeError(f"frequencies: expected RotaryFrequencies, got {type(frequencies).__name__}")
     shape, n = x0.shape, len(xs)
-    if out is None:
-        ys = [torch.empty_like(x) for x in xs]
-    else:
-        ys = [out] if isinstance(out, torch.Tensor) else list(out)
+    ys = None
+    if out is not None:
+        ys = (out,) if isinstance(out, torch.Tensor) else tuple(out)
         if len(ys) != n:
             raise ValueError(f"out: {len(ys)} tensors for {n}")
     jobs = (_RotaryJob * n)()
     turns = frequencies.turns
     here = turns.get_device() == at >= 0
+    given = []
     for i, x in enumerate(xs):
-        y = ys[i]
-        xb, xt, xh, *_ = _heads(x, "xs", i, x0, shape)
-        yb, yt, yh, *_ = _heads(y, "out", i, x0, shape)
+        s = _heads(x, "xs", i, x0, shape)
         heads = x.shape[-2]
-        if y.shape[-2] != heads:
-            raise ValueError(f"out[{i}]: shape {tuple(y.shape)}, expected {tuple(x.shape)}")
+        if ys is None:
+            y = torch.empty_like(x)
+            r = y.stride()
+            if len(r) == 3:
+                r = (0, *r)
+        else:
+            y = ys[i]
+            r = _heads(y, "out", i, x0, shape)
+            if y.shape[-2] != heads:
+                raise ValueError(f"out[{i}]: shape {tuple(y.shape)}, expected {tuple(x.shape)}")
+            here = here and y.get_device() == at
+        here = here and x.get_device() == at
         if heads >= 2**31:
             _int32(heads, "heads")
-        jobs[i] = (x.data_ptr(), y.data_ptr(), xb, xt, xh, yb, yt, yh, heads)
-        if here:
-            here = x.get_device() == at and y.get_device() == at
-    ys = tuple(ys)
+        jobs[i] = (x.data_ptr(), y.data_ptr(), s[0], s[1], s[2], r[0], r[1], r[2], heads)
+        given.append(y)
+    ys = tuple(given)
     batch, tokens, width = shape[0] if len(shape) == 4 else 1, shape[-3], _int32(shape[-1], "head_dim")
     if width < frequencies.dim:
         raise ValueError(f"xs[0]: heads of {width} elements, frequencies rotate {frequencies.dim}")
