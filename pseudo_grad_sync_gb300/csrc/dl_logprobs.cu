@@ -179,7 +179,8 @@ struct Share {
         begin = min(rank * each, packs.packs);
         end = min(begin + each, packs.packs);
         low = max(begin, packs.base < from ? 1 : 0);
-        high = min(end, packs.packs - (packs.base + int64_t(packs.packs) * packs.N > to ? 1 : 0));
+        // no less than low: one pack may hold both of the logits' ends
+        high = max(low, min(end, packs.packs - (packs.base + int64_t(packs.packs) * packs.N > to ? 1 : 0)));
         stages = max((end - begin + TPR * U - 1) / (TPR * U), 1);
     }
 };
@@ -233,9 +234,10 @@ struct Geometry {
 // The n_top-th largest of the threads' maxima is a bound that no alternative
 // lies below, and (ties aside) n_top threads and hardly more slots have a
 // logit that reaches it. (Of several warps' maxima the two largest of every
-// lane are taken for all: a bound hardly lower, for a part of the sorting.) Their packs alone are read again; what reaches the
-// bound is collected, and sorted in runs of 32. One warp's instructions are
-// what this costs: every step leaves the next one little to look at.
+// lane are taken for all: a bound hardly lower, for a part of the sorting.) Their
+// packs alone are read again; what reaches the bound is collected, and sorted in
+// runs of 32. One warp's instructions are what this costs: every step leaves the
+// next one little to look at.
 template <typename T, int TPR, int U, int WARPS, typename S>
 __device__ __forceinline__ uint64_t alternatives(const S& mine, const float (&most)[WARPS],
                                                  const T (*slots)[WARPS * 32], int n_top, int lane,

@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, TOP && !SHIFT ? 8 : 7) k_logprobs_bw
         if (edge >= 0) y[edge] = from_f32<T>(zero ? 0.f : r.at(both(at_edge)).x);
         if (has_token || (TOP && __any_sync(kAll, has_top))) {
             __syncwarp();
-            if (has_top) y[mine] = from_f32<T>(at_top);
+            if (has_top && !(has_token && mine == token)) y[mine] = from_f32<T>(at_top);
             if (has_token && lane == 0) y[token] = from_f32<T>(at_token);
         }
     }

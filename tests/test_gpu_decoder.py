@@ -322,6 +322,24 @@ def test_logprobs_strides_and_alignment(dl, kind, vocab):
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+def test_logprobs_slices(dl, kind):
+    """One row and two, of a few columns, anywhere in a buffer: a single pack may
+    hold both ends of the tensor."""
+    room = torch.full((64,), math.nan, device="cuda", dtype=TYPES[kind])
+    for vocab in (1, 2, 3, 5, 7, 8, 9, 16, 17):
+        for off in range(17):
+            for rows in (1, 2):
+                room.fill_(math.nan)
+                z = room[off:off + rows * vocab].view(rows, vocab)
+                z.copy_(logits_of(rows, vocab, kind, vocab + off))
+                tokens = tokens_of(rows, vocab, off)
+                r = dl.logprobs_forward(z, tokens, top=2, entropy=True)
+                check_logprobs(r, z, tokens, 2, True)
+                check_backward(dl, z, tokens, r, kind, off, 2, True)
+                check_logprobs(dl.logprobs_forward(z, tokens), z, tokens, 0, False)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("vocab", [40, 3000, 70001])
 def test_logprobs_masks(dl, kind, vocab):
     """Masked entries, rows with one entry and none, the lowest values, NaN and
