@@ -679,7 +679,9 @@ int dl_rotary_apply(const dl_rotary_job* jobs, int32_t n_jobs, int32_t type, int
  *    and entropy 0.
  *  - A row with NaN or +inf: NaN in every fp32 output, token -1 in top.
  * Pointers need the alignment of their elements only. rows = 0 is a no-op;
- * vocab >= 1.
+ * vocab >= 1. What lies between two rows of logits (stride > vocab) may be
+ * read, and counts for nothing; nothing before the first row's start or
+ * behind the last one's end is. The backward call reads likewise.
  */
 int dl_logprobs_forward(const void* logits, int64_t stride, int32_t type, int64_t rows,
                         int32_t vocab, const void* tokens, int32_t token_type, float* logp,

@@ -46,14 +46,24 @@ __device__ __forceinline__ uint64_t position_of(const RotaryArgs& a, int64_t bat
                                                            : static_cast<const int32_t*>(a.positions)[at]);
 }
 
-// A unit of a head: what one thread turns or copies at once.
+// A unit of a head: what one thread turns or copies at once. Packs of
+// neighbouring pairs lie at multiples of N from the head's start, the last
+// turned one perhaps with elements behind the rotated part; units of two packs
+// hold nothing but pairs, or nothing but elements behind them.
 template <int N, bool INTERLEAVED>
 struct Form {
     static constexpr bool kTwo = !INTERLEAVED || N == 1;  // two packs, else one
     static constexpr int kSize = kTwo ? 2 * N : N, kPairs = kSize / 2;
     static constexpr int kStep = INTERLEAVED ? kSize : N;  // from a turned unit's first pack to the next one's
+    static __host__ __device__ int turned(int pairs) { return (pairs + kPairs - 1) / kPairs; }
+    // elements of a head behind the rotated part's units
+    static __host__ __device__ int rest(int head_dim, int pairs) { return head_dim - turned(pairs) * kSize; }
     static __host__ __device__ int units(int head_dim, int pairs) {
-        return pairs / kPairs + ((head_dim - 2 * pairs) / N * N + kSize - 1) / kSize;
+        return turned(pairs) + (rest(head_dim, pairs) / N * N + kSize - 1) / kSize;
+    }
+    // whether packs of N suit these sizes
+    static bool fits(int head_dim, int pairs) {
+        return kTwo ? pairs % N == 0 || N == 1 : rest(head_dim, pairs) >= 0;
     }
 };
 
@@ -81,9 +91,10 @@ __device__ __forceinline__ void set_pair(Pack<T, N>& p, int i, float2 v) {
 }
 
 // A unit's pairs turned in place. Half layout: the pairs' first elements in v,
-// the second ones in w; interleaved: neighbours in v (packs of one: in v and w).
+// the second ones in w; interleaved: the first `pairs` neighbours in v (packs of
+// one: in v and w).
 template <typename T, int N, bool INTERLEAVED, int PAIRS>
-__device__ __forceinline__ void turn_unit(Pack<T, N>& v, Pack<T, N>& w, const float2 (&cs)[PAIRS]) {
+__device__ __forceinline__ void turn_unit(Pack<T, N>& v, Pack<T, N>& w, const float2 (&cs)[PAIRS], int pairs) {
     if constexpr (N == 1) {
         float a = to_f32(v.v[0]), b = to_f32(w.v[0]);
         turn(a, b, cs[0].x, cs[0].y);
@@ -91,6 +102,7 @@ __device__ __forceinline__ void turn_unit(Pack<T, N>& v, Pack<T, N>& w, const fl
     } else if constexpr (INTERLEAVED) {
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) {
+            if (i >= pairs) break;
             float2 e = pair_of(&v, i);
             turn(e.x, e.y, cs[i].x, cs[i].y);
             set_pair(v, i, e);
@@ -113,14 +125,14 @@ __device__ __forceinline__ void turn_unit(Pack<T, N>& v, Pack<T, N>& w, const fl
 // is a pack of N elements (half layout: with the pack of its pairs' partners),
 // or packs behind the rotated part that are only copied.
 //
-// Bound by HBM (reads and writes mixed, 77% of its peak in the counters): 4 x 8192
-// tokens of 32 + 8 heads of 128 bf16 110 us (90% of the copy rate), half of each
-// head rotated 113, 4 x 4096 in fp32 104 (96%), interleaved 109. With the cosines
+// Bound by HBM (reads and writes mixed, 78% of its peak in the counters): 4 x 8192
+// tokens of 32 + 8 heads of 128 bf16 106 us (93% of the copy rate), half of each
+// head rotated 111, 4 x 4096 in fp32 103 (96%), interleaved 111. With the cosines
 // read from shared memory for every head and an integer division per row it was
 // 218 us; one head at a time per thread 118. The next heads' loads ahead of the
 // cosines gained nothing on single tokens and cost the batch 8 us. Single tokens
-// (5 x 36 heads of 64): 3.6 us. What is left: heads few or narrow (one query and
-// one key head of 128: 22%), whose tokens share a cosine among two heads only, and
+// (5 x 36 heads of 64): 3.4 us. What is left: heads few or narrow (one query and
+// one key head of 128: 23%), whose tokens share a cosine among two heads only, and
 // packs below 16 bytes (heads of 75: 37-41%).
 template <typename T, int N, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads, 3) k_rotary(const __grid_constant__ RotaryArgs a) {
@@ -129,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_rotary(const __grid_constant__ 
     using F = Form<N, INTERLEAVED>;
     constexpr int kPairs = F::kPairs, kRows = 4;  // heads at a time
     constexpr bool kTwo = F::kTwo;
-    const int turned = a.pairs / kPairs, rotated = 2 * a.pairs, units = F::units(a.head_dim, a.pairs);
+    const int turned = F::turned(a.pairs), units = F::units(a.head_dim, a.pairs), behind = turned * F::kSize;
     const int wide = min(units, kThreads);
     const int slot = threadIdx.x / wide, local = slot / a.lanes, head = slot - local * a.lanes;
     const int token0 = threadIdx.x / a.pairs, pair0 = threadIdx.x - token0 * a.pairs;
@@ -150,10 +162,12 @@ __global__ void __launch_bounds__(kThreads, 3) k_rotary(const __grid_constant__ 
         for (int l = slot < a.side * a.lanes ? local : count, u = first_unit; l < count;
              u + wide < units ? u += wide : (u = first_unit, l += a.side)) {
             const bool turns = u < turned;
+            const int pairs = a.pairs - u * kPairs;  // of the unit, where it has fewer than kPairs
             float2 cs[kPairs];
 #pragma unroll
-            for (int i = 0; i < kPairs; ++i) cs[i] = turns ? table[l * a.pairs + u * kPairs + i] : make_float2(0.f, 0.f);
-            const int low = turns ? u * F::kStep : rotated + (u - turned) * F::kSize;
+            for (int i = 0; i < kPairs; ++i)
+                cs[i] = i < pairs ? table[l * a.pairs + u * kPairs + i] : make_float2(0.f, 0.f);
+            const int low = turns ? u * F::kStep : behind + (u - turned) * F::kSize;
             const int apart = turns && !INTERLEAVED ? a.pairs : N;  // between a unit's two packs
             const bool two = kTwo && (turns || low + 2 * N <= a.head_dim);
             for (int j = 0; j < a.n_jobs; ++j) {
@@ -174,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_rotary(const __grid_constant__ 
                     for (int r = 0; r < kRows; ++r)
                         if (h + r * a.lanes < job.heads) {
                             T* to = y + (h + r * a.lanes) * job.y_head;
-                            if (turns) turn_unit<T, N, INTERLEAVED>(v[r], w[r], cs);
+                            if (turns) turn_unit<T, N, INTERLEAVED>(v[r], w[r], cs, pairs);
                             *reinterpret_cast<P*>(to) = v[r];
                             if (two) *reinterpret_cast<P*>(to + apart) = w[r];
                         }
@@ -182,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_rotary(const __grid_constant__ 
             }
         }
         // elements behind the last whole pack
-        const int tail = (a.head_dim - rotated) % N;
+        const int tail = F::rest(a.head_dim, a.pairs) % N;
         if (N > 1 && tail > 0)
             for (int j = 0; j < a.n_jobs; ++j) {
                 const dl_rotary_job& job = a.job[j];
@@ -233,7 +247,7 @@ int launch(RotaryArgs a, cudaStream_t s) {
 // half of that, down to single elements.
 template <typename T, int N>
 int by_pack(const RotaryArgs& a, bool interleaved, cudaStream_t s) {
-    bool fits = (interleaved ? 2 * a.pairs : a.pairs) % N == 0;
+    bool fits = interleaved ? Form<N, true>::fits(a.head_dim, a.pairs) : Form<N, false>::fits(a.head_dim, a.pairs);
     for (int j = 0; j < a.n_jobs && fits; ++j) {
         const dl_rotary_job& q = a.job[j];
         fits = aligned_to(q.x, N * sizeof(T)) && aligned_to(q.y, N * sizeof(T)) &&

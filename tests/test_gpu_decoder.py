@@ -73,7 +73,8 @@ def check_rotary(x, y, angle, kind, **how):
 @pytest.mark.parametrize("batch,tokens,heads,width,dim", [
     (1, 1, 1, 2, 2), (2, 3, 5, 64, 64), (3, 17, 4, 128, 128), (2, 9, 3, 75, 50), (1, 33, 2, 96, 32),
     (5, 1, 36, 64, 64), (2, 5, 3, 83, 16), (1, 4, 2, 257, 256), (2, 301, 3, 40, 24),
-    (1, 2, 2, 2060, 2048), (1, 3, 1, 8193, 8192), (7, 1, 300, 8, 6)])
+    (1, 2, 2, 2060, 2048), (1, 3, 1, 8193, 8192), (7, 1, 300, 8, 6), (2, 7, 5, 96, 52), (1, 9, 3, 256, 2),
+    (2, 4, 3, 16, 14), (1, 5, 2, 24, 18), (1, 5, 2, 64, 62)])
 def test_rotary(dl, kind, interleaved, batch, tokens, heads, width, dim):
     F = dl.RotaryFrequencies(dim, amplitude=1.25)
     q, k = randn((batch, tokens, heads, width), 1, kind), randn((batch, tokens, 1, width), 2, kind)
