@@ -213,12 +213,12 @@ struct alignas(16) Finish {
     int waiting;
 };
 
-template <typename T, int TPR>
+template <typename T, int TPR, int UNROLL>
 struct Geometry {
     static constexpr int kWarps = TPR / 32;  // of a row
     static constexpr bool kAlone = kWarps == 1;
     static constexpr int kMain = kAlone ? 128 : TPR, kBlock = kAlone ? kMain : kMain + 32, kGroups = kMain / TPR;
-    static constexpr int U = kAlone ? 2 : 4, kStages = kAlone ? 6 : 3, kHands = kAlone ? 1 : 2;
+    static constexpr int U = UNROLL, kStages = !kAlone ? 3 : U == 2 ? 6 : 4, kHands = kAlone ? 1 : 2;
     static constexpr size_t kRing = size_t(kStages) * U * kMain * 16;
     static constexpr size_t kHand = sizeof(Handover<T, kWarps>), kFinish = sizeof(Finish<kWarps>);
     static_assert(kHand % 16 == 0 && kFinish % 16 == 0, "");
@@ -370,17 +370,17 @@ __device__ __forceinline__ uint64_t alternatives(const S& mine, const float (&mo
 // are at the next row; one barrier per row hands over (without that warp, the
 // alternatives found by all: 535 us where this takes 359).
 //
-// Bound by HBM without alternatives: 8192 x 128256 bf16 294 us (106% of the copy
-// rate, which also writes), with entropy 315 (98%); 16384 x 32000 157 (99%);
+// Bound by HBM without alternatives: 8192 x 128256 bf16 289 us (107% of the copy
+// rate, which also writes), with entropy 313 (99%); 16384 x 32000 157 (99%);
 // 8192 x 32000 fp32 with entropy and 5 alternatives 157 (99%). With alternatives
 // in 16 bits by instruction issue beside HBM: 8192 x 128256 with entropy and 20
 // of them 359 us (87%), 16384 x 32000 with 5 213 (73%). Few rows: 3 x 128256
 // with 8 alternatives 9.2 us, without 4.9; 512 x 512 2.8 us.
-template <typename T, int TPR, bool ENTROPY, bool TOP, bool CLUSTER>
-__global__ void __launch_bounds__(Geometry<T, TPR>::kBlock, TPR == 32 ? 6 : TPR == 128 ? 5 : 3)
+template <typename T, int TPR, int U, bool ENTROPY, bool TOP, bool CLUSTER>
+__global__ void __launch_bounds__(Geometry<T, TPR, U>::kBlock, TPR == 32 ? 6 : TPR == 128 ? 5 : 3)
     k_logprobs(const __grid_constant__ ForwardArgs<T> a) {
-    using Geo = Geometry<T, TPR>;
-    constexpr int N = 16 / sizeof(T), U = Geo::U, kWarps = Geo::kWarps, kAhead = Geo::kStages - 1;
+    using Geo = Geometry<T, TPR, U>;
+    constexpr int N = 16 / sizeof(T), kWarps = Geo::kWarps, kAhead = Geo::kStages - 1;
     constexpr bool kAlone = Geo::kAlone;
     using P = Pack<T, N>;
     using Mine = Share<T, TPR, U>;
@@ -608,10 +608,10 @@ __global__ void __launch_bounds__(Geometry<T, TPR>::kBlock, TPR == 32 ? 6 : TPR 
     copy_wait<0>();
 }
 
-template <typename T, int TPR, bool ENTROPY, bool TOP, bool CLUSTER>
+template <typename T, int TPR, int U, bool ENTROPY, bool TOP, bool CLUSTER>
 int launch(const ForwardArgs<T>& a, int ranks, cudaStream_t s) {
-    using Geo = Geometry<T, TPR>;
-    auto* kernel = k_logprobs<T, TPR, ENTROPY, TOP, CLUSTER>;
+    using Geo = Geometry<T, TPR, U>;
+    auto* kernel = k_logprobs<T, TPR, U, ENTROPY, TOP, CLUSTER>;
     static Resident resident;
     const int64_t work = (a.rows + Geo::kGroups - 1) / Geo::kGroups * ranks;
     const int grid = resident.grid(reinterpret_cast<const void*>(kernel), Geo::kBlock, Geo::bytes(TOP), work);
@@ -634,18 +634,22 @@ int launch(const ForwardArgs<T>& a, int ranks, cudaStream_t s) {
     return DL_OK;
 }
 
-template <typename T, int TPR, bool CLUSTER>
+template <typename T, int TPR, int U, bool CLUSTER, bool TOP = true>
 int launch(const ForwardArgs<T>& a, int ranks, cudaStream_t s) {
-    if (a.entropy)
-        return a.n_top ? launch<T, TPR, true, true, CLUSTER>(a, ranks, s)
-                       : launch<T, TPR, true, false, CLUSTER>(a, ranks, s);
-    return a.n_top ? launch<T, TPR, false, true, CLUSTER>(a, ranks, s)
-                   : launch<T, TPR, false, false, CLUSTER>(a, ranks, s);
+    if constexpr (TOP) {
+        if (a.n_top)
+            return a.entropy ? launch<T, TPR, U, true, true, CLUSTER>(a, ranks, s)
+                             : launch<T, TPR, U, false, true, CLUSTER>(a, ranks, s);
+    }
+    return a.entropy ? launch<T, TPR, U, true, false, CLUSTER>(a, ranks, s)
+                     : launch<T, TPR, U, false, false, CLUSTER>(a, ranks, s);
 }
 
 // A warp per row while that leaves it less than 64 packs per lane and there
-// are rows for every warp (65536 x 4096 bf16 109 us, 331 with a block of eight
-// warps; 16384 x 32000 166, with a block of four 157); few rows by clusters of
+// are rows for every warp (65536 x 4096 bf16 102 us, 331 with a block of eight
+// warps; in stages of four packs but for rows that fill less than a stage, and
+// with alternatives, whose shared memory leaves fewer blocks: 32768 x 8192 84 us,
+// in stages of two 93, but 262144 x 512 173 where those take 146; 16384 x 32000 166, with a block of four 157); few rows by clusters of
 // up to eight blocks of eight warps, while there are SMs for them and the
 // shares fill a block (64 x 128256: 8.0 us, with one block each 19); else a
 // block of four warps (eight: 16384 x 32000 185 us for 161 then, 8192 x 128256 291
@@ -654,11 +658,12 @@ template <typename T>
 int forward(const ForwardArgs<T>& a, cudaStream_t s) {
     constexpr int N = 16 / sizeof(T);
     const int64_t packs = a.vocab / N;
-    if (packs <= 2048 && (packs <= 256 || a.rows >= 4096)) return launch<T, 32, false>(a, 1, s);
+    if (packs <= 2048 && (packs <= 256 || a.rows >= 4096))
+        return packs > 96 && !a.n_top ? launch<T, 32, 4, false, false>(a, 1, s) : launch<T, 32, 2, false>(a, 1, s);
     int ranks = 1;
     while (ranks < 8 && a.rows * ranks * 2 <= 3 * sm_count() && packs / (ranks * 2) >= 256) ranks *= 2;
-    if (ranks > 1) return launch<T, 256, true>(a, ranks, s);
-    return launch<T, 128, false>(a, 1, s);
+    if (ranks > 1) return launch<T, 256, 4, true>(a, ranks, s);
+    return launch<T, 128, 4, false>(a, 1, s);
 }
 
 }  // namespace

@@ -269,7 +269,8 @@ def check_backward(dl, z, tokens, r, kind, seed, top=0, entropy=False, zero_rows
 @pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("rows,vocab", [
     (1, 1), (3, 2), (5, 7), (2, 31), (4, 33), (1, 64), (9, 129), (70, 255), (2, 1000), (33, 1025), (3, 2047),
-    (2, 4097), (5, 8192), (2, 20001), (40, 32000), (1, 32003), (1, 128256), (3, 131073), (700, 513)])
+    (2, 4097), (5, 8192), (2, 20001), (40, 32000), (1, 32003), (1, 128256), (3, 131073), (700, 513),
+    (4100, 5001), (4097, 2560)])
 def test_logprobs(dl, kind, rows, vocab):
     z, tokens = logits_of(rows, vocab, kind, rows + vocab), tokens_of(rows, vocab, 1)
     for top, entropy in ((0, False), (0, True), (1, False), (7, True), (32, False)):
@@ -664,7 +665,7 @@ def test_decoder_step(dl):
     want_loss = model(p64, lambda x, w: x * torch.rsqrt(x.square().mean(-1, keepdim=True) + 1e-5) * w, rotate64, theirs)
     want = torch.autograd.grad(want_loss, list(p64.values()))
     # products of 333, 128 and 64 terms in fp32, a few in a row: 2000 u of the norm
-    assert abs(float(loss) - float(want_loss)) <= 2000 * U * abs(float(want_loss))
+    assert abs(loss.item() - want_loss.item()) <= 2000 * U * abs(want_loss.item())
     for n, a, b in zip(p, got, want):
         assert float((a.double() - b).norm()) <= 2000 * U * float(b.norm()), n
 
