@@ -378,6 +378,26 @@ def test_logprobs_masks(dl, kind, vocab):
     near(dl.logprobs_forward(z, narrow).logp, r.logp, 0)
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("vocab,rows,limit", [
+    (100, 90, 1), (100, 90, 5), (1500, 61, 1), (1500, 61, 5), (9001, 4200, 24), (20011, 160, 1),
+    (20011, 160, 24), (70001, 21, 5), (131073, 9, 1), (131073, 9, 24)])
+def test_logprobs_many_rows_per_block(dl, kind, vocab, rows, limit, monkeypatch):
+    """Few blocks for many rows: runs of rows through the rings and the handovers, rows
+    left out at every place among them, masks that leave some empty."""
+    monkeypatch.setenv("DL_GRID_LIMIT", str(limit))
+    z = logits_of(rows, vocab, kind, limit)
+    z[torch.rand(rows, generator=gen(1), device="cuda") < 0.1] = -INF
+    z[torch.rand(rows, generator=gen(2), device="cuda") < 0.3, vocab // 2:] = -INF
+    tokens = tokens_of(rows, vocab, 3)
+    tokens[torch.rand(rows, generator=gen(4), device="cuda") < 0.4] = -1
+    for out in (tokens, torch.full_like(tokens, -1), torch.where(tokens < 0, tokens + 2, tokens)):
+        for top, entropy in ((0, False), (6, True)):
+            r = dl.logprobs_forward(z, out, top=top, entropy=entropy)
+            check_logprobs(r, z, out, top, entropy)
+    check_backward(dl, z, out, r, kind, 5, 6, True)
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 def test_logprobs_offset(dl, kind):
     """Logits on a common offset lose nothing: the statistics keep the maximum
