@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include "dl_norm.cuh"
+#include "dl_rotary_form.h"
 
 namespace dl {
 namespace {
@@ -45,27 +46,6 @@ __device__ __forceinline__ uint64_t position_of(const RotaryArgs& a, int64_t bat
     return static_cast<uint64_t>(a.position_type == DL_I64 ? static_cast<const int64_t*>(a.positions)[at]
                                                            : static_cast<const int32_t*>(a.positions)[at]);
 }
-
-// A unit of a head: what one thread turns or copies at once. Packs of
-// neighbouring pairs lie at multiples of N from the head's start, the last
-// turned one perhaps with elements behind the rotated part; units of two packs
-// hold nothing but pairs, or nothing but elements behind them.
-template <int N, bool INTERLEAVED>
-struct Form {
-    static constexpr bool kTwo = !INTERLEAVED || N == 1;  // two packs, else one
-    static constexpr int kSize = kTwo ? 2 * N : N, kPairs = kSize / 2;
-    static constexpr int kStep = INTERLEAVED ? kSize : N;  // from a turned unit's first pack to the next one's
-    static __host__ __device__ int turned(int pairs) { return (pairs + kPairs - 1) / kPairs; }
-    // elements of a head behind the rotated part's units
-    static __host__ __device__ int rest(int head_dim, int pairs) { return head_dim - turned(pairs) * kSize; }
-    static __host__ __device__ int units(int head_dim, int pairs) {
-        return turned(pairs) + (rest(head_dim, pairs) / N * N + kSize - 1) / kSize;
-    }
-    // whether packs of N suit these sizes
-    static bool fits(int head_dim, int pairs) {
-        return kTwo ? pairs % N == 0 || N == 1 : rest(head_dim, pairs) >= 0;
-    }
-};
 
 // Two pairs turned: a product and a fused product each, in this order in every
 // form of the kernel, so that they all give the same bits.
@@ -140,8 +120,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_rotary(const __grid_constant__ 
     using P = Pack<T, N>;
     using F = Form<N, INTERLEAVED>;
     constexpr int kPairs = F::kPairs, kRows = 4;  // heads at a time
-    constexpr bool kTwo = F::kTwo;
-    const int turned = F::turned(a.pairs), units = F::units(a.head_dim, a.pairs), behind = turned * F::kSize;
+    const int turned = F::turned(a.pairs), units = F::units(a.head_dim, a.pairs);
     const int wide = min(units, kThreads);
     const int slot = threadIdx.x / wide, local = slot / a.lanes, head = slot - local * a.lanes;
     const int token0 = threadIdx.x / a.pairs, pair0 = threadIdx.x - token0 * a.pairs;
@@ -167,27 +146,27 @@ __global__ void __launch_bounds__(kThreads, 3) k_rotary(const __grid_constant__ 
 #pragma unroll
             for (int i = 0; i < kPairs; ++i)
                 cs[i] = i < pairs ? table[l * a.pairs + u * kPairs + i] : make_float2(0.f, 0.f);
-            const int low = turns ? u * F::kStep : behind + (u - turned) * F::kSize;
+            const int low = F::first(u, turned);
             const int apart = turns && !INTERLEAVED ? a.pairs : N;  // between a unit's two packs
-            const bool two = kTwo && (turns || low + 2 * N <= a.head_dim);
+            const bool two = F::two(turns, low, a.head_dim);
             for (int j = 0; j < a.n_jobs; ++j) {
                 const dl_rotary_job& job = a.job[j];
                 if (!turns && job.x == job.y) continue;  // in place: nothing to copy
                 const T* x = static_cast<const T*>(job.x) + batch * job.x_batch + (begin + l) * job.x_token + low;
                 T* y = static_cast<T*>(job.y) + batch * job.y_batch + (begin + l) * job.y_token + low;
-                for (int h = head; h < job.heads; h += kRows * a.lanes) {
+                for (HeadWalk<kRows> h(head, a.lanes, job.heads); h.more(); h.next()) {
                     P v[kRows], w[kRows];
 #pragma unroll
                     for (int r = 0; r < kRows; ++r)
-                        if (h + r * a.lanes < job.heads) {
-                            const T* from = x + (h + r * a.lanes) * job.x_head;
+                        if (h.has(r)) {
+                            const T* from = x + h.row(r) * job.x_head;
                             v[r] = *reinterpret_cast<const P*>(from);
                             if (two) w[r] = *reinterpret_cast<const P*>(from + apart);
                         }
 #pragma unroll
                     for (int r = 0; r < kRows; ++r)
-                        if (h + r * a.lanes < job.heads) {
-                            T* to = y + (h + r * a.lanes) * job.y_head;
+                        if (h.has(r)) {
+                            T* to = y + h.row(r) * job.y_head;
                             if (turns) turn_unit<T, N, INTERLEAVED>(v[r], w[r], cs, pairs);
                             *reinterpret_cast<P*>(to) = v[r];
                             if (two) *reinterpret_cast<P*>(to + apart) = w[r];
