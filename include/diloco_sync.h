@@ -659,6 +659,7 @@ int dl_rotary_apply(const dl_rotary_job* jobs, int32_t n_jobs, int32_t type, int
  *   entropy = ln S - sum e^(z - m) (z - m) / S        (a term of z = -inf is 0)
  *   top     the n_top most probable tokens, most probable first, the lower
  *           token first where logits are equal, and their logp
+ * logp and top's are at most 0, ln S and entropy at least 0, as rounded too.
  * Sums in fp32, in a fixed order.
  *   logits    device [rows][vocab] of type (DL_F32, DL_BF16 or DL_F16); row r
  *             starts at r * stride elements, stride >= vocab

@@ -69,7 +69,8 @@ __device__ __forceinline__ float largest(const Pack<T, N> (&p)[U]) {
 // x * log2(e) + c with c = -m * log2(e) as rounded: all are off by the same
 // `off`, which the fused m * log2(e) + c gives exactly and the sums are
 // corrected by (16384 x 32000 bf16 with entropy and 5 alternatives 213 us,
-// 224 without). Not for maxima so large that it is no small number.
+// 224 without). The largest term is then the product of two approximate powers,
+// 1 to about 2^-21 only. Not for maxima so large that it is no small number.
 template <bool ENTROPY, typename T, int N, int U>
 __device__ __forceinline__ void add_packs(Part& part, const Pack<T, N> (&p)[U], float top) {
     part.raise(max_nan(part.m, top));
@@ -439,11 +440,14 @@ __global__ void __launch_bounds__(Geometry<T, TPR, U>::kBlock, TPR == 32 ? 6 : T
         }
         // nothing but -inf: no sum; NaN or +inf: a sum of NaN
         const bool empty = part.s == 0.f, bad = !(part.s >= 0.f);
-        const float m = bad ? NAN : empty ? 0.f : part.m, log_sum = logf(part.s);
+        // the largest term is 1, up to what the powers and their correction round: no
+        // probability is above 1, and no entropy below 0
+        const float s = empty ? 0.f : max_nan(part.s, 1.f);
+        const float m = bad ? NAN : empty ? 0.f : part.m, log_sum = logf(s);
         if (lane == 0) {
             if (a.tokens) a.logp[row] = empty && token < a.vocab ? -INFINITY : (z - m) - log_sum;
             if (a.lse) a.lse[row] = m + log_sum;
-            if (a.entropy) a.entropy[row] = empty ? 0.f : log_sum - part.a / part.s * kLn2;
+            if (a.entropy) a.entropy[row] = empty ? 0.f : max_nan(log_sum - part.a / s * kLn2, 0.f);
             if (a.row_max) a.row_max[row] = m, a.log_sum[row] = log_sum;
         }
         if (TOP && lane < a.n_top) {

@@ -46,3 +46,41 @@ def test_rotary_widest_head(dl):
     assert torch.equal(room[:16], dl.rotary_apply(x[:16].view(1, 1, 16), F, first=3).view(16))
     assert torch.equal(room[16:width], x[16:width])
     assert bool((room[width:] == 7).all())
+
+
+# ----------------------------------------------------------------------------
+# token log probabilities
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,vocab", [(600, 40), (600, 1000), (300, 2048), (4096, 5000), (40, 20001), (300, 20001),
+                                        (600, 32000)])
+def test_logprobs_certain_tokens(dl, kind, rows, vocab):
+    """One token has all of a row's probability: its log probability is at most 0
+    (so 1 - exp of it is no negative number) and the entropy at least 0, whatever the
+    logit; masks and logits far below beside it."""
+    at = base.tokens_of(rows, vocab, 1)
+    top_logit = (torch.rand(rows, generator=gen(2), device="cuda") * 2 - 1) * 60
+    top_logit[::7] *= 100
+    top_logit = top_logit.to(TYPES[kind])
+    for below in (None, 30.0, 90.0):
+        z = torch.full((rows, vocab), -INF, dtype=TYPES[kind], device="cuda")
+        if below is not None:
+            z[:, :] = (top_logit - below)[:, None]
+        z[torch.arange(rows), at] = top_logit
+        # The others are at d below the row's token: `below` after the rounding to the type, which
+        # near 2^12 moves bf16 values by up to 16. Their terms sum to s = (vocab - 1) e^-d, so that
+        # -logp = ln S = ln(1 + s) <= s and entropy = ln S + s d / S <= s + s d; beside them the
+        # bounds of check_logprobs, with far <= s d and |ln S| <= s.
+        d = (top_logit.double() - z[torch.arange(rows), (at + 1) % vocab].double())
+        s = (vocab - 1) * torch.exp(-d)
+        far = torch.nan_to_num(s * d)
+        tol = s + far + base.sum_tol(far) * (1 + 2 * far) + 4 * base.U * (s + far)
+        for top, entropy in ((0, False), (0, True), (1, True), (4, False)):
+            r = dl.logprobs_forward(z, at, top=top, entropy=entropy)
+            values = [r.logp, -r.log_sum] + ([-r.entropy] if entropy else []) + ([r.top_logp[:, 0]] if top else [])
+            for v in values:
+                assert float(v.max()) <= 0.0
+                assert bool((v.double() >= -tol).all())
+            if top:
+                assert torch.equal(r.top_tokens[:, 0], at)
