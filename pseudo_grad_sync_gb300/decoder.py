@@ -207,6 +207,9 @@ def rotary_apply(xs, frequencies, positions=None, first=0, interleaved=False, in
         if ys is None:
             y = torch.empty_like(x)
             r = y.stride()
+            if r[-1] != 1:  # windows that overlap may come back in another order
+                y = torch.empty(x.shape, dtype=x.dtype, device=device)
+                r = y.stride()
             if len(r) == 3:
                 r = (0, *r)
         else:

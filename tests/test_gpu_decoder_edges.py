@@ -48,6 +48,22 @@ def test_rotary_widest_head(dl):
     assert bool((room[width:] == 7).all())
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotary_of_windows(dl, kind, interleaved):
+    """Inputs and gradients whose rows overlap give what copies of them do."""
+    v = randn((4000,), 1, kind)
+    F = dl.RotaryFrequencies(48)
+    for x in (v.unfold(0, 64, 1)[:8].unsqueeze(1), v.unfold(0, 64, 1)[:30].view(2, 15, 64).unsqueeze(2),
+              v.as_strided((2, 5, 3, 64), (1, 64, 1, 1)), v.as_strided((2, 5, 3, 64), (400, 32, 32, 1))):
+        want = dl.rotary_apply(x.contiguous(), F, first=9, interleaved=interleaved)
+        got = dl.rotary_apply(x, F, first=9, interleaved=interleaved)
+        assert got.stride(-1) == 1 and torch.equal(got, want)
+        leaf = x.contiguous().clone().requires_grad_()  # (a clone of windows may be laid out otherwise)
+        dx, = torch.autograd.grad(dl.rotary(leaf, F, first=9, interleaved=interleaved), leaf, x)
+        assert torch.equal(dx, dl.rotary_apply(x.contiguous(), F, first=9, interleaved=interleaved, inverse=True))
+
+
 # ----------------------------------------------------------------------------
 # token log probabilities
 
