@@ -228,7 +228,8 @@ int launch(BackwardArgs<T> a, cudaStream_t s) {
     if (a.rows > INT64_MAX / a.chunks) return DL_ERR_ARG;
     a.items = a.rows * a.chunks;
     const int64_t blocks = (a.items + kThreads / 32 - 1) / (kThreads / 32);
-    k_logprobs_bwd<T, TOP, SHIFT><<<static_cast<unsigned>(blocks < INT32_MAX ? blocks : INT32_MAX), kThreads, 0, s>>>(a);
+    const int64_t grid = limited(blocks < INT32_MAX ? blocks : INT32_MAX);
+    k_logprobs_bwd<T, TOP, SHIFT><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a);
     return launch_status();
 }
 

@@ -217,8 +217,8 @@ int launch(RotaryArgs a, cudaStream_t s) {
     a.tiles_per_batch = (a.tokens + a.tile - 1) / a.tile;
     a.tiles = a.tiles_per_batch * a.batch;
     const size_t bytes = size_t(a.tile) * a.pairs * sizeof(float2);
-    k_rotary<T, N, INTERLEAVED>
-        <<<static_cast<unsigned>(a.tiles < INT32_MAX ? a.tiles : INT32_MAX), kThreads, bytes, s>>>(a);
+    const int64_t grid = limited(a.tiles < INT32_MAX ? a.tiles : INT32_MAX);
+    k_rotary<T, N, INTERLEAVED><<<static_cast<unsigned>(grid), kThreads, bytes, s>>>(a);
     return launch_status();
 }
 

@@ -83,6 +83,16 @@ __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
     return floats2(r);
 }
 
+// no more blocks than DL_GRID_LIMIT (environment; tests use it to make single
+// blocks cover much)
+inline int64_t limited(int64_t blocks) {
+    if (const char* cap = getenv("DL_GRID_LIMIT")) {
+        const long v = strtol(cap, nullptr, 10);
+        if (v > 0 && v < blocks) return v;
+    }
+    return blocks;
+}
+
 // Launch geometry of one kernel with its threads and dynamic shared memory:
 // the blocks that fit the current device at once, asked for on the first call
 // per device and kept; 0 (and no error left behind for a later call) when the
@@ -111,14 +121,9 @@ public:
         }
         return b;
     }
-    // a persistent grid: no more blocks than work items, or than DL_GRID_LIMIT
-    // (environment; tests use it to make single blocks cover much)
+    // a persistent grid: no more blocks than work items
     int grid(const void* kernel, int threads, size_t smem, int64_t work_items) {
-        int64_t g = blocks(kernel, threads, smem);
-        if (const char* cap = getenv("DL_GRID_LIMIT")) {
-            const long v = strtol(cap, nullptr, 10);
-            if (v > 0 && v < g) g = v;
-        }
+        const int64_t g = limited(blocks(kernel, threads, smem));
         return static_cast<int>(work_items < g ? work_items : g);
     }
 

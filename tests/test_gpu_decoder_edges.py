@@ -64,6 +64,26 @@ def test_rotary_of_windows(dl, kind, interleaved):
         assert torch.equal(dx, dl.rotary_apply(x.contiguous(), F, first=9, interleaved=interleaved, inverse=True))
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("limit", ["1", "5"])
+def test_rotary_many_tiles_per_block(dl, kind, interleaved, limit, monkeypatch):
+    """Few blocks for many tiles, of several sequences too: the same bits as with a block for each."""
+    for batch, tokens, heads, width, dim in ((3, 700, 2, 64, 64), (5, 131, 40, 128, 96), (2, 99, 3, 75, 50),
+                                             (700, 1, 4, 64, 64), (1, 2000, 1, 8, 6), (2, 7, 2, 2060, 2048)):
+        F = dl.RotaryFrequencies(dim)
+        xs = randn((batch, tokens, heads, width), 1, kind), randn((batch, tokens, 1, width), 2, kind)
+        positions = torch.randint(0, 9999, (batch, tokens), generator=gen(3), device="cuda")
+        for p in (None, positions):
+            monkeypatch.delenv("DL_GRID_LIMIT", raising=False)
+            want = dl.rotary_apply(xs, F, p, interleaved=interleaved)
+            monkeypatch.setenv("DL_GRID_LIMIT", limit)
+            got = dl.rotary_apply(xs, F, p, interleaved=interleaved)
+            here = [x.clone() for x in xs]
+            dl.rotary_apply(here, F, p, interleaved=interleaved, out=here)
+            assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(want, got, here))
+
+
 # ----------------------------------------------------------------------------
 # token log probabilities
 
@@ -100,3 +120,31 @@ def test_logprobs_certain_tokens(dl, kind, rows, vocab):
                 assert bool((v.double() >= -tol).all())
             if top:
                 assert torch.equal(r.top_tokens[:, 0], at)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,vocab", [(61, 40), (61, 1000), (23, 5003), (5, 70001)])
+@pytest.mark.parametrize("limit", ["1", "5"])
+def test_logprobs_gradient_many_chunks_per_block(dl, kind, rows, vocab, limit, monkeypatch):
+    """Few blocks for many rows and chunks, rows left out and without gradients among
+    them, dlogits aligned as the logits and otherwise, and in place: the same bits as
+    with warps for all."""
+    z, tokens = logits_of(rows, vocab, kind, 1), base.tokens_of(rows, vocab, 2)
+    tokens[torch.rand(rows, generator=gen(3), device="cuda") < 0.3] = -1
+    r = dl.logprobs_forward(z, tokens, top=5, entropy=True)
+    g, h, q = randn((rows,), 4), randn((rows,), 5), randn((rows, 5), 6)
+    for d in (g, h, q):
+        d[::4] = 0
+    for args in (dict(d_logp=g), dict(d_logp=g, d_entropy=h, entropy=r.entropy, top_tokens=r.top_tokens, d_top=q)):
+        def dlogits(out):
+            return dl.logprobs_backward(z, tokens, r.row_max, r.log_sum, out=out, **args)
+        monkeypatch.delenv("DL_GRID_LIMIT", raising=False)
+        want = dlogits(torch.empty_like(z))
+        monkeypatch.setenv("DL_GRID_LIMIT", limit)
+        assert torch.equal(dlogits(torch.empty_like(z)), want)
+        room = torch.full((rows, vocab + 3), 9.0, dtype=z.dtype, device="cuda")
+        assert torch.equal(dlogits(room[:, 1:vocab + 1]), want)
+        assert bool((room[:, 0] == 9).all()) and bool((room[:, vocab + 1:] == 9).all())
+        here = z.clone()
+        dl.logprobs_backward(here, tokens, r.row_max, r.log_sum, out=here, **args)
+        assert torch.equal(here, want)
