@@ -261,11 +261,13 @@ class _Rotary(torch.autograd.Function):
     def backward(ctx, *dys):
         frequencies, first, interleaved, inverse = ctx.how
         positions, = ctx.saved_tensors
-        # outputs that nothing used have no gradient; a broadcast one may have any stride
-        given = [dy if dy.stride(-1) == 1 else dy.contiguous() for dy in dys if dy is not None]
+        # outputs that nothing used have no gradient, and some inputs need none
+        asked = [dy is not None and need for dy, need in zip(dys, ctx.needs_input_grad[5:])]
+        # a broadcast gradient may have any stride
+        given = [dy if dy.stride(-1) == 1 else dy.contiguous() for dy, ask in zip(dys, asked) if ask]
         dxs = iter(_Rotary.apply(frequencies, positions, first, interleaved, not inverse, *given)
                    if given else ())
-        return (None,) * 5 + tuple([None if dy is None else next(dxs) for dy in dys])
+        return (None,) * 5 + tuple([next(dxs) if ask else None for ask in asked])
 
 
 def rotary(xs, frequencies, positions=None, first=0, interleaved=False):

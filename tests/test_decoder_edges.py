@@ -74,3 +74,22 @@ def test_rotary_of_any_layout(formula, name):
     assert y.stride(-1) == 1 and torch.allclose(y.double(), want, rtol=0, atol=1e-6)
     flat = dl.rotary_apply(x[1], F, first=3)
     assert flat.stride(-1) == 1 and torch.allclose(flat.double(), want[1], rtol=0, atol=1e-6)
+
+
+def test_rotary_turns_back_what_is_asked_for(formula):
+    """Only gradients of inputs that need one are computed, in one call."""
+    F = dl.RotaryFrequencies(16, device="cpu")
+    q, k = (torch.randn(2, 5, h, 16, generator=torch.Generator().manual_seed(h)) for h in (3, 1))
+    for needs in ((True, True), (True, False), (False, True)):
+        xs = [x.clone().requires_grad_(need) for x, need in zip((q, k), needs)]
+        formula.calls.clear()
+        sum(y.sum() for y in dl.rotary(xs, F)).backward()
+        assert formula.calls == [(2, 0), (sum(needs), dl.DL_ROTARY_INVERSE)]
+        for x, need in zip(xs, needs):
+            want = dl.rotary_apply(torch.ones_like(x), F, inverse=True)
+            assert torch.equal(x.grad, want) if need else x.grad is None
+    w = torch.randn_like(q).requires_grad_()  # a derivative of the gradient
+    x = q.clone().requires_grad_()
+    dx, = torch.autograd.grad((dl.rotary((x, k), F)[0] * w).sum(), x, create_graph=True)
+    dw, = torch.autograd.grad(dx.sum(), w)
+    assert torch.equal(dw, dl.rotary_apply(torch.ones_like(q), F))
