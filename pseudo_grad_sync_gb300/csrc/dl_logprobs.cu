@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(Geometry<T, TPR, U>::kBlock, TPR == 32 ? 6 : T
     P* const ring = reinterpret_cast<P*>(smem) + threadIdx.x;
     auto slot = [&](int stage, int u) { return ring + (stage * U + u) * Geo::kMain; };
     const T none = from_f32<T>(-INFINITY);
-    // what is copied next: stage `next_k` of row `next`
+    // what is copied next: a stage of row `next`, which has next_stages to go
     int64_t next = row, next_token = token, next_after = token_of(row + step);
     auto skip = [&]() {  // to the first row that is not left out
         while (next < a.rows && next_token < 0) next += step, next_token = next_after, next_after = token_of(next + step);

@@ -68,9 +68,6 @@ struct RowPacks {
         }
         return r;
     }
-    __device__ __forceinline__ Pack<T, N> load(int p, uint32_t fill) const {
-        return whole(p) ? reinterpret_cast<const Pack<T, N>*>(base)[p] : edge(p, fill);
-    }
 };
 
 // the bits of -inf
