@@ -660,7 +660,10 @@ int dl_rotary_apply(const dl_rotary_job* jobs, int32_t n_jobs, int32_t type, int
  *   top     the n_top most probable tokens, most probable first, the lower
  *           token first where logits are equal, and their logp
  * logp and top's are at most 0, ln S and entropy at least 0, as rounded too.
- * Sums in fp32, in a fixed order.
+ * Sums in fp32, in an order that type, sizes, alignment, n_top and the GPU's
+ * number of SMs fix: the same call gives the same bits; the same row among a
+ * different number of rows, or with alternatives and without, may differ in the
+ * last ones. Terms below 2^-126 count as 0, in the gradient's probabilities too.
  *   logits    device [rows][vocab] of type (DL_F32, DL_BF16 or DL_F16); row r
  *             starts at r * stride elements, stride >= vocab
  *   tokens    device [rows] of token_type (DL_I32 or DL_I64), or NULL for no logp

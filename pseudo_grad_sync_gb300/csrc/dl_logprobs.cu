@@ -651,13 +651,19 @@ int launch(const ForwardArgs<T>& a, int ranks, cudaStream_t s) {
 
 // A warp per row while that leaves it less than 64 packs per lane and there
 // are rows for every warp (65536 x 4096 bf16 102 us, 331 with a block of eight
-// warps; in stages of four packs but for rows that fill less than a stage, and
-// with alternatives, whose shared memory leaves fewer blocks: 32768 x 8192 84 us,
-// in stages of two 93, but 262144 x 512 173 where those take 146; 16384 x 32000 166, with a block of four 157); few rows by clusters of
-// up to eight blocks of eight warps, while there are SMs for them and the
-// shares fill a block (64 x 128256: 8.0 us, with one block each 19); else a
-// block of four warps (eight: 16384 x 32000 185 us for 161 then, 8192 x 128256 291
-// for 297, with entropy and 20 alternatives 388 for 376).
+// warps; 16384 x 32000 166, with a block of four 157). Its stages are of four packs
+// per lane for rows of more than 96 packs without alternatives (32768 x 8192 84 us,
+// in stages of two 93), of two for shorter rows (262144 x 512 146 us, in stages of
+// four 173) and with alternatives, whose shared memory leaves fewer blocks. So
+// the order of a row's sums goes by n_top too.
+//
+// Few rows by clusters of up to eight blocks of eight warps, while there are SMs
+// for them and the shares fill a block (64 x 128256: 8.0 us, with one block each 19);
+// else a block of four warps (eight: 16384 x 32000 185 us for 161 then, 8192 x 128256
+// 291 for 297, with entropy and 20 alternatives 388 for 376, 600 x 128256 30 for 27).
+// That one rule also takes the rows that do not fill the SMs, where eight warps
+// were faster: 300 x 128256 15.3 us for 17.9, with 8 alternatives 21 for 25,
+// 300 x 32000 7.1 for 7.5.
 template <typename T>
 int forward(const ForwardArgs<T>& a, cudaStream_t s) {
     constexpr int N = 16 / sizeof(T);

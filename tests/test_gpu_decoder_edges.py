@@ -148,3 +148,73 @@ def test_logprobs_gradient_many_chunks_per_block(dl, kind, rows, vocab, limit, m
         here = z.clone()
         dl.logprobs_backward(here, tokens, r.row_max, r.log_sum, out=here, **args)
         assert torch.equal(here, want)
+
+
+def forms(packs, narrow):
+    """(rows of a call, blocks or a warp per row, threads per row) of every form of the kernel that rows of
+    that many packs of 16 bytes are computed by."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    if packs <= 256:
+        return [(300, 1, 32)]
+    out = [(3 * sms // ranks, ranks, 256) for ranks in (2, 4, 8) if packs // ranks >= 256]
+    out.append((3 * sms // 2 + 1, 1, 128))
+    return out + [(4096, 1, 32)] if narrow else out
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("off", [0, 3])
+@pytest.mark.parametrize("vocab", [700, 2040, 5003, 20011, 131077])
+def test_logprobs_counts_every_border_once(dl, kind, off, vocab):
+    """Rows with a single finite column, at every border between threads, stages and
+    blocks that share a row: a sum of 1, which twice that column would make 2 and
+    without it nothing; the gradient likewise."""
+    n = 16 // TYPES[kind].itemsize
+    stride = (vocab + 3 + n - 1) // n * n  # every row as the first one on its 16-byte boundary
+    packs = (vocab + off % n + n - 1) // n
+    for rows, ranks, threads in forms(packs, vocab < 6000):
+        each = -(-packs // ranks)
+        starts = {b for r in range(ranks) for b in range(r * each, min(r * each + each, packs), threads)}
+        columns = {p * n - off % n + d for p in starts for d in (-1, 0, n - 1)} | {0, vocab // 3, vocab - 1}
+        columns = torch.tensor(sorted(c for c in columns if 0 <= c < vocab), device="cuda")
+        room = torch.empty((rows, stride), dtype=TYPES[kind], device="cuda")
+        for first in range(0, len(columns), rows):
+            at = columns[first:first + rows]
+            at = torch.cat([at, at[-1:].expand(rows - len(at))])  # the form goes by the number of rows
+            room.fill_(math.nan)
+            z = room[:, off:off + vocab]
+            z.fill_(-INF)
+            z[torch.arange(rows), at] = 1.5
+            zero = torch.zeros(rows, device="cuda")
+            for top, entropy in ((0, False), (3, True)):
+                r = dl.logprobs_forward(z, at, top=top, entropy=entropy)
+                assert bool((r.row_max == 1.5).all())
+                near(r.logp, zero, base.SUM_TOL, "logp")
+                near(r.log_sum, zero, base.SUM_TOL, "log_sum")
+                if top:
+                    near(r.entropy, zero, base.SUM_TOL, "entropy")
+                    assert torch.equal(r.top_tokens[:, 0], at) and bool((r.top_tokens[:, 1:] == -1).all())
+            other, g = (at + 1) % vocab, randn((rows,), 1)
+            dz = dl.logprobs_backward(z, other, r.row_max, r.log_sum, g)
+            # e^0 / S: the bound of S, and of 1 / S
+            near(dz[torch.arange(rows), at], -g, (base.SUM_TOL + 4 * base.U + base.UT[kind]) * g.abs().double(), "dz")
+            assert torch.equal(dz[torch.arange(rows), other], g.to(dz.dtype))
+            assert bool((torch.count_nonzero(dz, 1) == 2).all())
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+def test_logprobs_with_and_without_alternatives(dl, kind):
+    """The order of a row's sums goes by what else a call asks for and by its number
+    of rows: each result is within the bound of the others."""
+    n = 16 // TYPES[kind].itemsize
+    for packs in (95, 96, 97, 112, 127, 128, 129, 200, 255, 256, 257, 600):
+        vocab = packs * n
+        z, tokens = logits_of(4100, vocab, kind, packs), base.tokens_of(4100, vocab, 2)
+        want = dl.logprobs_forward(z[:40], tokens[:40])
+        far = base.ref.logprobs(z[:40], None)["far"]
+        for rows in (40, 300, 4100):
+            for top, entropy in ((0, False), (0, True), (1, False), (9, True)):
+                r = dl.logprobs_forward(z[:rows], tokens[:rows], top=top, entropy=entropy)
+                assert torch.equal(r.row_max[:40], want.row_max)
+                tol = 2 * (base.sum_tol(far) + 8 * base.U * (want.lse.abs() + want.logp.abs()).double())
+                near(r.logp[:40], want.logp, tol, (packs, rows, top, entropy))
+                near(r.lse[:40], want.lse, tol, (packs, rows, top, entropy))
