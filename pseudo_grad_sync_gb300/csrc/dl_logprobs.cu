@@ -371,12 +371,16 @@ __device__ __forceinline__ uint64_t alternatives(const S& mine, const float (&mo
 // are at the next row; one barrier per row hands over (without that warp, the
 // alternatives found by all: 535 us where this takes 359).
 //
-// Bound by HBM without alternatives: 8192 x 128256 bf16 289 us (107% of the copy
-// rate, which also writes), with entropy 313 (99%); 16384 x 32000 157 (99%);
-// 8192 x 32000 fp32 with entropy and 5 alternatives 157 (99%). With alternatives
-// in 16 bits by instruction issue beside HBM: 8192 x 128256 with entropy and 20
-// of them 359 us (87%), 16384 x 32000 with 5 213 (73%). Few rows: 3 x 128256
-// with 8 alternatives 9.2 us, without 4.9; 512 x 512 2.8 us.
+// Without alternatives near what HBM gives (80% of its peak in the counters): 8192 x
+// 128256 bf16 293 us (105% of the rate of a copy, half of whose bytes are writes),
+// with entropy 315 (98%); 16384 x 32000 158 (98%); 8192 x 32000 fp32 with entropy and
+// 5 alternatives 157 (98%). With alternatives in 16 bits by instruction issue beside
+// HBM: 8192 x 128256 with entropy and 20 of them 359 us (86%), 16384 x 32000 with 5
+// 212 (73%). fp16 takes longer (297, 337, 408 and 239 us for these), most where its
+// forms with entropy spill up to 64 bytes at the registers of five blocks per SM.
+// Few rows: 3 x 128256 with 8 alternatives 9.0 us, 1 x 128256 without 4.6; 512 x 512
+// 2.8 us. All logits equal, with 20 alternatives: 8192 x 128256 657 us, 16384 x 32000
+// 637; rising ones 373 and 302.
 template <typename T, int TPR, int U, bool ENTROPY, bool TOP, bool CLUSTER>
 __global__ void __launch_bounds__(Geometry<T, TPR, U>::kBlock, TPR == 32 ? 6 : TPR == 128 ? 5 : 3)
     k_logprobs(const __grid_constant__ ForwardArgs<T> a) {

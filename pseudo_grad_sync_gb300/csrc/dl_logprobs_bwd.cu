@@ -68,9 +68,10 @@ __device__ __forceinline__ Pack<T, N> shifted(const Pack<T, N>& p, const Pack<T,
 // computes that value aside and stores it after the chunk's packs.
 //
 // Bound by HBM: each logit is read once and written once. 8192 x 128256 bf16 with
-// entropy 618 us (101% of the copy rate), without 597; 16384 x 32000 308 (101%);
-// 8192 x 32000 fp32 with entropy and 5 alternatives 311 (100%). Shifted: 8192 x 32003
-// fp32 with both 341 us (91%), bf16 173 (90%; element by element 491). Chunks of a
+// entropy 617 us (100% of the copy rate), without 597; 16384 x 32000 308 (100%);
+// 8192 x 32000 fp32 with entropy and 5 alternatives 310 (100%). Shifted: 8192 x 32003
+// fp32 with both 341 us (91%), bf16 173 (89%; element by element 491). The shifted
+// forms and the aligned ones with alternatives spill 20 to 64 bytes. Chunks of a
 // warp need no barrier (a block's chunk with its token's column patched by the
 // thread that owns it: 635 us, and 3983 us instead of 155 for 262144 x 512). Eight
 // packs per lane (four: 753 us), blocks of 128 threads (256: 636); the edges go

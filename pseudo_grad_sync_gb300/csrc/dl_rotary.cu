@@ -107,13 +107,14 @@ __device__ __forceinline__ void turn_unit(Pack<T, N>& v, Pack<T, N>& w, const fl
 //
 // Bound by HBM (reads and writes mixed, 78% of its peak in the counters): 4 x 8192
 // tokens of 32 + 8 heads of 128 bf16 106 us (93% of the copy rate), half of each
-// head rotated 111, 4 x 4096 in fp32 103 (96%), interleaved 111. With the cosines
+// head rotated 110, 4 x 4096 in fp32 103 (96%), interleaved 111. With the cosines
 // read from shared memory for every head and an integer division per row it was
 // 218 us; one head at a time per thread 118. The next heads' loads ahead of the
 // cosines gained nothing on single tokens and cost the batch 8 us. Single tokens
 // (5 x 36 heads of 64): 3.4 us. What is left: heads few or narrow (one query and
 // one key head of 128: 23%), whose tokens share a cosine among two heads only, and
-// packs below 16 bytes (heads of 75: 37-41%).
+// packs below 16 bytes (heads of 75: 39-42%). The half layout in 16-bit packs of
+// eight spills 20 bytes at the 80 registers that three blocks per SM leave.
 template <typename T, int N, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads, 3) k_rotary(const __grid_constant__ RotaryArgs a) {
     extern __shared__ __align__(16) float2 table[];

@@ -171,7 +171,8 @@ def rotary_apply(xs, frequencies, positions=None, first=0, interleaved=False, in
     the others copied. positions: int32 or int64, [batch, tokens] or [tokens];
     without them token s of every sequence is at first + s. inverse: by the
     negative angle (the gradient). out: where to write (xs themselves for in
-    place). Returns a tensor for a tensor, a tuple for a sequence."""
+    place). Returns a tensor for a tensor, a tuple for a sequence. Autograd
+    records neither the call nor what it writes into out; rotary is for that."""
     single = isinstance(xs, torch.Tensor)
     xs = (xs,) if single else tuple(xs)
     if not 1 <= len(xs) <= DL_ROTARY_MAX_JOBS:
@@ -398,7 +399,8 @@ def logprobs_backward(logits, tokens, row_max, log_sum, d_logp=None, d_entropy=N
     logprobs_forward and the gradients of its outputs, contiguous float32, any
     of them None. entropy: the forward call's, with d_entropy. top_tokens:
     the forward call's, with d_top. out: where to write, logits themselves for
-    in place. A row whose gradients are all zero gets zeros and is not read."""
+    in place (unseen by autograd). A row whose gradients are all zero gets zeros
+    and is not read."""
     zp, zs = _rows(logits, "logits")
     device = logits.device
     if stream is not None:
